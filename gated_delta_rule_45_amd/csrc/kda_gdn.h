@@ -1,0 +1,59 @@
+// Gated delta rule with one log-gate per token and value head: declarations shared by the host
+// dispatch and the kernel files.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda.h"
+
+namespace kda {
+namespace gdn {
+
+// Tokens per chunk.  bf16: 64, so that the products over a chunk's tokens fill the matrix instruction's
+// 32-wide contraction twice; fp32: 32, what three staged chunks of 4-byte K and Q leave of the LDS.
+constexpr int kChunkBf16 = 64, kChunkF32 = 32;
+inline int chunk_of(int32_t io) { return io == KDA_BF16 ? kChunkBf16 : kChunkF32; }
+
+// First chunk slot of packed sequence n that starts at token `start`: sum_m<n ceil(len_m / C) is at
+// most start / C + n, so these bases leave room for every sequence and need no prefix sum.
+__host__ __device__ inline int64_t slot_base(int64_t start, int64_t n, int C) { return start / C + n; }
+
+struct GdnParams {
+    const void *q, *k;        // [tokens, Hk, d_k], ldq / ldk elements between tokens
+    const void *v;            // [tokens, Hv, dv], ldv elements between tokens (reverse scan: d_out)
+    const void *g, *beta;     // [tokens, Hv] fp32, or bf16 with gate_bf16
+    const void *s0;           // [num_seqs, Hv, d_k, dv] state the walk starts from, or null (zero)
+    void *sf;                 // the state it ends with, or null
+    const int32_t *cu;        // [num_seqs + 1], or null: sequence n is tokens [n T, (n + 1) T)
+    void *out;                // [tokens, Hv, dv] dense: o (forward) or dV (reverse)
+    void *hs = nullptr;       // [slots, Hv, dv, d_k] operand type: the state entering each chunk (keeping
+                              // forward) or the gradient of the state leaving it (reverse)
+    void *zs = nullptr;       // [tokens, Hv, dv] operand type: Z (keeping forward)
+    int64_t ldq, ldk, ldv;
+    int32_t num_seqs, T, Hk, Hv, dk, dv;
+    int32_t gate_bf16, state_bf16;
+    float scale;
+};
+
+// Walks every sequence's chunks.  mode: 0 forward, 1 forward that keeps states and Z (no output), 2 reverse.
+// cols: state columns per workgroup, 32 or 64.
+hipError_t launch_scan_bf16(int mode, int cols, const GdnParams &p, hipStream_t stream);
+hipError_t launch_scan_f32(int mode, int cols, const GdnParams &p, hipStream_t stream);
+
+struct DecodeParams {
+    const void *q, *k, *v;    // as above
+    const void *g, *beta;
+    void *state;              // [num_slots, Hv, d_k, dv] fp32 or bf16, read and written
+    const int32_t *slots;     // [num_seqs] slot of each sequence, or null (sequence n has slot n)
+    const int32_t *cu;
+    void *out;
+    int64_t ldq, ldk, ldv, num_slots;
+    int32_t num_seqs, T, Hk, Hv, dk, dv;
+    int32_t gate_bf16, state_bf16;
+    float scale;
+};
+hipError_t launch_decode(bool io_bf16, const DecodeParams &p, hipStream_t stream);
+
+}  // namespace gdn
+}  // namespace kda

@@ -1,0 +1,328 @@
+// Host side of the scalar-gate delta rule: argument checks, launch choices and the C ABI.  As for the other
+// entry points everything is checked before HIP is touched, so an invalid call returns a status
+// without launching anything (and works on machines without a GPU).
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "kda.h"
+#include "kda_gdn.h"
+#include "kda_internal.h"
+
+namespace {
+
+using kda::set_error;
+
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool dtype_ok(int32_t t) { return t == KDA_F32 || t == KDA_BF16; }
+int64_t bytes_of(int32_t t) { return t == KDA_BF16 ? 2 : 4; }
+
+kda_status_t done(hipError_t e, const char *what) {
+    if (e != hipSuccess) return set_error(KDA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+    set_error(KDA_OK, "%s", "");
+    return KDA_OK;
+}
+
+// A problem that has passed the checks, with its sizes worked out.
+struct Shape {
+    int64_t tokens = 0, ldq = 0, ldk = 0, ldv = 0;
+    int32_t num_seqs = 0;
+    int64_t io = 2, gate = 4, state = 4;      // bytes of an element
+    int64_t qk_row = 0, v_row = 0, states = 0;  // elements: a token's rows, all sequences' states
+    // bytes from the first to the last element of a strided tensor of `tokens` rows
+    int64_t span(int64_t ld, int64_t row) const { return tokens > 0 ? ((tokens - 1) * ld + row) * io : 0; }
+};
+
+kda_status_t check_shape(const kda_gdn_problem_t *p, bool packed, Shape &s) {
+    if (!p) return set_error(KDA_ERR_INVALID_ARGUMENT, "problem is NULL");
+    if (p->batch < 0 || p->seq_len < 0 || p->num_heads_k < 1 || p->num_heads_v < 1)
+        return set_error(KDA_ERR_INVALID_ARGUMENT, "bad sizes: batch=%d seq_len=%d num_heads_k=%d num_heads_v=%d",
+                         p->batch, p->seq_len, p->num_heads_k, p->num_heads_v);
+    if (p->num_heads_v % p->num_heads_k != 0)
+        return set_error(KDA_ERR_INVALID_ARGUMENT, "num_heads_v %d is not a multiple of num_heads_k %d", p->num_heads_v,
+                         p->num_heads_k);
+    if (!dtype_ok(p->io_dtype) || !dtype_ok(p->gate_dtype) || !dtype_ok(p->state_dtype))
+        return set_error(KDA_ERR_INVALID_ARGUMENT, "io_dtype %d, gate_dtype %d, state_dtype %d: each is KDA_F32 or KDA_BF16",
+                         (int)p->io_dtype, (int)p->gate_dtype, (int)p->state_dtype);
+    for (int d : {p->head_dim_k, p->head_dim_v})
+        if (d != 64 && d != 128)
+            return set_error(KDA_ERR_UNSUPPORTED, "head dims d_k=%d d_v=%d: supported are 64 and 128", p->head_dim_k,
+                             p->head_dim_v);
+    if (!std::isfinite(p->scale)) return set_error(KDA_ERR_INVALID_ARGUMENT, "scale is not finite");
+    if (packed) {
+        if (p->batch != 1) return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens needs batch == 1 (got %d)", p->batch);
+        if (p->num_seqs < 0) return set_error(KDA_ERR_INVALID_ARGUMENT, "num_seqs %d < 0", p->num_seqs);
+    }
+    s.num_seqs = packed ? p->num_seqs : p->batch;
+    s.tokens = packed ? p->seq_len : (int64_t)p->batch * p->seq_len;
+    s.io = bytes_of(p->io_dtype);
+    s.gate = bytes_of(p->gate_dtype);
+    s.state = bytes_of(p->state_dtype);
+    s.qk_row = (int64_t)p->num_heads_k * p->head_dim_k;
+    s.v_row = (int64_t)p->num_heads_v * p->head_dim_v;
+    const int64_t given[] = {p->stride_q, p->stride_k, p->stride_v};
+    const int64_t rows[] = {s.qk_row, s.qk_row, s.v_row};
+    int64_t *ld[] = {&s.ldq, &s.ldk, &s.ldv};
+    for (int i = 0; i < 3; ++i) {
+        *ld[i] = given[i] ? given[i] : rows[i];
+        if (*ld[i] < rows[i])
+            return set_error(KDA_ERR_INVALID_ARGUMENT, "stride_%c %lld is smaller than a token's %lld elements", "qkv"[i],
+                             (long long)*ld[i], (long long)rows[i]);
+        if (*ld[i] * s.io % 16 != 0)
+            return set_error(KDA_ERR_INVALID_ARGUMENT, "stride_%c %lld is not a multiple of 16 bytes", "qkv"[i],
+                             (long long)*ld[i]);
+        if (s.tokens > 0 && *ld[i] > (1LL << 60) / s.tokens) return set_error(KDA_ERR_UNSUPPORTED, "tensor too large");
+    }
+    // workgroups, and elements of a chunk's states, stay in range
+    if ((int64_t)s.num_seqs * p->num_heads_v > 0x7fffffffLL / 4)
+        return set_error(KDA_ERR_UNSUPPORTED, "too many (sequence, head) pairs");
+    s.states = (int64_t)s.num_seqs * p->num_heads_v * p->head_dim_k * p->head_dim_v;
+    return KDA_OK;
+}
+
+// One tensor argument of a call.
+struct Arg {
+    const char *name;
+    const void *p;
+    int64_t bytes;
+    size_t align;
+    bool needed, written;
+};
+
+// Pointers: given, aligned, and no written range meets another one (`twin`: the pair of arguments
+// that may be the same buffer).
+template <int N>
+kda_status_t check_args(const Arg (&a)[N], int twin0 = -1, int twin1 = -1) {
+    for (const Arg &x : a) {
+        if (!x.p && x.needed && x.bytes > 0) return set_error(KDA_ERR_INVALID_ARGUMENT, "%s is NULL", x.name);
+        if (x.p && !aligned(x.p, x.align))
+            return set_error(KDA_ERR_INVALID_ARGUMENT, "%s is not %zu-byte aligned", x.name, x.align);
+    }
+    for (int i = 0; i < N; ++i) {
+        if (!a[i].written || !a[i].p || a[i].bytes <= 0) continue;
+        const uintptr_t b = reinterpret_cast<uintptr_t>(a[i].p), e = b + (uintptr_t)a[i].bytes;
+        for (int j = 0; j < N; ++j) {
+            if (j == i || !a[j].p || a[j].bytes <= 0) continue;
+            const uintptr_t c = reinterpret_cast<uintptr_t>(a[j].p), f = c + (uintptr_t)a[j].bytes;
+            if (b == c && ((i == twin0 && j == twin1) || (i == twin1 && j == twin0))) continue;
+            if (b < f && c < e) return set_error(KDA_ERR_INVALID_ARGUMENT, "%s aliases %s", a[i].name, a[j].name);
+        }
+    }
+    return KDA_OK;
+}
+
+kda_status_t check_offsets(const kda_gdn_problem_t *p, const Shape &s, const int32_t *cu, const int32_t *host) {
+    if (!cu) {
+        if (host) return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens_host given without cu_seqlens");
+        return KDA_OK;
+    }
+    if (!aligned(cu, 4)) return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens is not 4-byte aligned");
+    if (!host) return KDA_OK;
+    if (host[0] != 0) return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens[0] = %d, expected 0", host[0]);
+    for (int32_t i = 0; i < s.num_seqs; ++i)
+        if (host[i + 1] < host[i])
+            return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens decreases at %d (%d -> %d)", i, host[i], host[i + 1]);
+    if (host[s.num_seqs] != p->seq_len)
+        return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens[%d] = %d, expected seq_len %d", s.num_seqs,
+                         host[s.num_seqs], p->seq_len);
+    return KDA_OK;
+}
+
+// State columns per workgroup: 64 where that still gives every CU a workgroup (K and Q of a chunk are
+// then staged half as often), else 32.
+int scan_cols(const kda_gdn_problem_t *p, const Shape &s, int cus) {
+    return (int64_t)s.num_seqs * p->num_heads_v * (p->head_dim_v / 64) >= cus ? 64 : 32;
+}
+
+int current_cus() {
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
+        return 256;
+    return n;
+}
+
+kda::gdn::GdnParams params_of(const kda_gdn_problem_t *p, const Shape &s, const void *q, const void *k, const void *v,
+                              const void *g, const void *beta, const int32_t *cu) {
+    kda::gdn::GdnParams r{};
+    r.q = q;
+    r.k = k;
+    r.v = v;
+    r.g = g;
+    r.beta = beta;
+    r.cu = cu;
+    r.ldq = s.ldq;
+    r.ldk = s.ldk;
+    r.ldv = s.ldv;
+    r.num_seqs = s.num_seqs;
+    r.T = p->seq_len;
+    r.Hk = p->num_heads_k;
+    r.Hv = p->num_heads_v;
+    r.dk = p->head_dim_k;
+    r.dv = p->head_dim_v;
+    r.gate_bf16 = p->gate_dtype == KDA_BF16;
+    r.state_bf16 = p->state_dtype == KDA_BF16;
+    r.scale = p->scale;
+    return r;
+}
+
+hipError_t launch_scan(const kda_gdn_problem_t *p, int mode, int cols, const kda::gdn::GdnParams &r, hipStream_t s) {
+    return p->io_dtype == KDA_BF16 ? kda::gdn::launch_scan_bf16(mode, cols, r, s) : kda::gdn::launch_scan_f32(mode, cols, r, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,
+                               const void *g, const void *beta, const void *initial_state, const int32_t *cu_seqlens,
+                               const int32_t *cu_seqlens_host, void *out, void *final_state, void *stream) {
+    try {
+        Shape s;
+        kda_status_t st = check_shape(problem, cu_seqlens != nullptr, s);
+        if (st != KDA_OK) return st;
+        const int64_t gates = s.tokens * problem->num_heads_v * s.gate;
+        const Arg args[] = {
+            {"q", q, s.span(s.ldq, s.qk_row), 16, true, false},
+            {"k", k, s.span(s.ldk, s.qk_row), 16, true, false},
+            {"v", v, s.span(s.ldv, s.v_row), 16, true, false},
+            {"g", g, gates, (size_t)s.gate, true, false},
+            {"beta", beta, gates, (size_t)s.gate, true, false},
+            {"initial_state", initial_state, s.states * s.state, 16, false, false},
+            {"final_state", final_state, s.states * s.state, 16, false, true},
+            {"out", out, s.tokens * s.v_row * s.io, 16, true, true},
+            {"cu_seqlens", cu_seqlens, ((int64_t)s.num_seqs + 1) * 4, 4, false, false},
+        };
+        st = check_args(args, 5, 6);
+        if (st == KDA_OK) st = check_offsets(problem, s, cu_seqlens, cu_seqlens_host);
+        if (st != KDA_OK) return st;
+        kda::gdn::GdnParams r = params_of(problem, s, q, k, v, g, beta, cu_seqlens);
+        r.s0 = initial_state;
+        r.sf = final_state;
+        r.out = out;
+        if (s.num_seqs == 0 || (s.tokens == 0 && !final_state)) return done(hipSuccess, "");
+        return done(launch_scan(problem, 0, scan_cols(problem, s, current_cus()), r, static_cast<hipStream_t>(stream)),
+                    "kda_gdn_chunk_fwd launch");
+    } catch (...) {
+        return KDA_ERR_HIP;
+    }
+}
+
+kda_status_t kda_gdn_decode(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,
+                            const void *g, const void *beta, void *state, int64_t num_slots, const int32_t *state_slots,
+                            const int32_t *state_slots_host, const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                            void *out, void *stream) {
+    try {
+        Shape s;
+        kda_status_t st = check_shape(problem, cu_seqlens != nullptr, s);
+        if (st != KDA_OK) return st;
+        if (num_slots < 0 || num_slots > 0x7fffffffLL)
+            return set_error(KDA_ERR_INVALID_ARGUMENT, "num_slots %lld out of range", (long long)num_slots);
+        if (!state_slots && num_slots < s.num_seqs)
+            return set_error(KDA_ERR_INVALID_ARGUMENT, "%d sequences without state_slots need as many slots (got %lld)",
+                             s.num_seqs, (long long)num_slots);
+        const int64_t gates = s.tokens * problem->num_heads_v * s.gate;
+        const int64_t per = (int64_t)problem->num_heads_v * problem->head_dim_k * problem->head_dim_v * s.state;
+        if (num_slots > (1LL << 62) / per) return set_error(KDA_ERR_UNSUPPORTED, "state too large");
+        const Arg args[] = {
+            {"q", q, s.span(s.ldq, s.qk_row), 16, true, false},
+            {"k", k, s.span(s.ldk, s.qk_row), 16, true, false},
+            {"v", v, s.span(s.ldv, s.v_row), 16, true, false},
+            {"g", g, gates, (size_t)s.gate, true, false},
+            {"beta", beta, gates, (size_t)s.gate, true, false},
+            {"state", state, num_slots * per, 16, true, true},
+            {"out", out, s.tokens * s.v_row * s.io, 16, true, true},
+            {"state_slots", state_slots, (int64_t)s.num_seqs * 4, 4, false, false},
+            {"cu_seqlens", cu_seqlens, ((int64_t)s.num_seqs + 1) * 4, 4, false, false},
+        };
+        st = check_args(args);
+        if (st == KDA_OK) st = check_offsets(problem, s, cu_seqlens, cu_seqlens_host);
+        if (st != KDA_OK) return st;
+        if (state_slots_host) {
+            if (!state_slots) return set_error(KDA_ERR_INVALID_ARGUMENT, "state_slots_host given without state_slots");
+            // each slot once: two sequences in one slot would race for it
+            for (int32_t i = 0; i < s.num_seqs; ++i) {
+                const int32_t x = state_slots_host[i];
+                if (x >= num_slots)
+                    return set_error(KDA_ERR_INVALID_ARGUMENT, "state_slots[%d] = %d, there are %lld", i, x, (long long)num_slots);
+                for (int32_t j = 0; x >= 0 && j < i; ++j)
+                    if (state_slots_host[j] == x)
+                        return set_error(KDA_ERR_INVALID_ARGUMENT, "state_slots[%d] and [%d] are both %d", j, i, x);
+            }
+        }
+        if (s.num_seqs == 0 || s.tokens == 0 || num_slots == 0) return done(hipSuccess, "");
+        kda::gdn::DecodeParams r{};
+        r.q = q;
+        r.k = k;
+        r.v = v;
+        r.g = g;
+        r.beta = beta;
+        r.state = state;
+        r.slots = state_slots;
+        r.cu = cu_seqlens;
+        r.out = out;
+        r.ldq = s.ldq;
+        r.ldk = s.ldk;
+        r.ldv = s.ldv;
+        r.num_slots = num_slots;
+        r.num_seqs = s.num_seqs;
+        r.T = problem->seq_len;
+        r.Hk = problem->num_heads_k;
+        r.Hv = problem->num_heads_v;
+        r.dk = problem->head_dim_k;
+        r.dv = problem->head_dim_v;
+        r.gate_bf16 = problem->gate_dtype == KDA_BF16;
+        r.state_bf16 = problem->state_dtype == KDA_BF16;
+        r.scale = problem->scale;
+        return done(kda::gdn::launch_decode(problem->io_dtype == KDA_BF16, r, static_cast<hipStream_t>(stream)),
+                    "kda_gdn_decode launch");
+    } catch (...) {
+        return KDA_ERR_HIP;
+    }
+}
+
+size_t kda_norm_gate_bwd_workspace(int64_t rows, int32_t d, int32_t io_dtype) {
+    if (rows < 0 || (d != 64 && d != 128) || !dtype_ok(io_dtype)) return 0;
+    const int b = kda::norm_gate_bwd_blocks(io_dtype == KDA_BF16 ? KDA_BF16 : KDA_F32, rows, d);
+    return b > 1 ? (size_t)b * d * sizeof(float) : 0;
+}
+
+kda_status_t kda_norm_gate_bwd(int64_t rows, int32_t d, int32_t io_dtype, float eps, const void *o, const void *gate,
+                               const float *weight, const void *d_out, void *d_o, void *d_gate, float *d_weight,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+    try {
+        if (rows < 0) return set_error(KDA_ERR_INVALID_ARGUMENT, "rows %lld < 0", (long long)rows);
+        if (!dtype_ok(io_dtype))
+            return set_error(KDA_ERR_INVALID_ARGUMENT, "io_dtype %d is not KDA_F32 or KDA_BF16", (int)io_dtype);
+        if (d != 64 && d != 128) return set_error(KDA_ERR_UNSUPPORTED, "d=%d: supported are 64 and 128", d);
+        if (!std::isfinite(eps) || eps < 0.f) return set_error(KDA_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+        if (rows > (1LL << 48)) return set_error(KDA_ERR_UNSUPPORTED, "too many rows");
+        const int64_t n = rows * d * bytes_of(io_dtype);
+        const size_t need = kda_norm_gate_bwd_workspace(rows, d, io_dtype);
+        const Arg args[] = {
+            {"o", o, n, 16, true, false},
+            {"gate", gate, n, 16, true, false},
+            {"weight", weight, 4 * d, 16, true, false},
+            {"d_out", d_out, n, 16, true, false},
+            {"d_o", d_o, n, 16, true, true},
+            {"d_gate", d_gate, n, 16, true, true},
+            {"d_weight", d_weight, 4 * d, 16, true, true},
+            {"workspace", workspace, (int64_t)need, 16, false, true},
+        };
+        kda_status_t st = check_args(args);
+        if (st != KDA_OK) return st;
+        if (need > 0 && (!workspace || workspace_bytes < need))
+            return set_error(KDA_ERR_WORKSPACE, "kda_norm_gate_bwd needs a workspace of %zu bytes (got %zu at %p)", need,
+                             workspace_bytes, workspace);
+        return done(kda::launch_norm_gate_bwd(io_dtype == KDA_BF16 ? KDA_BF16 : KDA_F32, rows, d, eps, o, gate, weight,
+                                              d_out, d_o, d_gate, d_weight, static_cast<float *>(workspace),
+                                              static_cast<hipStream_t>(stream)),
+                    "kda_norm_gate_bwd launch");
+    } catch (...) {
+        return KDA_ERR_HIP;
+    }
+}
+
+}  // extern "C"

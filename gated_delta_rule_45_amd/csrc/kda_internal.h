@@ -156,4 +156,10 @@ int64_t norm_gate_blocks(kda_dtype_t io, int64_t rows, int d);
 hipError_t launch_norm_gate(kda_dtype_t io, int64_t rows, int d, float eps, const void *o, const void *z,
                             const float *w, void *out, hipStream_t stream);
 
+// Gradients of the output epilogue; part: norm_gate_bwd_blocks() rows of d fp32 (unused with one block).
+int norm_gate_bwd_blocks(kda_dtype_t io, int64_t rows, int d);
+hipError_t launch_norm_gate_bwd(kda_dtype_t io, int64_t rows, int d, float eps, const void *o, const void *z,
+                                const float *w, const void *dy, void *d_o, void *d_z, float *dw, float *part,
+                                hipStream_t stream);
+
 }  // namespace kda

@@ -394,6 +394,84 @@ kda_status_t kda_chunk_fwd_noalloc(const kda_problem_t *problem, const void *q, 
 /* Bytes of the fixed scratch array kda_chunk_fwd_noalloc uses on each device. */
 size_t kda_noalloc_scratch_bytes(void);
 
+/* Shape of the scalar-gate delta rule calls (kda_gdn_*).  q and k have num_heads_k heads, v, g, beta, out
+ * and the states num_heads_v; value head h reads key head h / (num_heads_v / num_heads_k). */
+typedef struct {
+    int32_t batch;        /* B: sequences of seq_len tokens; must be 1 with cu_seqlens */
+    int32_t seq_len;      /* T per sequence, or the packed token count with cu_seqlens (>= 0) */
+    int32_t num_seqs;     /* with cu_seqlens: its sequences; else ignored */
+    int32_t num_heads_k;  /* Hk >= 1 */
+    int32_t num_heads_v;  /* Hv, a multiple of Hk */
+    int32_t head_dim_k;   /* 64 or 128 */
+    int32_t head_dim_v;   /* 64 or 128 */
+    int32_t io_dtype;     /* kda_dtype_t of q, k, v, out and their gradients */
+    int32_t gate_dtype;   /* kda_dtype_t of g, beta and their gradients */
+    int32_t state_dtype;  /* kda_dtype_t of the states in memory and their gradients (fp32 inside a call) */
+    float scale;          /* multiplies the output */
+    int64_t stride_q;     /* elements from one token of q to the next (0: dense, Hk * d_k); a multiple of */
+    int64_t stride_k;     /* 16 bytes, so that q, k and v may be slices of one projection's output.  The */
+    int64_t stride_v;     /* heads of a token are dense; sequence b starts at token b * seq_len. */
+} kda_gdn_problem_t;
+
+/*
+ * kda_gdn_chunk_fwd -- gated delta rule with one log-gate per token and value head, chunkwise forward
+ * (Kimi Linear summary page, "From linear attention to Gated DeltaNet" and "Chunkwise parallel
+ * algorithm"; the recurrence is kda_chunk_fwd's with exp(g_t) a scalar, so that q, k and the gate are
+ * read once per key head and value head and not expanded to channels):
+ *
+ *     S_t = (I - beta_t k_t k_t^T) exp(g_t) S_{t-1} + beta_t k_t v_t^T,     o_t = scale S_t^T q_t
+ *
+ *  q, k  [tokens, Hk, d_k], v [tokens, Hv, d_v]   io dtype, strides as in the problem
+ *  g, beta [tokens, Hv]            gate dtype; g <= 0 is expected (-inf, a reset, is allowed)
+ *  initial_state, final_state      [num_seqs, Hv, d_k, d_v] state dtype, either may be NULL (zero, not
+ *                                  written); they may be the same buffer
+ *  cu_seqlens, cu_seqlens_host     as for kda_chunk_fwd; offsets outside the tokens are cut off
+ *  out   [tokens, Hv, d_v]         io dtype, dense
+ * No workspace is used and nothing is allocated: the call can be captured and run on several streams
+ * at once.  bf16 io: products take bf16 operands and accumulate in fp32.  Any other overlap of an
+ * output with an argument is refused.  Errors as for kda_chunk_fwd.
+ */
+kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,
+                               const void *g, const void *beta, const void *initial_state, const int32_t *cu_seqlens,
+                               const int32_t *cu_seqlens_host, void *out, void *final_state, void *stream);
+
+/*
+ * kda_gdn_decode -- the same recurrence token by token for one or a few new tokens per sequence, on a pool
+ * of state slots updated in place (the serving form; fp32 arithmetic throughout).
+ *
+ *  q, k, v, g, beta, out, cu_seqlens(_host)  as for kda_gdn_chunk_fwd, with seq_len the new tokens of every
+ *                     sequence (1 for plain decoding), or packed ragged ones
+ *  state              [num_slots, Hv, d_k, d_v] state dtype, read and written
+ *  state_slots        int32 [num_seqs] device: the slot of each sequence; NULL: sequence n has slot n.
+ *                     A slot outside [0, num_slots) marks a padded row: nothing is read for it, and its
+ *                     outputs are left as they are.  Two sequences must not share a slot.
+ *  state_slots_host   optional host copy: slots >= num_slots and slots given twice are then refused.
+ * A sequence without tokens leaves its state as it is.
+ */
+kda_status_t kda_gdn_decode(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,
+                            const void *g, const void *beta, void *state, int64_t num_slots, const int32_t *state_slots,
+                            const int32_t *state_slots_host, const int32_t *cu_seqlens, const int32_t *cu_seqlens_host,
+                            void *out, void *stream);
+
+/*
+ * kda_norm_gate_bwd -- gradients of kda_norm_gate for L = sum(d_out * out).  With r = (mean_j o_j^2 + eps)^-1/2,
+ * hat = o r, s = sigmoid(gate) and dn = d_out * weight * s per row:
+ *
+ *     d_o = r (dn - hat mean_j(dn_j hat_j)),  d_gate = d_out hat weight s (1 - s),  d_weight = sum_rows d_out hat s
+ *
+ *  o (the forward's input, not its output), gate, d_out, d_o, d_gate  [rows, d] io dtype
+ *  weight, d_weight  [d] fp32 (d_weight is written, not added to; zero where rows == 0)
+ *  workspace         kda_norm_gate_bwd_workspace() bytes (may be 0), 16-byte aligned
+ *  Pointers are 16-byte aligned; no output may overlap anything else (for the forward in place, keep o).
+ *  The sums run in a fixed order: the results repeat bit for bit.  Errors as for kda_norm_gate.
+ */
+kda_status_t kda_norm_gate_bwd(int64_t rows, int32_t d, int32_t io_dtype, float eps, const void *o, const void *gate,
+                               const float *weight, const void *d_out, void *d_o, void *d_gate, float *d_weight,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes kda_norm_gate_bwd needs (0 also for arguments it refuses). */
+size_t kda_norm_gate_bwd_workspace(int64_t rows, int32_t d, int32_t io_dtype);
+
 /* Static description of a status code. */
 const char *kda_status_string(kda_status_t status);
 
