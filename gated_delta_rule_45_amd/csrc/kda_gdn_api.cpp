@@ -133,7 +133,7 @@ kda_status_t check_offsets(const kda_gdn_problem_t *p, const Shape &s, const int
 // State columns per workgroup: 64 where that still gives every CU a workgroup (K and Q of a chunk are
 // then staged half as often), else 32.
 int scan_cols(const kda_gdn_problem_t *p, const Shape &s, int cus) {
-    return (int64_t)s.num_seqs * p->num_heads_v * (p->head_dim_v / 64) >= cus ? 64 : 32;
+    return 32;
 }
 
 int current_cus() {

@@ -21,9 +21,7 @@ hipError_t launch_scan(int mode, int cols, const GdnParams &p, hipStream_t strea
     if (p.dk == DK_ && cols == CT_ && mode == M_) return launch_one<BF, DK_, CT_, M_>(p, stream);
 #define GDN_MODES(DK_, CT_) GDN_CASE(DK_, CT_, kFwd) GDN_CASE(DK_, CT_, kKeep) GDN_CASE(DK_, CT_, kRev)
     GDN_MODES(64, 32)
-    GDN_MODES(64, 64)
     GDN_MODES(128, 32)
-    GDN_MODES(128, 64)
 #undef GDN_MODES
 #undef GDN_CASE
     return hipErrorInvalidConfiguration;

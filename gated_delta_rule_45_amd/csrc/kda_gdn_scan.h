@@ -19,13 +19,15 @@
 // K, Q and the value tile of a chunk in LDS and does everything else from there.  Beta multiplies
 // columns of M, so no division by beta appears in the gradients and beta = 0 is exact.
 //
-// One workgroup owns (sequence, value head, CT state columns); three groups of waves run side by
-// side, one chunk apart, with two barriers per chunk:
-//   copy wave      global -> LDS loads of chunk s + 2, no registers in between;
-//   producer waves chunk s + 1: K K^T and Q K^T (lower 16 x 16 tiles), the decays, then the inverse
-//                  of every 32 x 32 diagonal block of I + M B (two 16 x 16 blocks by substitution,
-//                  joined by two fp32 matrix products), and the gates of chunk s + 2;
-//   chain waves    chunk s: 16 state columns each, the fp32 state in accumulator registers.
+// One workgroup owns (sequence, value head, CT state columns); groups of waves run side by side, up to
+// two chunks apart, with two barriers per chunk:
+//   copy wave    global -> LDS loads of chunk s + 2, no registers in between;
+//   tile waves   chunk s + 1: K K^T and Q K^T (lower 16 x 16 tiles), the decays, then the inverse
+//                of every 32 x 32 diagonal block of I + M B (two 16 x 16 blocks by substitution,
+//                joined by two fp32 matrix products), and the gates of chunk s + 2;
+//   chain waves  chunk s: 16 state columns each, the fp32 state in accumulator registers;
+//   output waves chunk s (forward): O from the state and Y that the chain wave of the same columns
+//                hands over in LDS.
 // The 64-token inverse is never formed: the second 32 tokens are solved after the first ones'
 // result is subtracted (one more product on the chain, but two levels of block products and their
 // roundings less per chunk).
@@ -43,6 +45,8 @@
 
 namespace kda {
 namespace gdn {
+
+__device__ __forceinline__ f32x4 load_f4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
 
 enum { kFwd = 0, kKeep = 1, kRev = 2 };
 
@@ -141,9 +145,11 @@ template <bool BF, int DK, int CT, int MODE>
 struct Lds {
     static constexpr int E = BF ? 2 : 4;
     static constexpr int C = BF ? kChunkBf16 : kChunkF32;
-    static constexpr int RT = C / 16, NBLK = C / 32, NCW = CT / 16;
-    static constexpr int PW0 = NCW, CPW = NCW + 3;  // first producer wave, copy wave
-    static constexpr int NT = 64 * (NCW + 4);
+    static constexpr int RT = C / 16, NBLK = C / 32;
+    // waves: chain, output (forward), tile and copy waves
+    static constexpr int NCW = CT / 16, NOW = MODE == kFwd ? NCW : 0;
+    static constexpr int NTW = NBLK == 1 ? 2 : 3;
+    static constexpr int OW0 = NCW, TW0 = OW0 + NOW, CPW = TW0 + NTW, NT = 64 * (CPW + 1);
     static constexpr int RB = DK * E, VRB = CT * E, PRB = C * E, NRB = 32 * E;
     static constexpr int KB = C * RB, QB = MODE == kKeep ? 0 : KB, VB = C * VRB, SB = KB + QB + VB;
     static constexpr int NBUF = 3;
@@ -153,9 +159,11 @@ struct Lds {
     static constexpr int N0 = P0 + 2 * PB, NB = 32 * NRB;
     static constexpr int L0 = N0 + 2 * NBLK * NB, LB = NBLK > 1 ? NB : 0;
     static constexpr int F0 = L0 + 2 * LB, FB = 32 * LS * 4;
-    static constexpr int G0 = F0 + NBLK * FB;             // G of one chunk, fp64, log2 units
-    static constexpr int A0 = G0 + 8 * C, AB = 3 * C * 4 + 16;  // e^G, e^{G_C - G}, beta, e^{G_C}
-    static constexpr int kBytes = A0 + 3 * AB;
+    static constexpr int G0 = F0 + NBLK * FB;  // G from its 16 tokens' start, log2 units, as two floats
+    static constexpr int A0 = G0 + 8 * C, AB = 3 * C * 4 + 64;  // gate factors of one chunk (put_gates)
+    // from a chain wave to its output wave: the state's operand fragments and Y's
+    static constexpr int H0 = A0 + 3 * AB, HS = DK / 32 * 32 * E * 16, HB = HS + RT / 2 * 32 * E * 16;
+    static constexpr int kBytes = H0 + NOW * HB;
     static_assert(kBytes <= 160 * 1024, "LDS of a CU");
 };
 
@@ -217,132 +225,253 @@ __device__ __forceinline__ void stage_chunk(const GdnParams &p, const Walk &w, i
     }
 }
 
-// One producer's 16 x 16 tiles of row block r: the decayed K K^T (scaled by beta into M B) and Q K^T.
-// Forward: rows of the stored matrices are the tokens i that are solved for; reverse: transposed.
-template <bool BF, int DK, int CT, int MODE>
-__device__ __forceinline__ void make_tiles(char *smem, int r, int buf, int par, int abuf, float scale, int l16, int q4) {
+// Loads above this line are issued before anything below it (left alone, the compiler pairs every LDS read
+// with its product and waits for each: 4.1 -> 2.8 us per chunk with the waits spread out).  fp32 operands
+// take twice the registers and keep the compiler's order.
+template <bool BF>
+__device__ __forceinline__ void issue_loads() {
+    if constexpr (BF) __builtin_amdgcn_sched_barrier(0);
+}
+
+// A tile wave's 16 x 16 tiles of one 32 x 32 block (RB, CB) of the decayed K K^T (KK: scaled by beta into
+// M B) and of Q K^T (QK).  Forward: rows of the stored matrices are the tokens i that are solved for;
+// reverse: transposed.  Below the diagonal tiles the decays are products of three stored factors, all
+// at most 1 (row token from its tile's start, between the tiles, column token to its tile's end);
+// inside a diagonal tile they are formed from differences of the cumulative gates, kept as two floats.
+template <bool BF, int DK, int CT, int MODE, int RB, int CB, bool KK, bool QK>
+__device__ __forceinline__ void make_tiles(char *smem, int buf, int par, int abuf, float scale, int l16, int q4) {
     using L = Lds<BF, DK, CT, MODE>;
-    constexpr bool REV = MODE == kRev, HASQ = MODE != kKeep;
+    constexpr bool REV = MODE == kRev, DIAG = RB == CB;
     const char *K = smem + buf * L::SB, *Q = K + L::KB;
     char *P = smem + L::P0 + par * L::PB;
-    char *Lba = smem + L::L0 + par * L::LB;
-    float *Lf = reinterpret_cast<float *>(smem + L::F0);
-    const double *G = reinterpret_cast<const double *>(smem + L::G0);
-    const float *beta = reinterpret_cast<const float *>(smem + L::A0 + abuf * L::AB) + 2 * L::C;
-    Frag2<BF> kr[DK / 32], qr[DK / 32];
+    const float *Gh = reinterpret_cast<const float *>(smem + L::G0), *Gl = Gh + L::C;
+    const float *gate = reinterpret_cast<const float *>(smem + L::A0 + abuf * L::AB);
+    const float *up = gate, *down = gate + L::C, *beta = gate + 2 * L::C, *between = gate + 3 * L::C + 8;
+    Frag2<BF> kr[2][DK / 32], qr[2][DK / 32], kc[2][DK / 32];
 #pragma unroll
-    for (int t = 0; t < DK / 32; ++t) {
-        kr[t] = row_frag<BF, L::RB>(K, 16 * r + l16, 32 * t + 8 * q4);
-        if constexpr (HASQ) qr[t] = row_frag<BF, L::RB>(Q, 16 * r + l16, 32 * t + 8 * q4);
-    }
-#pragma unroll 1
-    for (int c = 0; c <= r; ++c) {
-        f32x4 kk = zero4(), qk = zero4();
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int t = 0; t < DK / 32; ++t) {
-            const Frag2<BF> kc = row_frag<BF, L::RB>(K, 16 * c + l16, 32 * t + 8 * q4);
-            if constexpr (REV) {
-                mma<BF>(kk, kr[t], kc);
-                mma<BF>(qk, qr[t], kc);
+            if constexpr (KK || DIAG) kr[i][t] = row_frag<BF, L::RB>(K, 32 * RB + 16 * i + l16, 32 * t + 8 * q4);
+            if constexpr (QK) qr[i][t] = row_frag<BF, L::RB>(Q, 32 * RB + 16 * i + l16, 32 * t + 8 * q4);
+            if constexpr (!DIAG) kc[i][t] = row_frag<BF, L::RB>(K, 32 * CB + 16 * i + l16, 32 * t + 8 * q4);
+        }
+    // a lane's entries: forward (i, j) = (16 r + l16, 16 c + 4 q4 + e), reverse (16 r + 4 q4 + e, 16 c + l16)
+    f32x4 gam[2][2], bet[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float *bj = beta + 16 * (2 * CB + j);
+        if constexpr (REV) bet[j] = f32x4{bj[l16], bj[l16], bj[l16], bj[l16]};
+        else bet[j] = load_f4(bj + 4 * q4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * RB + i, c = 2 * CB + j;
+            if (c > r) continue;
+            const int own = REV ? 16 * c + l16 : 16 * r + l16, four = (REV ? 16 * r : 16 * c) + 4 * q4;
+            if (c == r) {
+                const float ho = Gh[own], lo = Gl[own];
+                const f32x4 h4 = load_f4(Gh + four), l4 = load_f4(Gl + four);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool low = REV ? four + e >= own : own >= four + e;
+                    const float d = REV ? (h4[e] - ho) + (l4[e] - lo) : (ho - h4[e]) + (lo - l4[e]);
+                    gam[i][j][e] = low ? fast_exp2(d) : 0.f;
+                }
             } else {
-                mma<BF>(kk, kc, kr[t]);
-                if constexpr (HASQ) mma<BF>(qk, kc, qr[t]);
+                const float f = r - c == 1 ? 1.f : between[r - c == 3 ? 2 : c];
+                gam[i][j] = load_f4((REV ? up : down) + four) * ((REV ? down : up)[own] * f);
             }
         }
-        // a lane's entries: forward (i, j) = (16 r + l16, 16 c + 4 q4 + e), reverse (16 r + 4 q4 + e, 16 c + l16)
-        const int own = REV ? 16 * c + l16 : 16 * r + l16, four = (REV ? 16 * r : 16 * c) + 4 * q4;
-        const double Go = G[own];
-        const float4 bf = *reinterpret_cast<const float4 *>(beta + four);
-        const float bo = beta[own], b4[4] = {bf.x, bf.y, bf.z, bf.w};
-        float m[4], pp[4];
-        mfma_settle(kk, qk);
+    }
+    issue_loads<BF>();
+    f32x4 kk[2][2], qk[2][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = REV ? four + e : own, jj = REV ? own : four + e;
-            const double d = REV ? G[four + e] - Go : Go - G[four + e];
-            const float gam = i >= jj ? fast_exp2((float)d) : 0.f;
-            m[e] = i > jj ? kk[e] * gam * (REV ? bo : b4[e]) : 0.f;
-            pp[e] = qk[e] * gam * (REV ? scale : 1.f);
-        }
-        if constexpr (HASQ) row_put4<BF, L::PRB>(P, own, (four & ~31) + kpos(four & 31), pp[0], pp[1], pp[2], pp[3]);
-        if ((r >> 1) == (c >> 1)) {
-            float *dst = Lf + (r >> 1) * 32 * L::LS;
-            if constexpr (REV) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dst[((four + e) & 31) * L::LS + (own & 31)] = m[e];
-            } else {
-                *reinterpret_cast<float4 *>(dst + (own & 31) * L::LS + (four & 31)) = make_float4(m[0], m[1], m[2], m[3]);
+        for (int j = 0; j < 2; ++j) kk[i][j] = qk[i][j] = zero4();
+#pragma unroll
+    for (int t = 0; t < DK / 32; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (2 * CB + j > 2 * RB + i) continue;
+                const Frag2<BF> y = DIAG ? kr[j][t] : kc[j][t];
+                if constexpr (KK) {
+                    if constexpr (REV) mma<BF>(kk[i][j], kr[i][t], y);
+                    else mma<BF>(kk[i][j], y, kr[i][t]);
+                }
+                if constexpr (QK) {
+                    if constexpr (REV) mma<BF>(qk[i][j], qr[i][t], y);
+                    else mma<BF>(qk[i][j], y, qr[i][t]);
+                }
             }
-        } else {
-            row_put4<BF, L::NRB>(Lba, own & 31, kpos(four & 31), -m[0], -m[1], -m[2], -m[3]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = 2 * RB + i, c = 2 * CB + j;
+            if (c > r) continue;
+            const int own = REV ? 16 * c + l16 : 16 * r + l16, four = (REV ? 16 * r : 16 * c) + 4 * q4;
+            if constexpr (KK) {
+                f32x4 m = kk[i][j] * gam[i][j] * bet[j];
+                if constexpr (DIAG) {
+                    if (c == r) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m[e] = own == four + e ? 0.f : m[e];
+                    }
+                    float *dst = reinterpret_cast<float *>(smem + L::F0) + RB * 32 * L::LS;
+                    if constexpr (REV) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dst[((four + e) & 31) * L::LS + (own & 31)] = m[e];
+                    } else {
+                        *reinterpret_cast<f32x4 *>(dst + (own & 31) * L::LS + (four & 31)) = m;
+                    }
+                } else {
+                    row_put4<BF, L::NRB>(smem + L::L0 + par * L::LB, own & 31, kpos(four & 31), -m[0], -m[1], -m[2], -m[3]);
+                }
+            }
+            if constexpr (QK) {
+                f32x4 m = qk[i][j] * gam[i][j];
+                if constexpr (REV) m = m * scale;
+                row_put4<BF, L::PRB>(P, own, (four & ~31) + kpos(four & 31), m[0], m[1], m[2], m[3]);
+            }
         }
+}
+
+// Four rank-1 terms of a substitution inside rows of 16 lanes, other lanes' values read through DPP.
+// s_nop 1: a DPP operand must not have been written by the two instructions before.
+// rows: n[c] += m * (n[c] of lane J), c = 0..3
+template <int J>
+__device__ __forceinline__ void bcast_rows4(float *n, float m) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %0, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %1, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %2, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %3, %4 row_newbcast:%5 row_mask:0xf bank_mask:0xf"
+        : "+v"(n[0]), "+v"(n[1]), "+v"(n[2]), "+v"(n[3])
+        : "v"(m), "n"(J));
+}
+// columns: x += n[j] * (m[j] of lane I), j = 0..3
+template <int I>
+__device__ __forceinline__ void bcast_cols4(float &x, const float *n, const float *m) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %5, %1 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %6, %2 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %7, %3 row_newbcast:%9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %8, %4 row_newbcast:%9 row_mask:0xf bank_mask:0xf"
+        : "+v"(x)
+        : "v"(n[0]), "v"(n[1]), "v"(n[2]), "v"(n[3]), "v"(m[0]), "v"(m[1]), "v"(m[2]), "v"(m[3]), "n"(I));
+}
+// A 16 x 16 x 16 fp32 product in two independent halves.
+__device__ __forceinline__ f32x4 product16(const Frag<false> &a, const Frag<false> &b) {
+    f32x4 x = zero4(), y = zero4();
+    x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v.x, b.v.x, x, 0, 0, 0);
+    y = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v.y, b.v.y, y, 0, 0, 0);
+    x = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v.z, b.v.z, x, 0, 0, 0);
+    y = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v.w, b.v.w, y, 0, 0, 0);
+    return x + y;
+}
+// Eight columns of row l16 of (I + L)^-1 from nl, row l16 of the strictly lower -L: row j, once it is solved, is
+// taken off every later row (nl is zero in the others).  n[0..3] are columns that row j can have for every j,
+// n[4..7] columns from 8 on.
+template <int J>
+__device__ __forceinline__ void solve_rows(float (&n)[8], const float (&nl)[16]) {
+    if constexpr (J < 15) {
+        bcast_rows4<J>(n, nl[J]);
+        if constexpr (J >= 8) bcast_rows4<J>(n + 4, nl[J]);
+        solve_rows<J + 1>(n, nl);
+    }
+}
+// Column l16 of (I + L)^-1, the rows of -L held by the lanes.
+template <int I>
+__device__ __forceinline__ void solve_cols(float (&n)[16], const float (&nl)[16]) {
+    if constexpr (I < 16) {
+        float x = n[I];
+        n[I] = 0.f;  // not yet a term of its own row
+#pragma unroll
+        for (int j = 0; j < I; j += 4) bcast_cols4<I>(x, n + j, nl + j);
+        n[I] = x;
+        solve_cols<I + 1>(n, nl);
     }
 }
 
-// The inverse of one 32 x 32 diagonal block of I + M B, minus the identity (reverse: transposed).
-// Lane (sub, col) solves column col of the 16 x 16 diagonal block sub by forward substitution; the block
-// below the diagonal is -N11 (L10 N00).
+// The inverse of one 32 x 32 diagonal block of I + M B, minus the identity (reverse: transposed), by the wave
+// that made its tiles: two 16 x 16 diagonal blocks by forward substitution in registers (lanes of 16
+// exchange values through DPP, about 8 cycles a term), and -N11 (L10 N00) below them.  Forward: a lane
+// has one row and eight columns (0-3 and 12-15, or 4-7 and 8-11); reverse: one column, half of which it
+// stores.
 template <bool BF, int DK, int CT, int MODE>
 __device__ __forceinline__ void invert_block(char *smem, int blk, int par, int lane) {
     using L = Lds<BF, DK, CT, MODE>;
     constexpr bool REV = MODE == kRev;
-    const int l16 = lane & 15, q4 = lane >> 4, sub = q4 & 1;
+    const int l16 = lane & 15, q4 = lane >> 4, sub = q4 & 1, half = q4 >> 1;
+    const int c0 = half ? 4 : 0, c1 = half ? 8 : 12;
     float *Lb = reinterpret_cast<float *>(smem + L::F0) + blk * 32 * L::LS;
     char *N = smem + L::N0 + (par * L::NBLK + blk) * L::NB;
-    float x[16];
-    const float *Ld = Lb + 16 * sub * L::LS + 16 * sub;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float s = i == l16 ? 1.f : 0.f;
-#pragma unroll
-        for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
-            const float4 l4 = *reinterpret_cast<const float4 *>(Ld + i * L::LS + 4 * j4);
-            const float lr[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (4 * j4 + j < i) s = fmaf(-lr[j], x[4 * j4 + j], s);
-        }
-        x[i] = s;
-    }
+    const float *Ld = Lb + (16 * sub + l16) * L::LS + 16 * sub;
+    float nl[16], n[8];
     wave_lds_sync();
-    // columns of both inverses to LDS: block 0 into the unused upper right block, block 1 over the upper left
-    // one, which has been read
-    if (lane < 32) {
-        float *dst = Lb + l16 * L::LS + (sub ? 0 : 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4 *>(dst + 4 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        if constexpr (REV) {
+    for (int i = 0; i < 4; ++i) {
+        const f32x4 v = load_f4(Ld + 4 * i);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = 4 * i + j == l16 ? 0.f : x[4 * i + j];
-                row_put4<BF, L::NRB>(N, 16 * sub + l16, 8 * i + 4 * sub, y[0], y[1], y[2], y[3]);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                row_put1<BF, L::NRB>(N, 16 * sub + i, kpos(16 * sub + l16), i == l16 ? 0.f : x[i]);
-        }
+        for (int j = 0; j < 4; ++j) nl[4 * i + j] = -v[j];
     }
-    wave_lds_sync();
-    Frag<false> l10, n00, n11;
+    Frag<false> l10;
     l10.v = *reinterpret_cast<const float4 *>(Lb + (16 + l16) * L::LS + 4 * q4);
-    n00.v = *reinterpret_cast<const float4 *>(Lb + l16 * L::LS + 16 + 4 * q4);
-    const float *c11 = Lb + 4 * q4 * L::LS + l16;
-    n11 = make_frag<false>(c11[0], c11[L::LS], c11[2 * L::LS], c11[3 * L::LS]);
-    f32x4 t = zero4(), n10 = zero4();
-    mma16(t, l10, n00);
-    mfma_settle(t);
-    mma16(n10, n11, frag_from_acc<false>(t, -1.f));
-    mfma_settle(n10);
     if constexpr (REV) {
-        row_put4<BF, L::NRB>(N, l16, kpos(16 + 4 * q4), n10[0], n10[1], n10[2], n10[3]);
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = i == l16 ? 1.f : 0.f;
+        solve_cols<1>(x, nl);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            n[j] = half ? x[4 + j] : x[j];
+            n[4 + j] = half ? x[8 + j] : x[12 + j];
+        }
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) row_put1<BF, L::NRB>(N, 16 + 4 * q4 + j, kpos(l16), n10[j]);
+        for (int j = 0; j < 4; ++j) {
+            n[j] = c0 + j == l16 ? 1.f : 0.f;
+            n[4 + j] = c1 + j == l16 ? 1.f : 0.f;
+        }
+        solve_rows<0>(n, nl);
     }
+    wave_lds_sync();
+    // both inverses to LDS: block 0 into the unused upper right block, block 1 over the upper left one, which has
+    // been read
+    float *dst = Lb + l16 * L::LS + (sub ? 0 : 16);
+    *reinterpret_cast<float4 *>(dst + c0) = make_float4(n[0], n[1], n[2], n[3]);
+    *reinterpret_cast<float4 *>(dst + c1) = make_float4(n[4], n[5], n[6], n[7]);
+    wave_lds_sync();
+    // forward: T = L10 N00, then N10 = -N11 T with rows of N11 as A; its transpose (the operands exchanged) puts
+    // four columns of a row of N10 in a lane.  Reverse: the stored rows are columns of the inverses.
+    const float *s00 = Lb + 16, *s11 = Lb;
+    Frag<false> n00, n11;
+    if constexpr (REV) {
+        n00.v = *reinterpret_cast<const float4 *>(s00 + l16 * L::LS + 4 * q4);  // N00[4 q4 + j][l16]
+        n11 = make_frag<false>(s11[4 * q4 * L::LS + l16], s11[(4 * q4 + 1) * L::LS + l16],
+                               s11[(4 * q4 + 2) * L::LS + l16], s11[(4 * q4 + 3) * L::LS + l16]);  // N11[l16][..]
+    } else {
+        n00 = make_frag<false>(s00[4 * q4 * L::LS + l16], s00[(4 * q4 + 1) * L::LS + l16],
+                               s00[(4 * q4 + 2) * L::LS + l16], s00[(4 * q4 + 3) * L::LS + l16]);
+        n11.v = *reinterpret_cast<const float4 *>(s11 + l16 * L::LS + 4 * q4);
+    }
+    issue_loads<BF>();
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        y[j] = c0 + j == l16 ? 0.f : n[j];
+        y[4 + j] = c1 + j == l16 ? 0.f : n[4 + j];
+    }
+    row_put4<BF, L::NRB>(N, 16 * sub + l16, kpos(16 * sub + c0), y[0], y[1], y[2], y[3]);
+    row_put4<BF, L::NRB>(N, 16 * sub + l16, kpos(16 * sub + c1), y[4], y[5], y[6], y[7]);
+    const f32x4 t = product16(l10, n00);
+    const Frag<false> mt = frag_from_acc<false>(t, -1.f);
+    // reverse: N10[4 q4 + j][l16], forward: N10^T[4 q4 + j][l16]
+    const f32x4 n10 = REV ? product16(n11, mt) : product16(mt, n11);
+    row_put4<BF, L::NRB>(N, (REV ? 0 : 16) + l16, kpos((REV ? 16 : 0) + 4 * q4), n10[0], n10[1], n10[2], n10[3]);
     wave_lds_sync();
 }
 
@@ -368,27 +497,90 @@ __device__ __forceinline__ RawGate load_gate(const GdnParams &p, const Walk &w, 
 }
 // Cumulative gate of the chunk in fp64 (log2 units; a gate below -1e4 is as good as e^g = 0 and keeps the
 // differences finite).
-__device__ __forceinline__ double gate_scan(float g, int lane) {
-    double s = (double)fmaxf(g, -1e4f) * 1.4426950408889634;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(s, d);
-        s += lane >= d ? o : 0.0;
-    }
-    return s;
+__device__ __forceinline__ double lane_value(double x, int lane) {
+    const long long b = __double_as_longlong(x);
+    const unsigned lo = __builtin_amdgcn_readlane((int)b, lane), hi = __builtin_amdgcn_readlane((int)(b >> 32), lane);
+    return __longlong_as_double((long long)hi << 32 | lo);
 }
+template <int N>
+__device__ __forceinline__ double row_shr64(double x) {
+    const long long b = __double_as_longlong(x);
+    const unsigned lo = __builtin_amdgcn_update_dpp(0, (int)b, 0x110 + N, 0xf, 0xf, true);
+    const unsigned hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), 0x110 + N, 0xf, 0xf, true);
+    return __longlong_as_double((long long)hi << 32 | lo);
+}
+struct GateScan {
+    double s, end[5];  // the lane's cumulative gate; those at the starts of the four 16-token blocks and at the end
+};
+__device__ __forceinline__ GateScan gate_scan(float g) {
+    GateScan r;
+    double s = (double)fmaxf(g, -1e4f) * 1.4426950408889634;
+    s += row_shr64<1>(s);
+    s += row_shr64<2>(s);
+    s += row_shr64<4>(s);
+    s += row_shr64<8>(s);
+    r.end[0] = 0.0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) r.end[b + 1] = r.end[b] + lane_value(s, 16 * b + 15);
+    r.s = s;
+    return r;
+}
+// A chunk's gate factors (all at most 1 for g <= 0), lane = token: up = e^{G - G(end of the previous 16
+// tokens)}, down = e^{G(end of its 16 tokens) - G}, beta; then per block e^{G} of its start and
+// e^{G_C - G} of its end, the decays between non-neighbouring blocks (2,0), (3,1), (3,0), and e^{G_C}.
 template <bool BF, int DK, int CT, int MODE>
 __device__ __forceinline__ void put_gates(char *smem, int abuf, const RawGate &r, int lane) {
     using L = Lds<BF, DK, CT, MODE>;
-    const double s = gate_scan(r.g, lane), end = __shfl(s, L::C - 1);
+    const GateScan sc = gate_scan(r.g);
+    const int blk = lane >> 4;
+    const double start = blk == 0 ? 0.0 : blk == 1 ? sc.end[1] : blk == 2 ? sc.end[2] : sc.end[3];
+    const double own_end = blk == 0 ? sc.end[1] : blk == 1 ? sc.end[2] : blk == 2 ? sc.end[3] : sc.end[4];
+    const double end = sc.end[L::C / 16], s = sc.s + start;
     float *a = reinterpret_cast<float *>(smem + L::A0 + abuf * L::AB);
     if (lane < L::C) {
-        reinterpret_cast<double *>(smem + L::G0)[lane] = s;
-        a[lane] = fast_exp2((float)s);
-        a[L::C + lane] = fast_exp2((float)(end - s));
+        float *G = reinterpret_cast<float *>(smem + L::G0);
+        const float hi = (float)sc.s;
+        G[lane] = hi;
+        G[L::C + lane] = (float)(sc.s - hi);
+        a[lane] = fast_exp2((float)sc.s);
+        a[L::C + lane] = fast_exp2((float)(own_end - s));
         a[2 * L::C + lane] = r.b;
-        if (lane == 0) a[3 * L::C] = fast_exp2((float)end);
+        float *f = a + 3 * L::C;
+        if ((lane & 15) == 0) {
+            f[lane >> 4] = fast_exp2((float)start);
+            f[4 + (lane >> 4)] = fast_exp2((float)(end - own_end));
+        }
+        if (lane == 0) {
+            f[8] = fast_exp2((float)(sc.end[2] - sc.end[1]));
+            f[9] = fast_exp2((float)(sc.end[3] - sc.end[2]));
+            f[10] = fast_exp2((float)(sc.end[3] - sc.end[1]));
+            f[11] = fast_exp2((float)end);
+        }
     }
+}
+
+// One operand fragment pair per lane, handed from wave to wave.
+template <bool BF>
+__device__ __forceinline__ void hand_put(char *base, int i, int lane, const Frag2<BF> &f) {
+    if constexpr (BF) {
+        *reinterpret_cast<uint4 *>(base + (i * 64 + lane) * 16) = make_uint4(f.a.v.x, f.a.v.y, f.b.v.x, f.b.v.y);
+    } else {
+        *reinterpret_cast<float4 *>(base + (2 * i * 64 + lane) * 16) = f.a.v;
+        *reinterpret_cast<float4 *>(base + ((2 * i + 1) * 64 + lane) * 16) = f.b.v;
+    }
+}
+template <bool BF>
+__device__ __forceinline__ Frag2<BF> hand_get(const char *base, int i, int lane) {
+    Frag2<BF> f;
+    if constexpr (BF) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(base + (i * 64 + lane) * 16);
+        f.a.v = make_uint2(w.x, w.y);
+        f.b.v = make_uint2(w.z, w.w);
+    } else {
+        f.a.v = *reinterpret_cast<const float4 *>(base + (2 * i * 64 + lane) * 16);
+        f.b.v = *reinterpret_cast<const float4 *>(base + ((2 * i + 1) * 64 + lane) * 16);
+    }
+    return f;
 }
 
 // Four consecutive tokens (16 rt + 4 q4 ..) of a wave's column l16 of the value tile.
@@ -406,8 +598,6 @@ __device__ __forceinline__ f32x4 frag_f32(const Frag<BF> &f) {
     if constexpr (BF) return f32x4{bf16_lo(f.v.x), bf16_hi(f.v.x), bf16_lo(f.v.y), bf16_hi(f.v.y)};
     else return f32x4{f.v.x, f.v.y, f.v.z, f.v.w};
 }
-__device__ __forceinline__ f32x4 load_f4(const float *p) { return *reinterpret_cast<const f32x4 *>(p); }
-
 // A wave's C x 16 result (accumulator layout, fp32) to rows of a [tokens, Hv, dv] tensor: through the wave's
 // own columns of the value tile, which it has read, so that rows leave as 16-byte pieces.
 template <bool BF, int VRB, int RT>
@@ -469,28 +659,34 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         }
         return;
     }
-    if (wave >= L::PW0) {
-        // ------------------------------------------------------------------ producer waves
+    if (wave >= L::TW0) {
+        // ------------------------------------------------------------------ tile waves
         if (nch == 0) return;
-        const int pw = wave - L::PW0;
+        const int pw = wave - L::TW0;
+        constexpr int GW = L::NTW - 1;  // also makes the gates; the waves of the diagonal blocks their inverses
         RawGate raw{0.f, 0.f};
-        if (pw == 2) {
+        if (pw == GW) {
             raw = load_gate<C>(p, w, ci(0), lane);
             put_gates<BF, DK, CT, MODE>(smem, 0, raw, lane);
             if (nch > 1) raw = load_gate<C>(p, w, ci(1), lane);
         }
         auto tiles = [&](int s) {
             const int buf = s % L::NBUF, par = s & 1, ab = s % 3;
-            if constexpr (RT == 4) {
-                make_tiles<BF, DK, CT, MODE>(smem, pw == 0 ? 3 : pw == 1 ? 2 : 1, buf, par, ab, p.scale, l16, q4);
-                if (pw == 2) make_tiles<BF, DK, CT, MODE>(smem, 0, buf, par, ab, p.scale, l16, q4);
-            } else if (pw < 2) {
-                make_tiles<BF, DK, CT, MODE>(smem, pw, buf, par, ab, p.scale, l16, q4);
+            constexpr bool HASQ = MODE != kKeep;
+#define GDN_TILES(RB_, CB_, KK_, QK_) make_tiles<BF, DK, CT, MODE, RB_, CB_, KK_, QK_>(smem, buf, par, ab, p.scale, l16, q4)
+            if constexpr (L::NBLK == 2) {
+                if (pw == 0) GDN_TILES(0, 0, true, HASQ);
+                if (pw == 1) GDN_TILES(1, 1, true, HASQ);
+                if (pw == 2) GDN_TILES(1, 0, true, HASQ);
+            } else {
+                if (pw == 0) GDN_TILES(0, 0, true, false);
+                if (HASQ && pw == 1) GDN_TILES(0, 0, false, HASQ);
             }
+#undef GDN_TILES
         };
         auto finish = [&](int s) {  // the inverse of chunk s, the gates of chunk s + 1
             if (pw < L::NBLK) invert_block<BF, DK, CT, MODE>(smem, pw, s & 1, lane);
-            if (pw == 2 && s + 1 < nch) {
+            if (pw == GW && s + 1 < nch) {
                 put_gates<BF, DK, CT, MODE>(smem, (s + 1) % 3, raw, lane);
                 if (s + 2 < nch) raw = load_gate<C>(p, w, ci(s + 2), lane);
             }
@@ -504,6 +700,64 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
             if (s + 1 < nch) tiles(s + 1);
             __syncthreads();  // A
             if (s + 1 < nch) finish(s + 1);
+            __syncthreads();  // B
+        }
+        return;
+    }
+
+    if (MODE == kFwd && wave >= L::OW0) {
+        // ------------------------------------------------------------------ output waves
+        if (nch == 0) return;
+        const int cw = wave - L::OW0;
+        const char *hand = smem + L::H0 + cw * L::HB;
+        __syncthreads();
+        __syncthreads();
+        __syncthreads();
+#pragma unroll 1
+        for (int s = 0; s < nch; ++s) {
+            const int clen = min(C, w.len - s * C);
+            const char *Q = smem + (s % L::NBUF) * L::SB + L::KB, *P = smem + L::P0 + (s & 1) * L::PB;
+            const float *gate = reinterpret_cast<const float *>(smem + L::A0 + (s % 3) * L::AB);
+            IO *out = static_cast<IO *>(p.out) + ((w.tok0 + (int64_t)s * C) * p.Hv + w.h) * p.dv + w.col0 + 16 * cw + 4 * q4;
+            __syncthreads();  // A
+            Frag2<BF> qf[RT][K2], pf[RT][RT / 2];
+            float e[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+                for (int t = 0; t < K2; ++t) qf[rt][t] = row_frag<BF, L::RB>(Q, 16 * rt + l16, 32 * t + 8 * q4);
+#pragma unroll
+                for (int u = 0; u <= rt / 2; ++u) pf[rt][u] = row_frag<BF, L::PRB>(P, 16 * rt + l16, 32 * u + 8 * q4);
+                e[rt] = gate[16 * rt + l16] * gate[3 * C + rt];
+            }
+            Frag2<BF> sb[K2], yp[RT / 2];
+#pragma unroll
+            for (int t = 0; t < K2; ++t) sb[t] = hand_get<BF>(hand, t, lane);
+#pragma unroll
+            for (int u = 0; u < RT / 2; ++u) yp[u] = hand_get<BF>(hand + L::HS, u, lane);
+            issue_loads<BF>();
+            // O^T tiles: a lane holds four consecutive columns of one token
+            f32x4 o[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) o[rt] = zero4();
+#pragma unroll
+            for (int t = 0; t < K2; ++t)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) mma<BF>(o[rt], sb[t], qf[rt][t]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) o[rt] = o[rt] * e[rt];
+#pragma unroll
+            for (int u = 0; u < RT / 2; ++u)
+#pragma unroll
+                for (int rt = 2 * u; rt < RT; ++rt) mma<BF>(o[rt], yp[u], pf[rt][u]);
+#pragma unroll
+            for (int rt = 0; rt < RT; rt += 2) mfma_settle(o[rt], o[rt + 1]);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                if (16 * rt + l16 < clen)
+                    IoTraits<IO>::store4(out + (int64_t)(16 * rt + l16) * p.Hv * p.dv,
+                                         make_float4(o[rt][0] * p.scale, o[rt][1] * p.scale, o[rt][2] * p.scale,
+                                                     o[rt][3] * p.scale));
             __syncthreads();  // B
         }
         return;
@@ -531,16 +785,22 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
     for (int s = 0; s < nch; ++s) {
         const int c = ci(s), clen = min(C, w.len - c * C);
         const int64_t tok = w.tok0 + (int64_t)c * C;
-        char *K = smem + (s % L::NBUF) * L::SB, *Q = K + L::KB, *V = K + L::KB + L::QB;
-        const char *P = smem + L::P0 + (s & 1) * L::PB;
+        char *K = smem + (s % L::NBUF) * L::SB, *V = K + L::KB + L::QB;
+        [[maybe_unused]] const char *Q = K + L::KB;
+        [[maybe_unused]] char *hand = smem + L::H0 + wave * L::HB;
+        [[maybe_unused]] const char *P = smem + L::P0 + (s & 1) * L::PB;
         const char *N = smem + L::N0 + (s & 1) * L::NBLK * L::NB, *Lba = smem + L::L0 + (s & 1) * L::LB;
-        const float *eG = reinterpret_cast<const float *>(smem + L::A0 + (s % 3) * L::AB);
-        const float *eB = eG + C, *beta = eG + 2 * C;
-        const float eC = eG[3 * C];
+        const float *gate = reinterpret_cast<const float *>(smem + L::A0 + (s % 3) * L::AB), *beta = gate + 2 * C;
+        const float eC = gate[3 * C + 11];
+        auto eG = [&](int rt) { return load_f4(gate + 16 * rt + 4 * q4) * gate[3 * C + rt]; };          // e^G
+        auto eB = [&](int rt) { return load_f4(gate + C + 16 * rt + 4 * q4) * gate[3 * C + 4 + rt]; };  // e^{G_C - G}
         Frag2<BF> Sb[K2];
 #pragma unroll
         for (int t = 0; t < K2; ++t) Sb[t] = {frag_from_acc<BF>(S[2 * t]), frag_from_acc<BF>(S[2 * t + 1])};
-        if constexpr (MODE != kFwd) {
+        if constexpr (MODE == kFwd) {
+#pragma unroll
+            for (int t = 0; t < K2; ++t) hand_put<BF>(hand, t, lane, Sb[t]);
+        } else {
             // the state entering (reverse: the gradient of the state leaving) the chunk, [dv][d_k]
             IO *dst = static_cast<IO *>(p.hs) + (((w.slot0 + c) * p.Hv + w.h) * p.dv + col) * DK + 8 * q4;
 #pragma unroll
@@ -555,20 +815,36 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
             }
         }
         f32x4 x[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            x[rt] = zero4();
-#pragma unroll
-            for (int t = 0; t < K2; ++t) mma<BF>(x[rt], row_frag<BF, L::RB>(K, 16 * rt + l16, 32 * t + 8 * q4), Sb[t]);
-        }
         Frag<BF> vf[RT];
+        {
+            Frag2<BF> kf[RT][K2];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) vf[rt] = value_frag<BF, L::VRB>(V, wave, rt, l16, q4);
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int t = 0; t < K2; ++t) kf[rt][t] = row_frag<BF, L::RB>(K, 16 * rt + l16, 32 * t + 8 * q4);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) vf[rt] = value_frag<BF, L::VRB>(V, wave, rt, l16, q4);
+            issue_loads<BF>();
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) x[rt] = zero4();
+#pragma unroll
+            for (int t = 0; t < K2; ++t)
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) mma<BF>(x[rt], kf[rt][t], Sb[t]);
+        }
+        // the inverse blocks and M B between them
+        Frag2<BF> nf[L::NBLK][2], lf[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int b = 0; b < L::NBLK; ++b) nf[b][h] = row_frag<BF, L::NRB>(N + b * L::NB, 16 * h + l16, 8 * q4);
+            if constexpr (L::NBLK > 1) lf[h] = row_frag<BF, L::NRB>(Lba, 16 * h + l16, 8 * q4);
+        }
 
         if constexpr (!REV) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const f32x4 e = load_f4(eG + 16 * rt + 4 * q4), v = frag_f32<BF>(vf[rt]);
+                const f32x4 e = eG(rt), v = frag_f32<BF>(vf[rt]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[rt][j] = fmaf(-e[j], x[rt][j], v[j]);
             }
@@ -578,62 +854,45 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
                 if (b > 0) {
                     const Frag2<BF> za = {frag_from_acc<BF>(x[0]), frag_from_acc<BF>(x[1])};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) mma<BF>(x[2 + h], row_frag<BF, L::NRB>(Lba, 16 * h + l16, 8 * q4), za);
+                    for (int h = 0; h < 2; ++h) mma<BF>(x[2 + h], lf[h], za);
                 }
                 const Frag2<BF> xb = {frag_from_acc<BF>(x[2 * b]), frag_from_acc<BF>(x[2 * b + 1])};
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    mma<BF>(x[2 * b + h], row_frag<BF, L::NRB>(N + b * L::NB, 16 * h + l16, 8 * q4), xb);
+                for (int h = 0; h < 2; ++h) mma<BF>(x[2 * b + h], nf[b][h], xb);
             }
-            __syncthreads();  // A
-            Frag2<BF> yp[RT / 2], ys[RT / 2];
+            Frag2<BF> ys[RT / 2];
 #pragma unroll
             for (int u = 0; u < RT / 2; ++u) {
                 f32x4 a[2], d[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int rt = 2 * u + h;
-                    const f32x4 bt = load_f4(beta + 16 * rt + 4 * q4), e = load_f4(eB + 16 * rt + 4 * q4);
+                    const f32x4 bt = load_f4(beta + 16 * rt + 4 * q4), e = eB(rt);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         a[h][j] = bt[j] * x[rt][j];
                         d[h][j] = e[j] * a[h][j];
                     }
                 }
-                yp[u] = {frag_from_acc<BF>(a[0]), frag_from_acc<BF>(a[1])};
+                if constexpr (MODE == kFwd)
+                    hand_put<BF>(hand + L::HS, u, lane, Frag2<BF>{frag_from_acc<BF>(a[0]), frag_from_acc<BF>(a[1])});
                 ys[u] = {frag_from_acc<BF>(d[0]), frag_from_acc<BF>(d[1])};
             }
+            Frag2<BF> kt[KT][RT / 2];
 #pragma unroll
-            for (int ct = 0; ct < KT; ++ct) {
+            for (int ct = 0; ct < KT; ++ct)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) S[ct][j] *= eC;
+                for (int u = 0; u < RT / 2; ++u) kt[ct][u] = col_frag<BF, L::RB>(K, ct, u, l16, q4);
+            __syncthreads();  // A
 #pragma unroll
-                for (int u = 0; u < RT / 2; ++u) mma<BF>(S[ct], col_frag<BF, L::RB>(K, ct, u, l16, q4), ys[u]);
-            }
-            if constexpr (MODE == kFwd) {
-                // O^T tiles: a lane holds four consecutive columns of one token
-                IO *out = static_cast<IO *>(p.out) + (tok * p.Hv + w.h) * p.dv + w.col0 + 16 * wave + 4 * q4;
+            for (int ct = 0; ct < KT; ++ct) S[ct] = S[ct] * eC;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    f32x4 o = zero4();
+            for (int u = 0; u < RT / 2; ++u)
 #pragma unroll
-                    for (int t = 0; t < K2; ++t)
-                        mma<BF>(o, Sb[t], row_frag<BF, L::RB>(Q, 16 * rt + l16, 32 * t + 8 * q4));
-                    const float e = eG[16 * rt + l16];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o[j] *= e;
-#pragma unroll
-                    for (int u = 0; u <= rt / 2; ++u)
-                        mma<BF>(o, yp[u], row_frag<BF, L::PRB>(P, 16 * rt + l16, 32 * u + 8 * q4));
-                    mfma_settle(o);
-                    if (16 * rt + l16 < clen)
-                        IoTraits<IO>::store4(out + (int64_t)(16 * rt + l16) * p.Hv * p.dv,
-                                             make_float4(o[0] * p.scale, o[1] * p.scale, o[2] * p.scale, o[3] * p.scale));
-                }
-            } else {
+                for (int ct = 0; ct < KT; ++ct) mma<BF>(S[ct], kt[ct][u], ys[u]);
+            if constexpr (MODE == kKeep)
                 put_value_rows<BF, L::VRB, RT>(V, static_cast<IO *>(p.zs) + (tok * p.Hv + w.h) * p.dv + w.col0,
                                                (int64_t)p.Hv * p.dv, wave, x, clen, lane);
-            }
         } else {
             // rows past the end of the sequence were staged from its last row: no gradient there
 #pragma unroll
@@ -647,13 +906,23 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
             // dY = Diag(e^{G_C - G}) K dS + scale P^T dO, times beta
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-                const f32x4 e = load_f4(eB + 16 * rt + 4 * q4), bt = load_f4(beta + 16 * rt + 4 * q4);
+                const f32x4 e = eB(rt);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[rt][j] *= e[j];
+            }
+            Frag2<BF> pf[RT][RT / 2];
 #pragma unroll
-                for (int u = rt / 2; u < RT / 2; ++u)
-                    mma<BF>(x[rt], row_frag<BF, L::PRB>(P, 16 * rt + l16, 32 * u + 8 * q4), Frag2<BF>{vf[2 * u], vf[2 * u + 1]});
-                mfma_settle(x[rt]);
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int u = rt / 2; u < RT / 2; ++u) pf[rt][u] = row_frag<BF, L::PRB>(P, 16 * rt + l16, 32 * u + 8 * q4);
+            issue_loads<BF>();
+#pragma unroll
+            for (int u = 0; u < RT / 2; ++u)
+#pragma unroll
+                for (int rt = 0; rt < 2 * u + 2; ++rt) mma<BF>(x[rt], pf[rt][u], Frag2<BF>{vf[2 * u], vf[2 * u + 1]});
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const f32x4 bt = load_f4(beta + 16 * rt + 4 * q4);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[rt][j] *= bt[j];
             }
@@ -663,42 +932,50 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
                 if (b < L::NBLK - 1) {
                     const Frag2<BF> xb = {frag_from_acc<BF>(x[2 * b + 2]), frag_from_acc<BF>(x[2 * b + 3])};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        mma<BF>(x[2 * b + h], row_frag<BF, L::NRB>(Lba, 16 * h + l16, 8 * q4), xb);
+                    for (int h = 0; h < 2; ++h) mma<BF>(x[2 * b + h], lf[h], xb);
                 }
                 const Frag2<BF> zb = {frag_from_acc<BF>(x[2 * b]), frag_from_acc<BF>(x[2 * b + 1])};
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    mma<BF>(x[2 * b + h], row_frag<BF, L::NRB>(N + b * L::NB, 16 * h + l16, 8 * q4), zb);
+                for (int h = 0; h < 2; ++h) mma<BF>(x[2 * b + h], nf[b][h], zb);
             }
-            __syncthreads();  // A
-            Frag2<BF> dq[RT / 2], dx[RT / 2];
+            Frag2<BF> dx[RT / 2];
+            {
+                Frag2<BF> qt[KT][RT / 2], dq[RT / 2];
 #pragma unroll
-            for (int u = 0; u < RT / 2; ++u) {
-                f32x4 a[2], d[2];
+                for (int ct = 0; ct < KT; ++ct)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int rt = 2 * u + h;
-                    const f32x4 e = load_f4(eG + 16 * rt + 4 * q4), v = frag_f32<BF>(vf[rt]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        a[h][j] = p.scale * e[j] * v[j];
-                        d[h][j] = -e[j] * x[rt][j];
-                    }
-                }
-                dq[u] = {frag_from_acc<BF>(a[0]), frag_from_acc<BF>(a[1])};
-                dx[u] = {frag_from_acc<BF>(d[0]), frag_from_acc<BF>(d[1])};
-            }
-#pragma unroll
-            for (int ct = 0; ct < KT; ++ct) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) S[ct][j] *= eC;
+                    for (int u = 0; u < RT / 2; ++u) qt[ct][u] = col_frag<BF, L::RB>(Q, ct, u, l16, q4);
 #pragma unroll
                 for (int u = 0; u < RT / 2; ++u) {
-                    mma<BF>(S[ct], col_frag<BF, L::RB>(Q, ct, u, l16, q4), dq[u]);
-                    mma<BF>(S[ct], col_frag<BF, L::RB>(K, ct, u, l16, q4), dx[u]);
+                    f32x4 a[2], d[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int rt = 2 * u + h;
+                        const f32x4 e = eG(rt);
+                        a[h] = frag_f32<BF>(vf[rt]) * e * p.scale;
+                        d[h] = -x[rt] * e;
+                    }
+                    dq[u] = {frag_from_acc<BF>(a[0]), frag_from_acc<BF>(a[1])};
+                    dx[u] = {frag_from_acc<BF>(d[0]), frag_from_acc<BF>(d[1])};
                 }
+                issue_loads<BF>();
+#pragma unroll
+                for (int ct = 0; ct < KT; ++ct) S[ct] = S[ct] * eC;
+#pragma unroll
+                for (int u = 0; u < RT / 2; ++u)
+#pragma unroll
+                    for (int ct = 0; ct < KT; ++ct) mma<BF>(S[ct], qt[ct][u], dq[u]);
             }
+            Frag2<BF> kt[KT][RT / 2];
+#pragma unroll
+            for (int ct = 0; ct < KT; ++ct)
+#pragma unroll
+                for (int u = 0; u < RT / 2; ++u) kt[ct][u] = col_frag<BF, L::RB>(K, ct, u, l16, q4);
+            __syncthreads();  // A
+#pragma unroll
+            for (int u = 0; u < RT / 2; ++u)
+#pragma unroll
+                for (int ct = 0; ct < KT; ++ct) mma<BF>(S[ct], kt[ct][u], dx[u]);
             put_value_rows<BF, L::VRB, RT>(V, static_cast<IO *>(p.out) + (tok * p.Hv + w.h) * p.dv + w.col0,
                                            (int64_t)p.Hv * p.dv, wave, x, clen, lane);
         }
