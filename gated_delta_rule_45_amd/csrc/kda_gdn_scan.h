@@ -21,13 +21,13 @@
 //
 // One workgroup owns (sequence, value head, CT state columns); groups of waves run side by side, up to
 // two chunks apart, with two barriers per chunk:
-//   copy wave    global -> LDS loads of chunk s + 2, no registers in between;
-//   tile waves   chunk s + 1: K K^T and Q K^T (lower 16 x 16 tiles), the decays, then the inverse
-//                of every 32 x 32 diagonal block of I + M B (two 16 x 16 blocks by substitution,
-//                joined by two fp32 matrix products), and the gates of chunk s + 2;
-//   chain waves  chunk s: 16 state columns each, the fp32 state in accumulator registers;
-//   output waves chunk s (forward): O from the state and Y that the chain wave of the same columns
-//                hands over in LDS.
+//   copy wave     global -> LDS loads of chunk s + 2, no registers in between;
+//   block waves   chunk s + 1: the lower 16 x 16 tiles of K K^T and Q K^T with their decays, the inverse
+//                 of every 32 x 32 diagonal block of I + M B (two 16 x 16 blocks by substitution, joined
+//                 by two fp32 matrix products), and the gates of chunk s + 2;
+//   chain waves   chunk s: 16 state columns each, the fp32 state in accumulator registers;
+//   output        chunk s (forward): O from the state and Y that the chain wave of the same columns hands
+//                 over in LDS at the step's middle barrier, by the waves that made Q K^T before it.
 // The 64-token inverse is never formed: the second 32 tokens are solved after the first ones'
 // result is subtracted (one more product on the chain, but two levels of block products and their
 // roundings less per chunk).
@@ -146,10 +146,12 @@ struct Lds {
     static constexpr int E = BF ? 2 : 4;
     static constexpr int C = BF ? kChunkBf16 : kChunkF32;
     static constexpr int RT = C / 16, NBLK = C / 32;
-    // waves: chain, output (forward), tile and copy waves
-    static constexpr int NCW = CT / 16, NOW = MODE == kFwd ? NCW : 0;
-    static constexpr int NTW = NBLK == 1 ? 2 : 3;
-    static constexpr int OW0 = NCW, TW0 = OW0 + NOW, CPW = TW0 + NTW, NT = 64 * (CPW + 1);
+    // Waves (wave i runs on SIMD i % 4, so that a chain wave shares its SIMD with an output wave, whose main work
+    // falls into the other phase): 0, 1 chain; 2, 3 the diagonal blocks of K K^T and their inverses; 4, 5 the blocks
+    // of Q K^T, then the output; 6 the block below the diagonal, and the gates; 7 copies.
+    static constexpr int NCW = 2, KW0 = 2, QW0 = 4, GW = 6, CPW = 7, NT = 512;
+    static constexpr int NOW = MODE == kFwd ? NCW : 0;
+    static_assert(CT == 16 * NCW, "a chain wave owns 16 columns");
     static constexpr int RB = DK * E, VRB = CT * E, PRB = C * E, NRB = 32 * E;
     static constexpr int KB = C * RB, QB = MODE == kKeep ? 0 : KB, VB = C * VRB, SB = KB + QB + VB;
     static constexpr int NBUF = 3;
@@ -234,11 +236,11 @@ __device__ __forceinline__ void issue_loads() {
 }
 
 // A tile wave's 16 x 16 tiles of one 32 x 32 block (RB, CB) of the decayed K K^T (KK: scaled by beta into
-// M B) and of Q K^T (QK).  Forward: rows of the stored matrices are the tokens i that are solved for;
+// M B) or of Q K^T (QK), its row tiles I0 .. I1 - 1.  Forward: rows of the stored matrices are the tokens i that are solved for;
 // reverse: transposed.  Below the diagonal tiles the decays are products of three stored factors, all
 // at most 1 (row token from its tile's start, between the tiles, column token to its tile's end);
 // inside a diagonal tile they are formed from differences of the cumulative gates, kept as two floats.
-template <bool BF, int DK, int CT, int MODE, int RB, int CB, bool KK, bool QK>
+template <bool BF, int DK, int CT, int MODE, int RB, int CB, bool KK, bool QK, int I0 = 0, int I1 = 2>
 __device__ __forceinline__ void make_tiles(char *smem, int buf, int par, int abuf, float scale, int l16, int q4) {
     using L = Lds<BF, DK, CT, MODE>;
     constexpr bool REV = MODE == kRev, DIAG = RB == CB;
@@ -252,8 +254,10 @@ __device__ __forceinline__ void make_tiles(char *smem, int buf, int par, int abu
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int t = 0; t < DK / 32; ++t) {
-            if constexpr (KK || DIAG) kr[i][t] = row_frag<BF, L::RB>(K, 32 * RB + 16 * i + l16, 32 * t + 8 * q4);
-            if constexpr (QK) qr[i][t] = row_frag<BF, L::RB>(Q, 32 * RB + 16 * i + l16, 32 * t + 8 * q4);
+            if (DIAG || (KK && i >= I0 && i < I1))
+                kr[i][t] = row_frag<BF, L::RB>(K, 32 * RB + 16 * i + l16, 32 * t + 8 * q4);
+            if (QK && i >= I0 && i < I1)
+                qr[i][t] = row_frag<BF, L::RB>(Q, 32 * RB + 16 * i + l16, 32 * t + 8 * q4);
             if constexpr (!DIAG) kc[i][t] = row_frag<BF, L::RB>(K, 32 * CB + 16 * i + l16, 32 * t + 8 * q4);
         }
     // a lane's entries: forward (i, j) = (16 r + l16, 16 c + 4 q4 + e), reverse (16 r + 4 q4 + e, 16 c + l16)
@@ -266,7 +270,7 @@ __device__ __forceinline__ void make_tiles(char *smem, int buf, int par, int abu
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = 2 * RB + i, c = 2 * CB + j;
-            if (c > r) continue;
+            if (c > r || i < I0 || i >= I1) continue;
             const int own = REV ? 16 * c + l16 : 16 * r + l16, four = (REV ? 16 * r : 16 * c) + 4 * q4;
             if (c == r) {
                 const float ho = Gh[own], lo = Gl[own];
@@ -295,7 +299,7 @@ __device__ __forceinline__ void make_tiles(char *smem, int buf, int par, int abu
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (2 * CB + j > 2 * RB + i) continue;
+                if (2 * CB + j > 2 * RB + i || i < I0 || i >= I1) continue;
                 const Frag2<BF> y = DIAG ? kr[j][t] : kc[j][t];
                 if constexpr (KK) {
                     if constexpr (REV) mma<BF>(kk[i][j], kr[i][t], y);
@@ -311,7 +315,7 @@ __device__ __forceinline__ void make_tiles(char *smem, int buf, int par, int abu
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int r = 2 * RB + i, c = 2 * CB + j;
-            if (c > r) continue;
+            if (c > r || i < I0 || i >= I1) continue;
             const int own = REV ? 16 * c + l16 : 16 * r + l16, four = (REV ? 16 * r : 16 * c) + 4 * q4;
             if constexpr (KK) {
                 f32x4 m = kk[i][j] * gam[i][j] * bet[j];
@@ -397,20 +401,24 @@ __device__ __forceinline__ void solve_cols(float (&n)[16], const float (&nl)[16]
 }
 
 // The inverse of one 32 x 32 diagonal block of I + M B, minus the identity (reverse: transposed), by the wave
-// that made its tiles: two 16 x 16 diagonal blocks by forward substitution in registers (lanes of 16
+// that made its tiles, in two parts on both sides of the step's middle barrier: two 16 x 16 diagonal blocks by forward substitution in registers (lanes of 16
 // exchange values through DPP, about 8 cycles a term), and -N11 (L10 N00) below them.  Forward: a lane
 // has one row and eight columns (0-3 and 12-15, or 4-7 and 8-11); reverse: one column, half of which it
 // stores.
+struct Inverse {
+    float n[8];
+    Frag<false> l10;
+};
 template <bool BF, int DK, int CT, int MODE>
-__device__ __forceinline__ void invert_block(char *smem, int blk, int par, int lane) {
+__device__ __forceinline__ void solve_diagonals(Inverse &inv, char *smem, int blk, int lane) {
     using L = Lds<BF, DK, CT, MODE>;
     constexpr bool REV = MODE == kRev;
     const int l16 = lane & 15, q4 = lane >> 4, sub = q4 & 1, half = q4 >> 1;
     const int c0 = half ? 4 : 0, c1 = half ? 8 : 12;
     float *Lb = reinterpret_cast<float *>(smem + L::F0) + blk * 32 * L::LS;
-    char *N = smem + L::N0 + (par * L::NBLK + blk) * L::NB;
     const float *Ld = Lb + (16 * sub + l16) * L::LS + 16 * sub;
-    float nl[16], n[8];
+    float nl[16];
+    auto &n = inv.n;
     wave_lds_sync();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -418,8 +426,7 @@ __device__ __forceinline__ void invert_block(char *smem, int blk, int par, int l
 #pragma unroll
         for (int j = 0; j < 4; ++j) nl[4 * i + j] = -v[j];
     }
-    Frag<false> l10;
-    l10.v = *reinterpret_cast<const float4 *>(Lb + (16 + l16) * L::LS + 4 * q4);
+    inv.l10.v = *reinterpret_cast<const float4 *>(Lb + (16 + l16) * L::LS + 4 * q4);
     if constexpr (REV) {
         float x[16];
 #pragma unroll
@@ -445,6 +452,16 @@ __device__ __forceinline__ void invert_block(char *smem, int blk, int par, int l
     *reinterpret_cast<float4 *>(dst + c0) = make_float4(n[0], n[1], n[2], n[3]);
     *reinterpret_cast<float4 *>(dst + c1) = make_float4(n[4], n[5], n[6], n[7]);
     wave_lds_sync();
+}
+template <bool BF, int DK, int CT, int MODE>
+__device__ __forceinline__ void join_inverse(const Inverse &inv, char *smem, int blk, int par, int lane) {
+    using L = Lds<BF, DK, CT, MODE>;
+    constexpr bool REV = MODE == kRev;
+    const int l16 = lane & 15, q4 = lane >> 4, sub = q4 & 1, half = q4 >> 1;
+    const int c0 = half ? 4 : 0, c1 = half ? 8 : 12;
+    const float *Lb = reinterpret_cast<const float *>(smem + L::F0) + blk * 32 * L::LS;
+    char *N = smem + L::N0 + (par * L::NBLK + blk) * L::NB;
+    const auto &n = inv.n;
     // forward: T = L10 N00, then N10 = -N11 T with rows of N11 as A; its transpose (the operands exchanged) puts
     // four columns of a row of N10 in a lane.  Reverse: the stored rows are columns of the inverses.
     const float *s00 = Lb + 16, *s11 = Lb;
@@ -459,6 +476,7 @@ __device__ __forceinline__ void invert_block(char *smem, int blk, int par, int l
         n11.v = *reinterpret_cast<const float4 *>(s11 + l16 * L::LS + 4 * q4);
     }
     issue_loads<BF>();
+    const f32x4 t = product16(inv.l10, n00);
     float y[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -467,7 +485,6 @@ __device__ __forceinline__ void invert_block(char *smem, int blk, int par, int l
     }
     row_put4<BF, L::NRB>(N, 16 * sub + l16, kpos(16 * sub + c0), y[0], y[1], y[2], y[3]);
     row_put4<BF, L::NRB>(N, 16 * sub + l16, kpos(16 * sub + c1), y[4], y[5], y[6], y[7]);
-    const f32x4 t = product16(l10, n00);
     const Frag<false> mt = frag_from_acc<false>(t, -1.f);
     // reverse: N10[4 q4 + j][l16], forward: N10^T[4 q4 + j][l16]
     const f32x4 n10 = REV ? product16(n11, mt) : product16(mt, n11);
@@ -528,36 +545,77 @@ __device__ __forceinline__ GateScan gate_scan(float g) {
 // A chunk's gate factors (all at most 1 for g <= 0), lane = token: up = e^{G - G(end of the previous 16
 // tokens)}, down = e^{G(end of its 16 tokens) - G}, beta; then per block e^{G} of its start and
 // e^{G_C - G} of its end, the decays between non-neighbouring blocks (2,0), (3,1), (3,0), and e^{G_C}.
-template <bool BF, int DK, int CT, int MODE>
-__device__ __forceinline__ void put_gates(char *smem, int abuf, const RawGate &r, int lane) {
-    using L = Lds<BF, DK, CT, MODE>;
+struct Gates {
+    float up, down, beta, hi, lo, f[6];  // f: block start and end, (2,0), (3,1), (3,0), whole chunk
+};
+template <int C>
+__device__ __forceinline__ Gates make_gates(const RawGate &r, int lane) {
     const GateScan sc = gate_scan(r.g);
     const int blk = lane >> 4;
     const double start = blk == 0 ? 0.0 : blk == 1 ? sc.end[1] : blk == 2 ? sc.end[2] : sc.end[3];
     const double own_end = blk == 0 ? sc.end[1] : blk == 1 ? sc.end[2] : blk == 2 ? sc.end[3] : sc.end[4];
-    const double end = sc.end[L::C / 16], s = sc.s + start;
-    float *a = reinterpret_cast<float *>(smem + L::A0 + abuf * L::AB);
+    const double end = sc.end[C / 16];
+    Gates g;
+    g.hi = (float)sc.s;
+    g.lo = (float)(sc.s - g.hi);
+    g.up = fast_exp2(g.hi);
+    g.down = fast_exp2((float)(own_end - start - sc.s));
+    g.beta = r.b;
+    g.f[0] = fast_exp2((float)start);
+    g.f[1] = fast_exp2((float)(end - own_end));
+    g.f[2] = fast_exp2((float)(sc.end[2] - sc.end[1]));
+    g.f[3] = fast_exp2((float)(sc.end[3] - sc.end[2]));
+    g.f[4] = fast_exp2((float)(sc.end[3] - sc.end[1]));
+    g.f[5] = fast_exp2((float)end);
+    return g;
+}
+template <bool BF, int DK, int CT, int MODE>
+__device__ __forceinline__ void put_gates(char *smem, int abuf, const Gates &g, int lane) {
+    using L = Lds<BF, DK, CT, MODE>;
+    float *a = reinterpret_cast<float *>(smem + L::A0 + abuf * L::AB), *G = reinterpret_cast<float *>(smem + L::G0);
     if (lane < L::C) {
-        float *G = reinterpret_cast<float *>(smem + L::G0);
-        const float hi = (float)sc.s;
-        G[lane] = hi;
-        G[L::C + lane] = (float)(sc.s - hi);
-        a[lane] = fast_exp2((float)sc.s);
-        a[L::C + lane] = fast_exp2((float)(own_end - s));
-        a[2 * L::C + lane] = r.b;
+        G[lane] = g.hi;
+        G[L::C + lane] = g.lo;
+        a[lane] = g.up;
+        a[L::C + lane] = g.down;
+        a[2 * L::C + lane] = g.beta;
         float *f = a + 3 * L::C;
         if ((lane & 15) == 0) {
-            f[lane >> 4] = fast_exp2((float)start);
-            f[4 + (lane >> 4)] = fast_exp2((float)(end - own_end));
+            f[lane >> 4] = g.f[0];
+            f[4 + (lane >> 4)] = g.f[1];
         }
         if (lane == 0) {
-            f[8] = fast_exp2((float)(sc.end[2] - sc.end[1]));
-            f[9] = fast_exp2((float)(sc.end[3] - sc.end[2]));
-            f[10] = fast_exp2((float)(sc.end[3] - sc.end[1]));
-            f[11] = fast_exp2((float)end);
+#pragma unroll
+            for (int i = 2; i < 6; ++i) f[6 + i] = g.f[i];
         }
     }
 }
+
+// The gates of the chunks to come: in the second phase of step s those of chunk s + 2, made a step before, are
+// stored (in the first phase the tile waves read the cumulative gates of chunk s + 1) and those of
+// chunk s + 3 made.
+template <bool BF, int DK, int CT, int MODE>
+struct GateMaker {
+    using L = Lds<BF, DK, CT, MODE>;
+    const GdnParams &p;
+    const Walk &w;
+    char *smem;
+    int lane;
+    RawGate raw{0.f, 0.f};
+    Gates g{};
+    __device__ __forceinline__ int chunk(int s) const { return MODE == kRev ? w.nch - 1 - s : s; }
+    __device__ __forceinline__ void load(int s) {
+        if (s < w.nch) raw = load_gate<L::C>(p, w, chunk(s), lane);
+    }
+    __device__ __forceinline__ void make(int s) {  // chunk s, whose raw gates have been loaded
+        if (s < w.nch) g = make_gates<L::C>(raw, lane);
+        load(s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __device__ __forceinline__ void put(int s) {
+        if (s < w.nch) put_gates<BF, DK, CT, MODE>(smem, s % 3, g, lane);
+    }
+};
 
 // One operand fragment pair per lane, handed from wave to wave.
 template <bool BF>
@@ -659,67 +717,38 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         }
         return;
     }
-    if (wave >= L::TW0) {
-        // ------------------------------------------------------------------ tile waves
+#define GDN_TILES(...) \
+    make_tiles<BF, DK, CT, MODE, __VA_ARGS__>(smem, s % L::NBUF, s & 1, s % 3, p.scale, l16, q4)
+    if (wave >= L::QW0 && wave < L::QW0 + 2) {
+        // ------------------------------------------------------------------ Q K^T and output waves
         if (nch == 0) return;
-        const int pw = wave - L::TW0;
-        constexpr int GW = L::NTW - 1;  // also makes the gates; the waves of the diagonal blocks their inverses
-        RawGate raw{0.f, 0.f};
-        if (pw == GW) {
-            raw = load_gate<C>(p, w, ci(0), lane);
-            put_gates<BF, DK, CT, MODE>(smem, 0, raw, lane);
-            if (nch > 1) raw = load_gate<C>(p, w, ci(1), lane);
-        }
+        const int cw = wave - L::QW0;
         auto tiles = [&](int s) {
-            const int buf = s % L::NBUF, par = s & 1, ab = s % 3;
-            constexpr bool HASQ = MODE != kKeep;
-#define GDN_TILES(RB_, CB_, KK_, QK_) make_tiles<BF, DK, CT, MODE, RB_, CB_, KK_, QK_>(smem, buf, par, ab, p.scale, l16, q4)
-            if constexpr (L::NBLK == 2) {
-                if (pw == 0) GDN_TILES(0, 0, true, HASQ);
-                if (pw == 1) GDN_TILES(1, 1, true, HASQ);
-                if (pw == 2) GDN_TILES(1, 0, true, HASQ);
-            } else {
-                if (pw == 0) GDN_TILES(0, 0, true, false);
-                if (HASQ && pw == 1) GDN_TILES(0, 0, false, HASQ);
-            }
-#undef GDN_TILES
-        };
-        auto finish = [&](int s) {  // the inverse of chunk s, the gates of chunk s + 1
-            if (pw < L::NBLK) invert_block<BF, DK, CT, MODE>(smem, pw, s & 1, lane);
-            if (pw == GW && s + 1 < nch) {
-                put_gates<BF, DK, CT, MODE>(smem, (s + 1) % 3, raw, lane);
-                if (s + 2 < nch) raw = load_gate<C>(p, w, ci(s + 2), lane);
+            if constexpr (MODE != kKeep) {
+                if (cw == 0) GDN_TILES(0, 0, false, true);
+                if constexpr (L::NBLK == 2) {
+                    if (cw == 0) GDN_TILES(1, 0, false, true, 0, 1);
+                    if (cw == 1) {
+                        GDN_TILES(1, 1, false, true);
+                        GDN_TILES(1, 0, false, true, 1, 2);
+                    }
+                }
             }
         };
         __syncthreads();
         tiles(0);
         __syncthreads();
-        finish(0);
-        __syncthreads();
-        for (int s = 0; s < nch; ++s) {
-            if (s + 1 < nch) tiles(s + 1);
-            __syncthreads();  // A
-            if (s + 1 < nch) finish(s + 1);
-            __syncthreads();  // B
-        }
-        return;
-    }
-
-    if (MODE == kFwd && wave >= L::OW0) {
-        // ------------------------------------------------------------------ output waves
-        if (nch == 0) return;
-        const int cw = wave - L::OW0;
-        const char *hand = smem + L::H0 + cw * L::HB;
-        __syncthreads();
-        __syncthreads();
         __syncthreads();
 #pragma unroll 1
         for (int s = 0; s < nch; ++s) {
+            if (s + 1 < nch) tiles(s + 1);
+            __syncthreads();  // A
+            if constexpr (MODE == kFwd) {
             const int clen = min(C, w.len - s * C);
+            const char *hand = smem + L::H0 + cw * L::HB;
             const char *Q = smem + (s % L::NBUF) * L::SB + L::KB, *P = smem + L::P0 + (s & 1) * L::PB;
             const float *gate = reinterpret_cast<const float *>(smem + L::A0 + (s % 3) * L::AB);
             IO *out = static_cast<IO *>(p.out) + ((w.tok0 + (int64_t)s * C) * p.Hv + w.h) * p.dv + w.col0 + 16 * cw + 4 * q4;
-            __syncthreads();  // A
             Frag2<BF> qf[RT][K2], pf[RT][RT / 2];
             float e[RT];
 #pragma unroll
@@ -758,12 +787,71 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
                     IoTraits<IO>::store4(out + (int64_t)(16 * rt + l16) * p.Hv * p.dv,
                                          make_float4(o[rt][0] * p.scale, o[rt][1] * p.scale, o[rt][2] * p.scale,
                                                      o[rt][3] * p.scale));
+            }
             __syncthreads();  // B
         }
         return;
     }
+    if (wave == L::GW) {
+        // ------------------------------------------------------------------ block below the diagonal, gates
+        if (nch == 0) return;
+        GateMaker<BF, DK, CT, MODE> gm{p, w, smem, lane};
+        gm.load(0);
+        gm.make(0);
+        gm.put(0);
+        gm.make(1);
+        auto tiles = [&](int s) {
+            if constexpr (L::NBLK == 2) GDN_TILES(1, 0, true, false);
+        };
+        __syncthreads();
+        tiles(0);
+        __syncthreads();
+        gm.put(1);
+        gm.make(2);
+        __syncthreads();
+#pragma unroll 1
+        for (int s = 0; s < nch; ++s) {
+            if (s + 1 < nch) tiles(s + 1);
+            __syncthreads();  // A
+            gm.put(s + 2);
+            gm.make(s + 3);
+            __syncthreads();  // B
+        }
+        return;
+    }
+    if (wave >= L::KW0) {
+        // ------------------------------------------------------------------ diagonal blocks and their inverses
+        if (nch == 0) return;
+        const int blk = wave - L::KW0;
+        Inverse inv;
+        auto tiles = [&](int s) {
+            if (blk == 0) GDN_TILES(0, 0, true, false);
+            if constexpr (L::NBLK == 2) {
+                if (blk == 1) GDN_TILES(1, 1, true, false);
+            }
+            if (blk < L::NBLK) solve_diagonals<BF, DK, CT, MODE>(inv, smem, blk, lane);
+        };
+        auto join = [&](int s) {
+            if (blk < L::NBLK) join_inverse<BF, DK, CT, MODE>(inv, smem, blk, s & 1, lane);
+        };
+        __syncthreads();
+        tiles(0);
+        __syncthreads();
+        join(0);
+        __syncthreads();
+#pragma unroll 1
+        for (int s = 0; s < nch; ++s) {
+            if (s + 1 < nch) tiles(s + 1);
+            __syncthreads();  // A
+            if (s + 1 < nch) join(s + 1);
+            __syncthreads();  // B
+        }
+        return;
+    }
+#undef GDN_TILES
 
     // ------------------------------------------------------------------ chain waves
+    __builtin_amdgcn_s_setprio(2);  // the chain is what every other wave waits for
     const int col = w.col0 + 16 * wave + l16;
     const int64_t sbase = ((int64_t)w.n * p.Hv + w.h) * DK * p.dv + col;
     f32x4 S[KT];
@@ -781,6 +869,21 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         __syncthreads();
         __syncthreads();
     }
+    // K's and the values' fragments of a chunk are read before the barrier that opens its step: they have been in
+    // LDS for a step by then
+    Frag2<BF> kf[RT][K2];
+    Frag<BF> vf[RT];
+    auto fetch = [&](int s) {
+        const char *K = smem + (s % L::NBUF) * L::SB, *V = K + L::KB + L::QB;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+            for (int t = 0; t < K2; ++t) kf[rt][t] = row_frag<BF, L::RB>(K, 16 * rt + l16, 32 * t + 8 * q4);
+            vf[rt] = value_frag<BF, L::VRB>(V, wave, rt, l16, q4);
+        }
+    };
+    // (not in reverse, which has no registers left for them)
+    if (!REV && nch > 0) fetch(0);
 #pragma unroll 1
     for (int s = 0; s < nch; ++s) {
         const int c = ci(s), clen = min(C, w.len - c * C);
@@ -815,23 +918,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
             }
         }
         f32x4 x[RT];
-        Frag<BF> vf[RT];
-        {
-            Frag2<BF> kf[RT][K2];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int t = 0; t < K2; ++t) kf[rt][t] = row_frag<BF, L::RB>(K, 16 * rt + l16, 32 * t + 8 * q4);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) vf[rt] = value_frag<BF, L::VRB>(V, wave, rt, l16, q4);
-            issue_loads<BF>();
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) x[rt] = zero4();
-#pragma unroll
-            for (int t = 0; t < K2; ++t)
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) mma<BF>(x[rt], kf[rt][t], Sb[t]);
-        }
+        if constexpr (REV) fetch(s);
         // the inverse blocks and M B between them
         Frag2<BF> nf[L::NBLK][2], lf[2];
 #pragma unroll
@@ -840,7 +927,13 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
             for (int b = 0; b < L::NBLK; ++b) nf[b][h] = row_frag<BF, L::NRB>(N + b * L::NB, 16 * h + l16, 8 * q4);
             if constexpr (L::NBLK > 1) lf[h] = row_frag<BF, L::NRB>(Lba, 16 * h + l16, 8 * q4);
         }
-
+        issue_loads<BF>();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) x[rt] = zero4();
+#pragma unroll
+        for (int t = 0; t < K2; ++t)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) mma<BF>(x[rt], kf[rt][t], Sb[t]);
         if constexpr (!REV) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -878,6 +971,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
                     hand_put<BF>(hand + L::HS, u, lane, Frag2<BF>{frag_from_acc<BF>(a[0]), frag_from_acc<BF>(a[1])});
                 ys[u] = {frag_from_acc<BF>(d[0]), frag_from_acc<BF>(d[1])};
             }
+            issue_loads<BF>();
             Frag2<BF> kt[KT][RT / 2];
 #pragma unroll
             for (int ct = 0; ct < KT; ++ct)
@@ -940,6 +1034,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
             }
             Frag2<BF> dx[RT / 2];
             {
+                issue_loads<BF>();
                 Frag2<BF> qt[KT][RT / 2], dq[RT / 2];
 #pragma unroll
                 for (int ct = 0; ct < KT; ++ct)
@@ -966,6 +1061,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
 #pragma unroll
                     for (int ct = 0; ct < KT; ++ct) mma<BF>(S[ct], qt[ct][u], dq[u]);
             }
+            issue_loads<BF>();
             Frag2<BF> kt[KT][RT / 2];
 #pragma unroll
             for (int ct = 0; ct < KT; ++ct)
@@ -981,14 +1077,19 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         }
 #pragma unroll
         for (int ct = 0; ct < KT; ct += 2) mfma_settle(S[ct], S[ct + 1]);
+        issue_loads<BF>();
+        if (!REV && s + 1 < nch) fetch(s + 1);
         __syncthreads();  // B
     }
     if (p.sf) {
+        // formed anew: otherwise the 64-bit addresses of the first loads stay in registers over the whole walk
+        int q4b = q4;
+        asm volatile("" : "+v"(q4b));
 #pragma unroll
         for (int ct = 0; ct < KT; ++ct)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int64_t at = sbase + (int64_t)state_channel(ct, q4, j) * p.dv;
+                const int64_t at = sbase + (int64_t)state_channel(ct, q4b, j) * p.dv;
                 if (p.state_bf16) static_cast<uint16_t *>(p.sf)[at] = f32_to_bf16(S[ct][j]);
                 else static_cast<float *>(p.sf)[at] = S[ct][j];
             }
