@@ -13,8 +13,8 @@ Entry points (same names as the C ABI):
 * ``recurrent_fwd`` -- token-by-token reference mode on the GPU (same arguments)
 * ``decode_step``   -- one token per sequence, state updated in place
 * ``query``         -- launch configuration, algorithmic flops/bytes, device info
-* ``gdn_chunk_fwd``, ``gdn_decode`` -- the delta rule with one log-gate per head and grouped heads:
-                       prefill, and new tokens on a pool of state slots (``gdn.py``)
+* ``gdn_chunk_fwd``, ``gdn_chunk_bwd``, ``gdn_decode`` -- the delta rule with one log-gate per head and
+                       grouped heads: prefill, gradients, and new tokens on a pool of state slots (``gdn.py``)
 * ``norm_gate_bwd`` -- gradients of the output epilogue
 """
 from __future__ import annotations
@@ -26,7 +26,7 @@ from typing import Optional, Tuple
 import torch
 
 __all__ = ["chunk_fwd", "chunk_fwd_prologue", "chunk_fwd_noalloc", "noalloc_scratch_bytes", "chunk_bwd", "dplr_chunk_fwd", "recurrent_fwd", "decode_step", "decode_step_gated", "prologue", "norm_gate", "query", "tune", "KdaError",
-           "LIB_PATH", "library", "gdn_chunk_fwd", "gdn_decode", "norm_gate_bwd"]
+           "LIB_PATH", "library", "gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode", "norm_gate_bwd"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
@@ -643,4 +643,4 @@ def query(batch: int, seq_len: int, num_heads: int, head_dim_k: int, head_dim_v:
 
 
 from . import gdn  # noqa: E402  (it uses the helpers above)
-from .gdn import gdn_chunk_fwd, gdn_decode, norm_gate_bwd  # noqa: E402
+from .gdn import gdn_chunk_bwd, gdn_chunk_fwd, gdn_decode, norm_gate_bwd  # noqa: E402

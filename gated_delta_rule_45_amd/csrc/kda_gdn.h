@@ -41,6 +41,17 @@ struct GdnParams {
 hipError_t launch_scan_bf16(int mode, int cols, const GdnParams &p, hipStream_t stream);
 hipError_t launch_scan_f32(int mode, int cols, const GdnParams &p, hipStream_t stream);
 
+// Gradients inside the chunks, after a keeping forward and a reverse scan.
+struct GradParams {
+    GdnParams f;                       // q, k, g, beta, cu, sizes; v = d_out (dense)
+    const void *hs, *dhs, *zs, *dx;    // what the scans left: S, dS [slots, Hv, dv, d_k], Z, dX [tokens, Hv, dv]
+    void *dq, *dk;                     // [tokens, Hk, d_k] dense
+    void *dg, *dbeta;                  // [tokens, Hv] gate type
+    int64_t slots;
+};
+hipError_t launch_grad_bf16(const GradParams &p, hipStream_t stream);
+hipError_t launch_grad_f32(const GradParams &p, hipStream_t stream);
+
 struct DecodeParams {
     const void *q, *k, *v;    // as above
     const void *g, *beta;

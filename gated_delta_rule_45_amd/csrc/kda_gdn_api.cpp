@@ -172,6 +172,24 @@ hipError_t launch_scan(const kda_gdn_problem_t *p, int mode, int cols, const kda
     return p->io_dtype == KDA_BF16 ? kda::gdn::launch_scan_bf16(mode, cols, r, s) : kda::gdn::launch_scan_f32(mode, cols, r, s);
 }
 
+// Workspace of the backward: S and dS per chunk slot, Z per token.
+struct BwdLayout {
+    int64_t slots = 0;
+    size_t dhs = 0, zs = 0, bytes = 0;
+};
+kda_status_t bwd_layout(const kda_gdn_problem_t *p, const Shape &s, bool packed, BwdLayout &b) {
+    const int64_t C = kda::gdn::chunk_of(p->io_dtype), per = (int64_t)p->seq_len / C;
+    b.slots = packed ? per + s.num_seqs : (int64_t)s.num_seqs * (per + (p->seq_len % C != 0));
+    const int64_t row = s.v_row * s.io;
+    if (b.slots > 0x7fffffffLL / p->num_heads_k || b.slots > (1LL << 60) / (row * p->head_dim_k))
+        return set_error(KDA_ERR_UNSUPPORTED, "too many chunks");
+    auto align = [](int64_t x) { return (size_t)((x + 255) / 256 * 256); };
+    b.dhs = align(b.slots * row * p->head_dim_k);
+    b.zs = 2 * b.dhs;
+    b.bytes = b.zs + align(s.tokens * row);
+    return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -205,6 +223,95 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
         if (s.num_seqs == 0 || (s.tokens == 0 && !final_state)) return done(hipSuccess, "");
         return done(launch_scan(problem, 0, scan_cols(problem, s, current_cus()), r, static_cast<hipStream_t>(stream)),
                     "kda_gdn_chunk_fwd launch");
+    } catch (...) {
+        return KDA_ERR_HIP;
+    }
+}
+
+kda_status_t kda_gdn_chunk_bwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes) {
+    if (!bytes) return set_error(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    *bytes = 0;
+    Shape s;
+    const bool packed = problem && problem->num_seqs > 0;
+    kda_status_t st = check_shape(problem, packed, s);
+    BwdLayout b;
+    if (st == KDA_OK) st = bwd_layout(problem, s, packed, b);
+    if (st != KDA_OK) return st;
+    *bytes = b.bytes;
+    return done(hipSuccess, "");
+}
+
+kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,
+                               const void *g, const void *beta, const void *initial_state, const int32_t *cu_seqlens,
+                               const int32_t *cu_seqlens_host, const void *d_out, const void *d_final_state, void *dq,
+                               void *dk, void *dv, void *dg, void *dbeta, void *d_initial_state, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+    try {
+        Shape s;
+        kda_status_t st = check_shape(problem, cu_seqlens != nullptr, s);
+        if (st != KDA_OK) return st;
+        BwdLayout b;
+        st = bwd_layout(problem, s, cu_seqlens != nullptr, b);
+        if (st != KDA_OK) return st;
+        const int64_t gates = s.tokens * problem->num_heads_v * s.gate, qk = s.tokens * s.qk_row * s.io,
+                      vo = s.tokens * s.v_row * s.io, states = s.states * s.state;
+        const Arg args[] = {
+            {"q", q, s.span(s.ldq, s.qk_row), 16, true, false},
+            {"k", k, s.span(s.ldk, s.qk_row), 16, true, false},
+            {"v", v, s.span(s.ldv, s.v_row), 16, true, false},
+            {"g", g, gates, (size_t)s.gate, true, false},
+            {"beta", beta, gates, (size_t)s.gate, true, false},
+            {"initial_state", initial_state, states, 16, false, false},
+            {"d_out", d_out, vo, 16, true, false},
+            {"d_final_state", d_final_state, states, 16, false, false},
+            {"cu_seqlens", cu_seqlens, ((int64_t)s.num_seqs + 1) * 4, 4, false, false},
+            {"dq", dq, qk, 16, true, true},
+            {"dk", dk, qk, 16, true, true},
+            {"dv", dv, vo, 16, true, true},
+            {"dg", dg, gates, (size_t)s.gate, true, true},
+            {"dbeta", dbeta, gates, (size_t)s.gate, true, true},
+            {"d_initial_state", d_initial_state, states, 16, false, true},
+            {"workspace", workspace, (int64_t)b.bytes, 256, false, true},
+        };
+        st = check_args(args);
+        if (st == KDA_OK) st = check_offsets(problem, s, cu_seqlens, cu_seqlens_host);
+        if (st != KDA_OK) return st;
+        if (b.bytes > 0 && (!workspace || workspace_bytes < b.bytes))
+            return set_error(KDA_ERR_WORKSPACE, "kda_gdn_chunk_bwd needs a 256-byte aligned workspace of %zu bytes (got %zu at %p)",
+                             b.bytes, workspace_bytes, workspace);
+        if (s.num_seqs == 0 || (s.tokens == 0 && !d_initial_state)) return done(hipSuccess, "");
+        hipStream_t hs = static_cast<hipStream_t>(stream);
+        char *ws = static_cast<char *>(workspace);
+        const int cols = scan_cols(problem, s, current_cus());
+        kda::gdn::GdnParams keep = params_of(problem, s, q, k, v, g, beta, cu_seqlens);
+        keep.s0 = initial_state;
+        keep.hs = ws;
+        keep.zs = ws + b.zs;
+        kda::gdn::GdnParams rev = params_of(problem, s, q, k, d_out, g, beta, cu_seqlens);
+        rev.ldv = s.v_row;
+        rev.s0 = d_final_state;
+        rev.sf = d_initial_state;
+        rev.out = dv;
+        rev.hs = ws + b.dhs;
+        kda::gdn::GradParams grad{};
+        grad.f = rev;
+        grad.hs = keep.hs;
+        grad.dhs = rev.hs;
+        grad.zs = keep.zs;
+        grad.dx = dv;
+        grad.dq = dq;
+        grad.dk = dk;
+        grad.dg = dg;
+        grad.dbeta = dbeta;
+        grad.slots = b.slots;
+        if (s.tokens > 0) {
+            st = done(launch_scan(problem, 1, cols, keep, hs), "kda_gdn_chunk_bwd forward launch");
+            if (st != KDA_OK) return st;
+        }
+        st = done(launch_scan(problem, 2, cols, rev, hs), "kda_gdn_chunk_bwd reverse launch");
+        if (st != KDA_OK || s.tokens == 0) return st;
+        return done(problem->io_dtype == KDA_BF16 ? kda::gdn::launch_grad_bf16(grad, hs) : kda::gdn::launch_grad_f32(grad, hs),
+                    "kda_gdn_chunk_bwd gradient launch");
     } catch (...) {
         return KDA_ERR_HIP;
     }

@@ -1,0 +1,469 @@
+// Gated delta rule with one log-gate per token and value head: the gradients of a chunk, once the
+// reverse scan has left dX (= dV) and the gradient dS of the state leaving every chunk, and the keeping
+// forward the state S entering it and Z (notation of kda_gdn_scan.h).  Per chunk and value head, with
+// W1 = dO Z^T, W2 = dX Z^T, E = scale W1 B o Gam (i >= j), F = -W2 B o Gam (i > j):
+//
+//     dQ = scale Diag(e^G) dO S^T + E K
+//     dK = -Diag(e^G) dX S^T + Diag(beta e^{G_C - G}) Z dS^T + E^T Q + (F + F^T) K
+//     t_ij = Gam_ij (scale (Q K^T)_ij W1_ij - (K K^T)_ij W2_ij),   x_i = e^{G_C - G_i} k_i . (dS Z_i)
+//     dbeta_j = sum_{i > j} t_ij + scale (q_j . k_j) W1_jj + x_j
+//     dG_i = sum_{j < i} beta_j t_ij - beta_i sum_{j > i} t_ji + q_i . dQ(state part)_i + k_i . dK(S part)_i - beta_i x_i
+//     dG_C += sum_i beta_i x_i + e^{G_C} <S, dS>,   dg = reverse cumulative sum of dG over the chunk
+//
+// No division (beta = 0 is exact), and the diagonal, where the gate cancels, is left out of dG rather than
+// added and subtracted.
+//
+// One workgroup owns (chunk, key head) and walks the value heads that share it, so that dQ and dK are
+// summed over them in registers, in a fixed order.  Wave r owns the 16 tokens of row tile r: its dO, dX,
+// and Z rows are operand fragments read straight from memory, dQ^T and dK^T stay in accumulators
+// (lane = token, so the gates are lane scalars and 8 consecutive channels leave as 16 bytes).  S, dS,
+// then Z with E and F + F^T take turns in one 32 KB LDS buffer beside K and Q: 67 KB, two workgroups per
+// CU, one's loads behind the other's products.  Bound: HBM (reads 9 and writes 2 tensors' rows per chunk).
+#pragma once
+
+#include "kda_gdn_scan.h"
+
+namespace kda {
+namespace gdn {
+
+// As col_frag, the contraction over 8 consecutive rows per lane: 32 u + 8 q4 ..
+template <bool BF, int RB>
+__device__ __forceinline__ Frag2<BF> col_frag8(const char *base, int ct, int u, int l16, int q4) {
+    Frag2<BF> f;
+    if constexpr (BF) {
+        const int byte = 16 * (4 * (ct >> 1) + (l16 & 3)) + 8 * (ct & 1);
+        const int r0 = 32 * u + 8 * q4 + (l16 >> 2);
+        f.a = read_tr4x16(base + row_off<RB>(r0, byte));
+        f.b = read_tr4x16(base + row_off<RB>(r0 + 4, byte));
+    } else {
+        const int byte = 4 * state_channel(ct, l16 >> 2, l16 & 3);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const float *>(base + row_off<RB>(32 * u + 8 * q4 + j, byte));
+        f.a = make_frag<BF>(x[0], x[1], x[2], x[3]);
+        f.b = make_frag<BF>(x[4], x[5], x[6], x[7]);
+    }
+    return f;
+}
+// Column 16 c + l16 of a stored [rows][cols] matrix, rows 32 u + 8 q4 ..
+template <bool BF, int RB>
+__device__ __forceinline__ Frag2<BF> plain_col_frag8(const char *base, int c, int u, int l16, int q4) {
+    Frag2<BF> f;
+    const int r0 = 32 * u + 8 * q4;
+    if constexpr (BF) {
+        const int byte = 2 * (16 * c + 4 * (l16 & 3));
+        f.a = read_tr4x16(base + row_off<RB>(r0 + (l16 >> 2), byte));
+        f.b = read_tr4x16(base + row_off<RB>(r0 + 4 + (l16 >> 2), byte));
+    } else {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const float *>(base + row_off<RB>(r0 + j, 4 * (16 * c + l16)));
+        f.a = make_frag<BF>(x[0], x[1], x[2], x[3]);
+        f.b = make_frag<BF>(x[4], x[5], x[6], x[7]);
+    }
+    return f;
+}
+// Eight consecutive values of a row in memory (zero for a row past the end).
+template <bool BF>
+__device__ __forceinline__ Frag2<BF> mem_frag(const void *p, int64_t at, bool valid) {
+    Frag2<BF> f;
+    if constexpr (BF) {
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (valid) w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
+        f.a.v = make_uint2(w.x, w.y);
+        f.b.v = make_uint2(w.z, w.w);
+    } else {
+        f.a.v = f.b.v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (valid) {
+            f.a.v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
+            f.b.v = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at + 4);
+        }
+    }
+    return f;
+}
+// The same fragment to a row in LDS.
+template <bool BF, int RB>
+__device__ __forceinline__ void row_put_frag(char *base, int row, int e0, const Frag2<BF> &f) {
+    if constexpr (BF) {
+        *reinterpret_cast<uint4 *>(base + row_off<RB>(row, 2 * e0)) = make_uint4(f.a.v.x, f.a.v.y, f.b.v.x, f.b.v.y);
+    } else {
+        *reinterpret_cast<float4 *>(base + row_off<RB>(row, 4 * e0)) = f.a.v;
+        *reinterpret_cast<float4 *>(base + row_off<RB>(row, 4 * e0 + 16)) = f.b.v;
+    }
+}
+template <bool BF>
+__device__ __forceinline__ float dot4(const f32x4 &x, const f32x4 &y, float s) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s = fmaf(x[j], y[j], s);
+    return s;
+}
+template <bool BF>
+__device__ __forceinline__ float dot16(const u32x4 &x, const u32x4 &y, float s) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (BF) {
+            s = fmaf(bf16_lo(x[j]), bf16_lo(y[j]), s);
+            s = fmaf(bf16_hi(x[j]), bf16_hi(y[j]), s);
+        } else {
+            s = fmaf(__uint_as_float(x[j]), __uint_as_float(y[j]), s);
+        }
+    }
+    return s;
+}
+
+template <bool BF, int DK, int DV>
+struct GradLds {
+    static constexpr int E = BF ? 2 : 4, C = BF ? kChunkBf16 : kChunkF32, RT = C / 16, NT = 64 * RT;
+    static constexpr int RB = DK * E, ZRB = DV * E, MRB = C * E;
+    static constexpr int KB = C * RB, SB = DV * RB, ZB = C * ZRB, MB = C * MRB;
+    static constexpr int B0 = 2 * KB, BB = SB > ZB + 2 * MB ? SB : ZB + 2 * MB;
+    static constexpr int G0 = B0 + BB;                     // up, down, beta, hi, lo [C]; 12 block factors
+    static constexpr int T0 = G0 + 5 * C * 4 + 64;         // column sums [RT][C]
+    static constexpr int V0 = T0 + RT * C * 4;             // row terms, x, diagonal [C]; <S, dS> per wave
+    static constexpr int kBytes = V0 + 3 * C * 4 + 32;
+};
+
+template <bool BF, int DK, int DV>
+__global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_grad_kernel(GradParams gp) {
+    using L = GradLds<BF, DK, DV>;
+    using IO = typename std::conditional<BF, uint16_t, float>::type;
+    constexpr int C = L::C, RT = L::RT, KT = DK / 16, K2 = DK / 32, V2 = DV / 32;
+    __shared__ __attribute__((aligned(16))) char smem[L::kBytes];
+    const GdnParams &p = gp.f;
+    const int tid = threadIdx.x, lane = tid & 63, r = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int l16 = lane & 15, q4 = lane >> 4;
+    // the chunk of this slot
+    const int64_t slot = blockIdx.x / p.Hk;
+    const int hk = (int)(blockIdx.x % p.Hk), rep = p.Hv / p.Hk;
+    int64_t tok;
+    int clen;
+    if (p.cu) {
+        // last sequence whose first slot is not behind this one
+        int lo = 0, hi = p.num_seqs - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (slot_base(min(max(p.cu[mid], 0), p.T), mid, C) <= slot) lo = mid;
+            else hi = mid - 1;
+        }
+        const int a = min(max(p.cu[lo], 0), p.T), b = min(max(p.cu[lo + 1], a), p.T);
+        const int64_t c = slot - slot_base(a, lo, C);
+        if (c < 0 || c * C >= b - a) return;
+        tok = a + c * C;
+        clen = (int)min((int64_t)C, b - tok);
+    } else {
+        const int nch = (p.T + C - 1) / C;
+        const int c = (int)(slot % nch);
+        tok = slot / nch * p.T + (int64_t)c * C;
+        clen = min(C, p.T - c * C);
+    }
+    const int row = 16 * r + l16;
+    const bool valid = row < clen;
+    char *K = smem, *Q = smem + L::KB, *buf = smem + L::B0;
+    char *E1 = buf + L::ZB, *H = E1 + L::MB;
+    float *gate = reinterpret_cast<float *>(smem + L::G0), *fac = gate + 5 * C;
+    float *colsum = reinterpret_cast<float *>(smem + L::T0);
+    float *rowv = reinterpret_cast<float *>(smem + L::V0), *xv = rowv + C, *diag = xv + C, *sds = diag + C;
+
+#pragma unroll
+    for (int t = 0; t < K2; ++t) {
+        const int e0 = 32 * t + 8 * q4;
+        row_put_frag<BF, L::RB>(K, row, e0, mem_frag<BF>(p.k, (tok + row) * p.ldk + hk * DK + e0, valid));
+        row_put_frag<BF, L::RB>(Q, row, e0, mem_frag<BF>(p.q, (tok + row) * p.ldq + hk * DK + e0, valid));
+    }
+    f32x4 dq[KT], dk[KT];
+#pragma unroll
+    for (int ct = 0; ct < KT; ++ct) dq[ct] = dk[ct] = zero4();
+    // loops over the channel tiles run in pairs, so that not all their operands are loaded at once
+    auto pair_end = [] { __builtin_amdgcn_sched_barrier(0); };
+
+#pragma unroll 1
+    for (int g = 0; g < rep; ++g) {
+        const int h = hk * rep + g;
+        // addresses are formed anew for every head rather than kept in (or spilled from) registers
+        asm volatile("" : "+v"(l16), "+v"(q4));
+        const int row = 16 * r + l16;
+        auto own_row = [&](const char *m, int t) { return row_frag<BF, L::RB>(m, row, 32 * t + 8 * q4); };
+        const int64_t vrow = ((tok + row) * p.Hv + h) * DV;
+        Frag2<BF> dof[V2], dxf[V2], zf[V2];
+#pragma unroll
+        for (int u = 0; u < V2; ++u) {
+            dof[u] = mem_frag<BF>(p.v, vrow + 32 * u + 8 * q4, valid);
+            dxf[u] = mem_frag<BF>(gp.dx, vrow + 32 * u + 8 * q4, valid);
+        }
+        // S to LDS, <S, dS> on the way; bf16: dS waits in registers for its turn
+        constexpr int NP = L::SB / 16 / L::NT;
+        const u32x4 *sp = reinterpret_cast<const u32x4 *>(static_cast<const char *>(gp.hs) + (slot * p.Hv + h) * L::SB);
+        const u32x4 *dp = reinterpret_cast<const u32x4 *>(static_cast<const char *>(gp.dhs) + (slot * p.Hv + h) * L::SB);
+        auto put_state = [&](int i, const u32x4 &v) {
+            const int piece = i * L::NT + tid;
+            *reinterpret_cast<u32x4 *>(buf + row_off<L::RB>(piece / (L::RB / 16), piece % (L::RB / 16) * 16)) = v;
+        };
+        u32x4 held[BF ? NP : 1];
+        float ss = 0.f;
+        if constexpr (BF) {
+            u32x4 sv[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                sv[i] = sp[i * L::NT + tid];
+                held[i] = dp[i * L::NT + tid];
+            }
+            if (g > 0) __syncthreads();  // the last head's reads of the buffer
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                put_state(i, sv[i]);
+                ss = dot16<BF>(sv[i], held[i], ss);
+            }
+        } else {
+            if (g > 0) __syncthreads();
+#pragma unroll 4
+            for (int i = 0; i < NP; ++i) {
+                const u32x4 v = sp[i * L::NT + tid];
+                put_state(i, v);
+                ss = dot16<BF>(v, dp[i * L::NT + tid], ss);
+            }
+        }
+        if (r == 0) {
+            Walk w;
+            w.tok0 = tok;
+            w.len = clen;
+            w.h = h;
+            const Gates gt = make_gates<C>(load_gate<C>(p, w, 0, lane), lane);
+            if (lane < C) {
+                gate[lane] = gt.up;
+                gate[C + lane] = gt.down;
+                gate[2 * C + lane] = gt.beta;
+                gate[3 * C + lane] = gt.hi;
+                gate[4 * C + lane] = gt.lo;
+                if ((lane & 15) == 0) {
+                    fac[lane >> 4] = gt.f[0];
+                    fac[4 + (lane >> 4)] = gt.f[1];
+                }
+                if (lane == 0) {
+#pragma unroll
+                    for (int i = 2; i < 6; ++i) fac[6 + i] = gt.f[i];
+                }
+            }
+        }
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) ss += __shfl_xor(ss, off);
+        if (lane == 0) sds[r] = ss;
+        __syncthreads();
+        const float up = gate[row], down = gate[C + row], bet = gate[2 * C + row];
+        const float eG = up * fac[r], eB = down * fac[4 + r];
+        // the parts through the state entering the chunk
+        float rowsum = 0.f, xk = 0.f;
+#pragma unroll
+        for (int t = 0; t < K2; ++t) {
+            const Frag2<BF> kr = own_row(K, t), qr = own_row(Q, t);
+            f32x4 r1[2], r2[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) r1[i] = r2[i] = zero4();
+#pragma unroll
+            for (int u = 0; u < V2; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const Frag2<BF> a = col_frag8<BF, L::RB>(buf, 2 * t + i, u, l16, q4);
+                    mma<BF>(r1[i], a, dof[u]);
+                    mma<BF>(r2[i], a, dxf[u]);
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                r1[i] = r1[i] * (eG * p.scale);
+                r2[i] = r2[i] * -eG;
+                rowsum = dot4<BF>(frag_f32<BF>(i ? qr.b : qr.a), r1[i], rowsum);
+                rowsum = dot4<BF>(frag_f32<BF>(i ? kr.b : kr.a), r2[i], rowsum);
+                dq[2 * t + i] = dq[2 * t + i] + r1[i];
+                dk[2 * t + i] = dk[2 * t + i] + r2[i];
+            }
+            pair_end();
+        }
+#pragma unroll
+        for (int u = 0; u < V2; ++u) zf[u] = mem_frag<BF>(gp.zs, vrow + 32 * u + 8 * q4, valid);
+        __syncthreads();
+        if constexpr (BF) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) put_state(i, held[i]);
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < NP; ++i) put_state(i, dp[i * L::NT + tid]);
+        }
+        __syncthreads();
+        // the part through the state leaving it
+#pragma unroll
+        for (int t = 0; t < K2; ++t) {
+            const Frag2<BF> kr = own_row(K, t);
+            f32x4 r3[2] = {zero4(), zero4()};
+#pragma unroll
+            for (int u = 0; u < V2; ++u)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mma<BF>(r3[i], col_frag8<BF, L::RB>(buf, 2 * t + i, u, l16, q4), zf[u]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                r3[i] = r3[i] * eB;
+                xk = dot4<BF>(frag_f32<BF>(i ? kr.b : kr.a), r3[i], xk);
+                dk[2 * t + i] = dk[2 * t + i] + r3[i] * bet;
+            }
+            pair_end();
+        }
+        __syncthreads();
+        // inside the chunk: Z to LDS, then the 16 x 16 tiles of row tile r
+#pragma unroll
+        for (int u = 0; u < V2; ++u) row_put_frag<BF, L::ZRB>(buf, row, 32 * u + 8 * q4, zf[u]);
+        __syncthreads();
+#pragma unroll 1
+        for (int c = 0; c <= r; ++c) {
+            f32x4 kk = zero4(), qk = zero4(), w1 = zero4(), w2 = zero4();
+#pragma unroll
+            for (int t = 0; t < K2; ++t) {
+                const Frag2<BF> kc = row_frag<BF, L::RB>(K, 16 * c + l16, 32 * t + 8 * q4);
+                mma<BF>(kk, kc, own_row(K, t));
+                mma<BF>(qk, kc, own_row(Q, t));
+            }
+#pragma unroll
+            for (int u = 0; u < V2; ++u) {
+                const Frag2<BF> zc = row_frag<BF, L::ZRB>(buf, 16 * c + l16, 32 * u + 8 * q4);
+                mma<BF>(w1, zc, dof[u]);
+                mma<BF>(w2, zc, dxf[u]);
+            }
+            const int j0 = 16 * c + 4 * q4;
+            f32x4 gam;
+            if (c == r) {
+                const f32x4 h4 = load_f4(gate + 3 * C + j0), l4 = load_f4(gate + 4 * C + j0);
+                const float ho = gate[3 * C + row], lo = gate[4 * C + row];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) gam[e] = row >= j0 + e ? fast_exp2((ho - h4[e]) + (lo - l4[e])) : 0.f;
+            } else {
+                const float f = r - c == 1 ? 1.f : fac[8 + (r - c == 3 ? 2 : c)];
+                gam = load_f4(gate + C + j0) * (up * f);
+            }
+            const f32x4 b4 = load_f4(gate + 2 * C + j0);
+            mfma_settle(kk, qk);
+            mfma_settle(w1, w2);
+            f32x4 e1, f1, t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = p.scale * w1[e] * gam[e], b = -w2[e] * gam[e];
+                const bool strict = c < r || row > j0 + e;
+                e1[e] = a * b4[e];
+                f1[e] = strict ? b * b4[e] : 0.f;
+                t[e] = qk[e] * a;
+                if (c == r && row == j0 + e) diag[row] = t[e];
+                t[e] = strict ? fmaf(kk[e], b, t[e]) : 0.f;
+                rowsum = fmaf(b4[e], t[e], rowsum);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // over the tile's 16 rows: the last lane of 16 has the sum
+                t[e] = scan16_add(t[e]);
+            }
+            if (l16 == 15) *reinterpret_cast<f32x4 *>(colsum + r * C + j0) = t;
+            row_put4<BF, L::MRB>(E1, row, j0, e1[0], e1[1], e1[2], e1[3]);
+            row_put4<BF, L::MRB>(H, row, j0, f1[0], f1[1], f1[2], f1[3]);
+            wave_lds_sync();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c < r || row > j0 + e) row_put1<BF, L::MRB>(H, j0 + e, row, f1[e]);
+            wave_lds_sync();
+        }
+        if ((r & 1) == 0) row_put4<BF, L::MRB>(E1, row, 16 * (r + 1) + 4 * q4, 0.f, 0.f, 0.f, 0.f);
+        rowsum += __shfl_xor(rowsum, 16);
+        rowsum += __shfl_xor(rowsum, 32);
+        xk += __shfl_xor(xk, 16);
+        xk += __shfl_xor(xk, 32);
+        if (q4 == 0) {
+            rowv[row] = rowsum;
+            xv[row] = xk;
+        }
+        __syncthreads();
+        Frag2<BF> er[RT / 2], hr[RT / 2], ec[RT / 2];
+#pragma unroll
+        for (int u = 0; u < RT / 2; ++u) {
+            er[u] = row_frag<BF, L::MRB>(E1, row, 32 * u + 8 * q4);
+            hr[u] = row_frag<BF, L::MRB>(H, row, 32 * u + 8 * q4);
+            ec[u] = plain_col_frag8<BF, L::MRB>(E1, r, u, l16, q4);
+        }
+        // row tiles of the first 32 tokens need E's columns there, those of the second its rows there
+        auto products = [&](auto second) {
+            constexpr int R2 = decltype(second)::value;
+#pragma unroll
+            for (int ct = 0; ct < KT; ++ct) {
+#pragma unroll
+                for (int u = 0; u < RT / 2; ++u) {
+                    const Frag2<BF> kt = col_frag8<BF, L::RB>(K, ct, u, l16, q4);
+                    if (u <= R2) mma<BF>(dq[ct], kt, er[u]);
+                    mma<BF>(dk[ct], kt, hr[u]);
+                    if (u >= R2) mma<BF>(dk[ct], col_frag8<BF, L::RB>(Q, ct, u, l16, q4), ec[u]);
+                }
+                if (ct & 1) pair_end();
+            }
+        };
+        if (RT > 2 && r >= 2) products(std::integral_constant<int, 1>{});
+        else products(std::integral_constant<int, 0>{});
+#pragma unroll
+        for (int ct = 0; ct < KT; ++ct) mfma_settle(dq[ct], dk[ct]);
+        if (r == 0) {
+            // gates' gradients, lane = token
+            float dG = 0.f, db = 0.f, bx = 0.f;
+            if (lane < C) {
+                float cs = 0.f;
+                for (int rr = lane >> 4; rr < RT; ++rr) cs += colsum[rr * C + lane];
+                const float b = gate[2 * C + lane];
+                db = cs + diag[lane] + xv[lane];
+                bx = b * xv[lane];
+                dG = rowv[lane] - b * cs - bx;
+            }
+            float end = bx;
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1) end += __shfl_xor(end, off);
+            float sd = 0.f;
+            for (int i = 0; i < RT; ++i) sd += sds[i];
+            if (lane == C - 1) dG += fmaf(fac[11], sd, end);
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const float o = __shfl_down(dG, off);
+                dG += lane + off < 64 ? o : 0.f;
+            }
+            if (lane < clen) {
+                const int64_t at = (tok + lane) * p.Hv + h;
+                if (p.gate_bf16) {
+                    static_cast<uint16_t *>(gp.dg)[at] = f32_to_bf16(dG);
+                    static_cast<uint16_t *>(gp.dbeta)[at] = f32_to_bf16(db);
+                } else {
+                    static_cast<float *>(gp.dg)[at] = dG;
+                    static_cast<float *>(gp.dbeta)[at] = db;
+                }
+            }
+        }
+    }
+    if (valid) {
+        IO *oq = static_cast<IO *>(gp.dq) + ((tok + row) * p.Hk + hk) * DK + 8 * q4;
+        IO *ok = static_cast<IO *>(gp.dk) + ((tok + row) * p.Hk + hk) * DK + 8 * q4;
+#pragma unroll
+        for (int ct = 0; ct < KT; ++ct) {
+            const int at = 32 * (ct >> 1) + 4 * (ct & 1);
+            IoTraits<IO>::store4(oq + at, make_float4(dq[ct][0], dq[ct][1], dq[ct][2], dq[ct][3]));
+            IoTraits<IO>::store4(ok + at, make_float4(dk[ct][0], dk[ct][1], dk[ct][2], dk[ct][3]));
+        }
+    }
+}
+
+template <bool BF>
+hipError_t launch_grad(const GradParams &gp, hipStream_t stream) {
+    const GdnParams &p = gp.f;
+    const int64_t blocks = gp.slots * p.Hk;
+    if (blocks <= 0) return hipSuccess;
+#define GDN_GRAD(DK_, DV_)                                                                              \
+    if (p.dk == DK_ && p.dv == DV_) {                                                                   \
+        hipLaunchKernelGGL((gdn_grad_kernel<BF, DK_, DV_>), dim3((unsigned)blocks),                     \
+                           dim3((GradLds<BF, DK_, DV_>::NT)), 0, stream, gp);                           \
+        return hipGetLastError();                                                                       \
+    }
+    GDN_GRAD(64, 64)
+    GDN_GRAD(64, 128)
+    GDN_GRAD(128, 64)
+    GDN_GRAD(128, 128)
+#undef GDN_GRAD
+    return hipErrorInvalidConfiguration;
+}
+
+}  // namespace gdn
+}  // namespace kda

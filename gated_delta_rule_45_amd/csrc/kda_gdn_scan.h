@@ -688,7 +688,8 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
     constexpr int C = L::C, RT = L::RT, KT = DK / 16, K2 = DK / 32;
     constexpr bool REV = MODE == kRev;
     __shared__ __attribute__((aligned(16))) char smem[L::kBytes];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q4 = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, q4 = lane >> 4;
     const Walk w = walk_of<C, CT>(p);
     const int nch = w.nch;
     // step s works on chunk ci(s); the reverse scan walks from the last chunk to the first

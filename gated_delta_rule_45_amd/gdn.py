@@ -17,7 +17,7 @@ import torch
 
 from . import _P, _check, _io_code, _need, _ptr, library
 
-__all__ = ["gdn_chunk_fwd", "gdn_decode", "norm_gate_bwd"]
+__all__ = ["gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode", "norm_gate_bwd"]
 
 
 class GdnProblem(ctypes.Structure):
@@ -34,7 +34,9 @@ def declare(lib: ctypes.CDLL) -> None:
         [ctypes.c_size_t, _P]
     lib.kda_norm_gate_bwd_workspace.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
     lib.kda_norm_gate_bwd_workspace.restype = ctypes.c_size_t
-    for f in (lib.kda_gdn_chunk_fwd, lib.kda_gdn_decode, lib.kda_norm_gate_bwd):
+    lib.kda_gdn_chunk_bwd.argtypes = [prob] + [_P] * 17 + [ctypes.c_size_t, _P]
+    lib.kda_gdn_chunk_bwd_workspace.argtypes = [prob, ctypes.POINTER(ctypes.c_size_t)]
+    for f in (lib.kda_gdn_chunk_bwd, lib.kda_gdn_chunk_bwd_workspace, lib.kda_gdn_chunk_fwd, lib.kda_gdn_decode, lib.kda_norm_gate_bwd):
         f.restype = ctypes.c_int
 
 
@@ -146,6 +148,49 @@ def gdn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
                                            _ptr(initial_state), _ptr(cu_seqlens), _ptr(host), _ptr(out),
                                            _ptr(final_state), handle))
     return out, final_state
+
+
+def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                  d_out: torch.Tensor, initial_state: Optional[torch.Tensor] = None,
+                  d_final_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, *,
+                  cu_seqlens_host=None, scale: float = 1.0, need_d_initial_state: bool = True,
+                  workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None, stream=None) -> dict:
+    """Gradients of gdn_chunk_fwd for L = sum(d_out * out) + sum(d_final_state * final_state).  d_out: out's
+    shape and dtype; d_final_state: as the states, or None (zero).  Returns dict(dq, dk [B, T, Hk, d_k],
+    dv [B, T, Hv, d_v] (io dtype), dg, dbeta [B, T, Hv] (g's dtype), d_initial_state [N, Hv, d_k, d_v]
+    (the states' dtype, fp32 where no state is given, or None)), all dense; `out` (a dict returned by an
+    earlier call of the same shape) is written in place."""
+    given = initial_state if initial_state is not None else d_final_state
+    sdt = given.dtype if given is not None else torch.float32
+    p, n = _problem(q, k, v, g, beta, cu_seqlens, sdt, scale)
+    dev, states = q.device, (n, v.shape[2], q.shape[3], v.shape[3])
+    _need(d_out, "d_out", q.dtype, v.shape, dev)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", sdt, states, dev)
+    if d_final_state is not None:
+        _need(d_final_state, "d_final_state", sdt, states, dev)
+    host = _host_i32(cu_seqlens_host, n + 1, "cu_seqlens_host")
+    lib = library()
+    want = {"dq": (q.shape, q.dtype), "dk": (q.shape, q.dtype), "dv": (v.shape, q.dtype), "dg": (g.shape, g.dtype),
+            "dbeta": (g.shape, g.dtype), "d_initial_state": (states, sdt)}
+    with _Launch(dev, stream) as handle:
+        if out is None:
+            out = {name: torch.empty(s, dtype=t, device=dev) if name != "d_initial_state" or need_d_initial_state else None
+                   for name, (s, t) in want.items()}
+        else:
+            for name, (s, t) in want.items():
+                if name != "d_initial_state" or out.get(name) is not None:
+                    _need(out[name], name, t, s, dev)
+        if workspace is None:
+            need = ctypes.c_size_t(0)
+            _check(lib.kda_gdn_chunk_bwd_workspace(ctypes.byref(p), ctypes.byref(need)))
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        _check(lib.kda_gdn_chunk_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state),
+                                     _ptr(cu_seqlens), _ptr(host), _ptr(d_out), _ptr(d_final_state), _ptr(out["dq"]),
+                                     _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
+                                     _ptr(out.get("d_initial_state")), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), handle))
+    return out
 
 
 def gdn_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,

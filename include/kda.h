@@ -436,6 +436,31 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
                                const int32_t *cu_seqlens_host, void *out, void *final_state, void *stream);
 
 /*
+ * kda_gdn_chunk_bwd -- gradients of kda_gdn_chunk_fwd for L = sum(d_out * out) + sum(d_final_state * final_state)
+ * (the reverse-mode derivative of the chunk equations; the forward is recomputed, out is not needed).
+ *
+ *  q, k, v, g, beta, initial_state, cu_seqlens, cu_seqlens_host   as for kda_gdn_chunk_fwd
+ *  d_out            [tokens, Hv, d_v] io dtype, dense
+ *  d_final_state    [num_seqs, Hv, d_k, d_v] state dtype, or NULL for zero
+ *  dq, dk           [tokens, Hk, d_k] io dtype, dense: summed over the value heads of a key head, in a fixed order
+ *  dv               [tokens, Hv, d_v] io dtype, dense
+ *  dg, dbeta        [tokens, Hv] gate dtype
+ *  d_initial_state  [num_seqs, Hv, d_k, d_v] state dtype, or NULL to skip it
+ *  workspace        kda_gdn_chunk_bwd_workspace() bytes, 256-byte aligned: the states entering the chunks and
+ *                   the gradients of those leaving them (bf16 or fp32, the io dtype) and one value tensor
+ * No output may overlap anything else.  beta = 0 is exact (nothing is divided by it).  The results repeat
+ * bit for bit.  Calls that overlap in time need a workspace each.  Errors as for kda_chunk_bwd.
+ */
+kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,
+                               const void *g, const void *beta, const void *initial_state, const int32_t *cu_seqlens,
+                               const int32_t *cu_seqlens_host, const void *d_out, const void *d_final_state, void *dq,
+                               void *dk, void *dv, void *dg, void *dbeta, void *d_initial_state, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Workspace bytes kda_gdn_chunk_bwd needs (a packed batch where problem->num_seqs > 0); *bytes = 0 on error. */
+kda_status_t kda_gdn_chunk_bwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes);
+
+/*
  * kda_gdn_decode -- the same recurrence token by token for one or a few new tokens per sequence, on a pool
  * of state slots updated in place (the serving form; fp32 arithmetic throughout).
  *
