@@ -52,6 +52,18 @@ struct GradParams {
 hipError_t launch_grad_bf16(const GradParams &p, hipStream_t stream);
 hipError_t launch_grad_f32(const GradParams &p, hipStream_t stream);
 
+// Rows of bf16 values, ld elements apart, and their dense fp32 copy.
+struct ConvertRows {
+    void *bf16, *f32;
+    int64_t rows, cols, ld;  // cols, ld multiples of 8
+};
+struct ConvertParams {
+    ConvertRows t[4];
+    int32_t n;
+};
+// widen: bf16 -> fp32, else fp32 -> bf16
+hipError_t launch_convert(bool widen, const ConvertParams &p, hipStream_t stream);
+
 struct DecodeParams {
     const void *q, *k, *v;    // as above
     const void *g, *beta;

@@ -172,21 +172,36 @@ hipError_t launch_scan(const kda_gdn_problem_t *p, int mode, int cols, const kda
     return p->io_dtype == KDA_BF16 ? kda::gdn::launch_scan_bf16(mode, cols, r, s) : kda::gdn::launch_scan_f32(mode, cols, r, s);
 }
 
-// Workspace of the backward: S and dS per chunk slot, Z per token.
+// Whether the gradients of a bf16 call are computed on fp32 operands.  With few gates' gradients the
+// roundings of the products' operands do not average out (260 values: the norm of the error of dg up
+// to 5.7e-3 of dg's, 3e-3 for thousands of values and about 1e-6 on fp32 operands), and so short a call
+// is bound by its launches either way.
+bool bwd_wide(const kda_gdn_problem_t *p, const Shape &s) {
+    return p->io_dtype == KDA_BF16 && s.tokens <= 256 && s.tokens * p->num_heads_v <= 512;
+}
+
+// Workspace of the backward: S and dS per chunk slot, Z per token; on fp32 operands also the copies of the
+// tensors in bf16 (q, k, v, d_out, dq, dk, dv).
 struct BwdLayout {
     int64_t slots = 0;
-    size_t dhs = 0, zs = 0, bytes = 0;
+    size_t dhs = 0, zs = 0, copies = 0, qk = 0, vo = 0, bytes = 0;
 };
 kda_status_t bwd_layout(const kda_gdn_problem_t *p, const Shape &s, bool packed, BwdLayout &b) {
-    const int64_t C = kda::gdn::chunk_of(p->io_dtype), per = (int64_t)p->seq_len / C;
+    const bool wide = bwd_wide(p, s);
+    const int64_t C = kda::gdn::chunk_of(wide ? KDA_F32 : p->io_dtype), per = (int64_t)p->seq_len / C;
     b.slots = packed ? per + s.num_seqs : (int64_t)s.num_seqs * (per + (p->seq_len % C != 0));
-    const int64_t row = s.v_row * s.io;
+    const int64_t row = s.v_row * (wide ? 4 : s.io);
     if (b.slots > 0x7fffffffLL / p->num_heads_k || b.slots > (1LL << 60) / (row * p->head_dim_k))
         return set_error(KDA_ERR_UNSUPPORTED, "too many chunks");
     auto align = [](int64_t x) { return (size_t)((x + 255) / 256 * 256); };
     b.dhs = align(b.slots * row * p->head_dim_k);
     b.zs = 2 * b.dhs;
-    b.bytes = b.zs + align(s.tokens * row);
+    b.copies = b.bytes = b.zs + align(s.tokens * row);
+    if (wide) {
+        b.qk = align(s.tokens * s.qk_row * 4);
+        b.vo = align(s.tokens * s.v_row * 4);
+        b.bytes += 4 * b.qk + 3 * b.vo;
+    }
     return KDA_OK;
 }
 
@@ -283,11 +298,34 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
         hipStream_t hs = static_cast<hipStream_t>(stream);
         char *ws = static_cast<char *>(workspace);
         const int cols = scan_cols(problem, s, current_cus());
-        kda::gdn::GdnParams keep = params_of(problem, s, q, k, v, g, beta, cu_seqlens);
+        kda_gdn_problem_t run = *problem;
+        kda::gdn::ConvertParams in{}, back{};
+        if (bwd_wide(problem, s) && s.tokens > 0) {
+            char *at = ws + b.copies;
+            auto copy = [&](kda::gdn::ConvertParams &c, const void *p, int64_t cols_, int64_t ld, size_t bytes) {
+                c.t[c.n++] = {const_cast<void *>(p), at, s.tokens, cols_, ld};
+                void *f = at;
+                at += bytes;
+                return f;
+            };
+            q = copy(in, q, s.qk_row, s.ldq, b.qk);
+            k = copy(in, k, s.qk_row, s.ldk, b.qk);
+            v = copy(in, v, s.v_row, s.ldv, b.vo);
+            d_out = copy(in, d_out, s.v_row, s.v_row, b.vo);
+            dq = copy(back, dq, s.qk_row, s.qk_row, b.qk);
+            dk = copy(back, dk, s.qk_row, s.qk_row, b.qk);
+            dv = copy(back, dv, s.v_row, s.v_row, b.vo);
+            run.io_dtype = KDA_F32;
+            s.ldq = s.ldk = s.qk_row;
+            s.ldv = s.v_row;
+            st = done(kda::gdn::launch_convert(true, in, hs), "kda_gdn_chunk_bwd widening launch");
+            if (st != KDA_OK) return st;
+        }
+        kda::gdn::GdnParams keep = params_of(&run, s, q, k, v, g, beta, cu_seqlens);
         keep.s0 = initial_state;
         keep.hs = ws;
         keep.zs = ws + b.zs;
-        kda::gdn::GdnParams rev = params_of(problem, s, q, k, d_out, g, beta, cu_seqlens);
+        kda::gdn::GdnParams rev = params_of(&run, s, q, k, d_out, g, beta, cu_seqlens);
         rev.ldv = s.v_row;
         rev.s0 = d_final_state;
         rev.sf = d_initial_state;
@@ -305,13 +343,15 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
         grad.dbeta = dbeta;
         grad.slots = b.slots;
         if (s.tokens > 0) {
-            st = done(launch_scan(problem, 1, cols, keep, hs), "kda_gdn_chunk_bwd forward launch");
+            st = done(launch_scan(&run, 1, cols, keep, hs), "kda_gdn_chunk_bwd forward launch");
             if (st != KDA_OK) return st;
         }
-        st = done(launch_scan(problem, 2, cols, rev, hs), "kda_gdn_chunk_bwd reverse launch");
+        st = done(launch_scan(&run, 2, cols, rev, hs), "kda_gdn_chunk_bwd reverse launch");
         if (st != KDA_OK || s.tokens == 0) return st;
-        return done(problem->io_dtype == KDA_BF16 ? kda::gdn::launch_grad_bf16(grad, hs) : kda::gdn::launch_grad_f32(grad, hs),
-                    "kda_gdn_chunk_bwd gradient launch");
+        st = done(run.io_dtype == KDA_BF16 ? kda::gdn::launch_grad_bf16(grad, hs) : kda::gdn::launch_grad_f32(grad, hs),
+                  "kda_gdn_chunk_bwd gradient launch");
+        if (st != KDA_OK || back.n == 0) return st;
+        return done(kda::gdn::launch_convert(false, back, hs), "kda_gdn_chunk_bwd narrowing launch");
     } catch (...) {
         return KDA_ERR_HIP;
     }

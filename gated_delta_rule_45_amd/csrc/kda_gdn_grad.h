@@ -14,17 +14,39 @@
 // added and subtracted.
 //
 // One workgroup owns (chunk, key head) and walks the value heads that share it, so that dQ and dK are
-// summed over them in registers, in a fixed order.  Wave r owns the 16 tokens of row tile r: its dO, dX,
-// and Z rows are operand fragments read straight from memory, dQ^T and dK^T stay in accumulators
-// (lane = token, so the gates are lane scalars and 8 consecutive channels leave as 16 bytes).  S, dS,
-// then Z with E and F + F^T take turns in one 32 KB LDS buffer beside K and Q: 67 KB, two workgroups per
-// CU, one's loads behind the other's products.  Bound: HBM (reads 9 and writes 2 tensors' rows per chunk).
+// summed over them in registers, in a fixed order.  Two waves own the 16 tokens of row tile r, one
+// half of the channels each: dO, dX and Z rows are operand fragments read straight from memory, dQ^T
+// and dK^T stay in accumulators (lane = token, so the gates are lane scalars and 8 consecutive channels
+// leave as 16 bytes).  S, dS, then Z with E and F + F^T take turns in one 32 KB LDS buffer beside K and Q:
+// 70 KB and at most 128 registers, two workgroups per CU, one's loads behind the other's products.
+// Bound: HBM and its latency (reads 9 and writes 2 tensors' rows per chunk).
 #pragma once
 
 #include "kda_gdn_scan.h"
 
 namespace kda {
 namespace gdn {
+
+// Rows as row_off lays them out, the slots of rows 16 apart exchanged too: the four groups of 4 rows, 8
+// apart, of a transposed read then meet 4 deep instead of 8 in the banks.  (Not in the scan, whose
+// addresses differ by constants from row tile to row tile only without it.)
+template <int RB>
+__device__ __forceinline__ int mix_off(int row, int byte) {
+    return RB >= 256 ? row_off<RB>(row, byte) ^ (row >> 4 & 3) << 6 : row_off<RB>(row, byte);
+}
+template <bool BF, int RB>
+__device__ __forceinline__ Frag2<BF> mix_frag(const char *base, int row, int e0) {
+    Frag2<BF> f;
+    if constexpr (BF) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(base + mix_off<RB>(row, 2 * e0));
+        f.a.v = make_uint2(w.x, w.y);
+        f.b.v = make_uint2(w.z, w.w);
+    } else {
+        f.a.v = *reinterpret_cast<const float4 *>(base + mix_off<RB>(row, 4 * e0));
+        f.b.v = *reinterpret_cast<const float4 *>(base + mix_off<RB>(row, 4 * e0 + 16));
+    }
+    return f;
+}
 
 // As col_frag, the contraction over 8 consecutive rows per lane: 32 u + 8 q4 ..
 template <bool BF, int RB>
@@ -33,13 +55,13 @@ __device__ __forceinline__ Frag2<BF> col_frag8(const char *base, int ct, int u, 
     if constexpr (BF) {
         const int byte = 16 * (4 * (ct >> 1) + (l16 & 3)) + 8 * (ct & 1);
         const int r0 = 32 * u + 8 * q4 + (l16 >> 2);
-        f.a = read_tr4x16(base + row_off<RB>(r0, byte));
-        f.b = read_tr4x16(base + row_off<RB>(r0 + 4, byte));
+        f.a = read_tr4x16(base + mix_off<RB>(r0, byte));
+        f.b = read_tr4x16(base + mix_off<RB>(r0 + 4, byte));
     } else {
         const int byte = 4 * state_channel(ct, l16 >> 2, l16 & 3);
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const float *>(base + row_off<RB>(32 * u + 8 * q4 + j, byte));
+        for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const float *>(base + mix_off<RB>(32 * u + 8 * q4 + j, byte));
         f.a = make_frag<BF>(x[0], x[1], x[2], x[3]);
         f.b = make_frag<BF>(x[4], x[5], x[6], x[7]);
     }
@@ -52,12 +74,12 @@ __device__ __forceinline__ Frag2<BF> plain_col_frag8(const char *base, int c, in
     const int r0 = 32 * u + 8 * q4;
     if constexpr (BF) {
         const int byte = 2 * (16 * c + 4 * (l16 & 3));
-        f.a = read_tr4x16(base + row_off<RB>(r0 + (l16 >> 2), byte));
-        f.b = read_tr4x16(base + row_off<RB>(r0 + 4 + (l16 >> 2), byte));
+        f.a = read_tr4x16(base + mix_off<RB>(r0 + (l16 >> 2), byte));
+        f.b = read_tr4x16(base + mix_off<RB>(r0 + 4 + (l16 >> 2), byte));
     } else {
         float x[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const float *>(base + row_off<RB>(r0 + j, 4 * (16 * c + l16)));
+        for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const float *>(base + mix_off<RB>(r0 + j, 4 * (16 * c + l16)));
         f.a = make_frag<BF>(x[0], x[1], x[2], x[3]);
         f.b = make_frag<BF>(x[4], x[5], x[6], x[7]);
     }
@@ -85,13 +107,23 @@ __device__ __forceinline__ Frag2<BF> mem_frag(const void *p, int64_t at, bool va
 template <bool BF, int RB>
 __device__ __forceinline__ void row_put_frag(char *base, int row, int e0, const Frag2<BF> &f) {
     if constexpr (BF) {
-        *reinterpret_cast<uint4 *>(base + row_off<RB>(row, 2 * e0)) = make_uint4(f.a.v.x, f.a.v.y, f.b.v.x, f.b.v.y);
+        *reinterpret_cast<uint4 *>(base + mix_off<RB>(row, 2 * e0)) = make_uint4(f.a.v.x, f.a.v.y, f.b.v.x, f.b.v.y);
     } else {
-        *reinterpret_cast<float4 *>(base + row_off<RB>(row, 4 * e0)) = f.a.v;
-        *reinterpret_cast<float4 *>(base + row_off<RB>(row, 4 * e0 + 16)) = f.b.v;
+        *reinterpret_cast<float4 *>(base + mix_off<RB>(row, 4 * e0)) = f.a.v;
+        *reinterpret_cast<float4 *>(base + mix_off<RB>(row, 4 * e0 + 16)) = f.b.v;
     }
 }
-template <bool BF>
+// Eight consecutive fp32 values to memory.
+template <bool BF, typename IO>
+__device__ __forceinline__ void put_row8(IO *p, const f32x4 &a, const f32x4 &b) {
+    if constexpr (BF) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                                   pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
+    } else {
+        *reinterpret_cast<f32x4 *>(p) = a;
+        *reinterpret_cast<f32x4 *>(p + 4) = b;
+    }
+}
 __device__ __forceinline__ float dot4(const f32x4 &x, const f32x4 &y, float s) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) s = fmaf(x[j], y[j], s);
@@ -113,24 +145,27 @@ __device__ __forceinline__ float dot16(const u32x4 &x, const u32x4 &y, float s) 
 
 template <bool BF, int DK, int DV>
 struct GradLds {
-    static constexpr int E = BF ? 2 : 4, C = BF ? kChunkBf16 : kChunkF32, RT = C / 16, NT = 64 * RT;
+    static constexpr int E = BF ? 2 : 4, C = BF ? kChunkBf16 : kChunkF32, RT = C / 16, NT = 128 * RT;
     static constexpr int RB = DK * E, ZRB = DV * E, MRB = C * E;
     static constexpr int KB = C * RB, SB = DV * RB, ZB = C * ZRB, MB = C * MRB;
     static constexpr int B0 = 2 * KB, BB = SB > ZB + 2 * MB ? SB : ZB + 2 * MB;
     static constexpr int G0 = B0 + BB;                     // up, down, beta, hi, lo [C]; 12 block factors
     static constexpr int T0 = G0 + 5 * C * 4 + 64;         // column sums [RT][C]
-    static constexpr int V0 = T0 + RT * C * 4;             // row terms, x, diagonal [C]; <S, dS> per wave
-    static constexpr int kBytes = V0 + 3 * C * 4 + 32;
+    static constexpr int V0 = T0 + RT * C * 4;             // row terms and x, per channel half, and the diagonal [C]
+    static constexpr int D0 = V0 + 5 * C * 4;              // <S, dS> per wave
+    static constexpr int kBytes = D0 + 2 * RT * 4;
 };
 
 template <bool BF, int DK, int DV>
 __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_grad_kernel(GradParams gp) {
     using L = GradLds<BF, DK, DV>;
     using IO = typename std::conditional<BF, uint16_t, float>::type;
-    constexpr int C = L::C, RT = L::RT, KT = DK / 16, K2 = DK / 32, V2 = DV / 32;
+    constexpr int C = L::C, RT = L::RT, K2 = DK / 32, V2 = DV / 32, T2 = K2 / 2;
     __shared__ __attribute__((aligned(16))) char smem[L::kBytes];
     const GdnParams &p = gp.f;
-    const int tid = threadIdx.x, lane = tid & 63, r = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int tid = threadIdx.x;
+    // wave: row tile r, half hf of the channels
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = wave >> 1, hf = wave & 1;
     int l16 = lane & 15, q4 = lane >> 4;
     // the chunk of this slot
     const int64_t slot = blockIdx.x / p.Hk;
@@ -156,33 +191,36 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
         tok = slot / nch * p.T + (int64_t)c * C;
         clen = min(C, p.T - c * C);
     }
-    const int row = 16 * r + l16;
-    const bool valid = row < clen;
     char *K = smem, *Q = smem + L::KB, *buf = smem + L::B0;
     char *E1 = buf + L::ZB, *H = E1 + L::MB;
     float *gate = reinterpret_cast<float *>(smem + L::G0), *fac = gate + 5 * C;
     float *colsum = reinterpret_cast<float *>(smem + L::T0);
-    float *rowv = reinterpret_cast<float *>(smem + L::V0), *xv = rowv + C, *diag = xv + C, *sds = diag + C;
+    float *rowv = reinterpret_cast<float *>(smem + L::V0), *xv = rowv + 2 * C, *diag = xv + 2 * C;
+    float *sds = reinterpret_cast<float *>(smem + L::D0);
 
+    {
+        const int row = 16 * r + l16;
+        const bool valid = row < clen;
 #pragma unroll
-    for (int t = 0; t < K2; ++t) {
-        const int e0 = 32 * t + 8 * q4;
-        row_put_frag<BF, L::RB>(K, row, e0, mem_frag<BF>(p.k, (tok + row) * p.ldk + hk * DK + e0, valid));
-        row_put_frag<BF, L::RB>(Q, row, e0, mem_frag<BF>(p.q, (tok + row) * p.ldq + hk * DK + e0, valid));
+        for (int t = 0; t < T2; ++t) {
+            const int e0 = 32 * (T2 * hf + t) + 8 * q4;
+            row_put_frag<BF, L::RB>(K, row, e0, mem_frag<BF>(p.k, (tok + row) * p.ldk + hk * DK + e0, valid));
+            row_put_frag<BF, L::RB>(Q, row, e0, mem_frag<BF>(p.q, (tok + row) * p.ldq + hk * DK + e0, valid));
+        }
     }
-    f32x4 dq[KT], dk[KT];
+    f32x4 dq[2 * T2], dk[2 * T2];
 #pragma unroll
-    for (int ct = 0; ct < KT; ++ct) dq[ct] = dk[ct] = zero4();
-    // loops over the channel tiles run in pairs, so that not all their operands are loaded at once
-    auto pair_end = [] { __builtin_amdgcn_sched_barrier(0); };
+    for (int i = 0; i < 2 * T2; ++i) dq[i] = dk[i] = zero4();
+    // loops over the channel tiles end here, so that the operands of one tile are loaded at a time
+    auto tile_end = [] { __builtin_amdgcn_sched_barrier(0); };
 
 #pragma unroll 1
     for (int g = 0; g < rep; ++g) {
         const int h = hk * rep + g;
         // addresses are formed anew for every head rather than kept in (or spilled from) registers
-        asm volatile("" : "+v"(l16), "+v"(q4));
+        asm volatile("" : "+v"(l16), "+v"(q4), "+v"(tid));
         const int row = 16 * r + l16;
-        auto own_row = [&](const char *m, int t) { return row_frag<BF, L::RB>(m, row, 32 * t + 8 * q4); };
+        const bool valid = row < clen;
         const int64_t vrow = ((tok + row) * p.Hv + h) * DV;
         Frag2<BF> dof[V2], dxf[V2], zf[V2];
 #pragma unroll
@@ -190,39 +228,23 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
             dof[u] = mem_frag<BF>(p.v, vrow + 32 * u + 8 * q4, valid);
             dxf[u] = mem_frag<BF>(gp.dx, vrow + 32 * u + 8 * q4, valid);
         }
-        // S to LDS, <S, dS> on the way; bf16: dS waits in registers for its turn
         constexpr int NP = L::SB / 16 / L::NT;
-        const u32x4 *sp = reinterpret_cast<const u32x4 *>(static_cast<const char *>(gp.hs) + (slot * p.Hv + h) * L::SB);
-        const u32x4 *dp = reinterpret_cast<const u32x4 *>(static_cast<const char *>(gp.dhs) + (slot * p.Hv + h) * L::SB);
-        auto put_state = [&](int i, const u32x4 &v) {
+        const int64_t sat = (slot * p.Hv + h) * (int64_t)L::SB;
+        const u32x4 *sp = reinterpret_cast<const u32x4 *>(static_cast<const char *>(gp.hs) + sat);
+        const u32x4 *dp = reinterpret_cast<const u32x4 *>(static_cast<const char *>(gp.dhs) + sat);
+        auto state_at = [&](int i) {
             const int piece = i * L::NT + tid;
-            *reinterpret_cast<u32x4 *>(buf + row_off<L::RB>(piece / (L::RB / 16), piece % (L::RB / 16) * 16)) = v;
+            return reinterpret_cast<u32x4 *>(buf + mix_off<L::RB>(piece / (L::RB / 16), piece % (L::RB / 16) * 16));
         };
-        u32x4 held[BF ? NP : 1];
-        float ss = 0.f;
-        if constexpr (BF) {
+        {
             u32x4 sv[NP];
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                sv[i] = sp[i * L::NT + tid];
-                held[i] = dp[i * L::NT + tid];
-            }
+            for (int i = 0; i < NP; ++i) sv[i] = sp[i * L::NT + tid];
             if (g > 0) __syncthreads();  // the last head's reads of the buffer
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                put_state(i, sv[i]);
-                ss = dot16<BF>(sv[i], held[i], ss);
-            }
-        } else {
-            if (g > 0) __syncthreads();
-#pragma unroll 4
-            for (int i = 0; i < NP; ++i) {
-                const u32x4 v = sp[i * L::NT + tid];
-                put_state(i, v);
-                ss = dot16<BF>(v, dp[i * L::NT + tid], ss);
-            }
+            for (int i = 0; i < NP; ++i) *state_at(i) = sv[i];
         }
-        if (r == 0) {
+        if (wave == 0) {
             Walk w;
             w.tok0 = tok;
             w.len = clen;
@@ -244,84 +266,88 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
                 }
             }
         }
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) ss += __shfl_xor(ss, off);
-        if (lane == 0) sds[r] = ss;
         __syncthreads();
-        const float up = gate[row], down = gate[C + row], bet = gate[2 * C + row];
-        const float eG = up * fac[r], eB = down * fac[4 + r];
+        const float up = gate[row], bet = gate[2 * C + row];
+        const float eG = up * fac[r], eB = gate[C + row] * fac[4 + r];
         // the parts through the state entering the chunk
         float rowsum = 0.f, xk = 0.f;
 #pragma unroll
-        for (int t = 0; t < K2; ++t) {
-            const Frag2<BF> kr = own_row(K, t), qr = own_row(Q, t);
-            f32x4 r1[2], r2[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) r1[i] = r2[i] = zero4();
-#pragma unroll
-            for (int u = 0; u < V2; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const Frag2<BF> a = col_frag8<BF, L::RB>(buf, 2 * t + i, u, l16, q4);
-                    mma<BF>(r1[i], a, dof[u]);
-                    mma<BF>(r2[i], a, dxf[u]);
-                }
+        for (int t = 0; t < T2; ++t) {
+            const int e0 = 32 * (T2 * hf + t) + 8 * q4;
+            const Frag2<BF> kr = mix_frag<BF, L::RB>(K, row, e0), qr = mix_frag<BF, L::RB>(Q, row, e0);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                r1[i] = r1[i] * (eG * p.scale);
-                r2[i] = r2[i] * -eG;
-                rowsum = dot4<BF>(frag_f32<BF>(i ? qr.b : qr.a), r1[i], rowsum);
-                rowsum = dot4<BF>(frag_f32<BF>(i ? kr.b : kr.a), r2[i], rowsum);
-                dq[2 * t + i] = dq[2 * t + i] + r1[i];
-                dk[2 * t + i] = dk[2 * t + i] + r2[i];
+                f32x4 r1 = zero4(), r2 = zero4();
+#pragma unroll
+                for (int u = 0; u < V2; ++u) {
+                    const Frag2<BF> a = col_frag8<BF, L::RB>(buf, 2 * (T2 * hf + t) + i, u, l16, q4);
+                    mma<BF>(r1, a, dof[u]);
+                    mma<BF>(r2, a, dxf[u]);
+                }
+                r1 = r1 * (eG * p.scale);
+                r2 = r2 * -eG;
+                rowsum = dot4(frag_f32<BF>(i ? qr.b : qr.a), r1, rowsum);
+                rowsum = dot4(frag_f32<BF>(i ? kr.b : kr.a), r2, rowsum);
+                dq[2 * t + i] = dq[2 * t + i] + r1;
+                dk[2 * t + i] = dk[2 * t + i] + r2;
+                tile_end();
             }
-            pair_end();
+        }
+        // dS takes the place of S; a thread stores where it stored before and meets its pieces of S there
+        float ss = 0.f;
+        {
+            u32x4 dv[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) dv[i] = dp[i * L::NT + tid];
+#pragma unroll
+            for (int u = 0; u < V2; ++u) zf[u] = mem_frag<BF>(gp.zs, vrow + 32 * u + 8 * q4, valid);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                u32x4 *at = state_at(i);
+                ss = dot16<BF>(*at, dv[i], ss);
+                *at = dv[i];
+            }
         }
 #pragma unroll
-        for (int u = 0; u < V2; ++u) zf[u] = mem_frag<BF>(gp.zs, vrow + 32 * u + 8 * q4, valid);
-        __syncthreads();
-        if constexpr (BF) {
-#pragma unroll
-            for (int i = 0; i < NP; ++i) put_state(i, held[i]);
-        } else {
-#pragma unroll 4
-            for (int i = 0; i < NP; ++i) put_state(i, dp[i * L::NT + tid]);
-        }
+        for (int off = 32; off >= 1; off >>= 1) ss += __shfl_xor(ss, off);
+        if (lane == 0) sds[wave] = ss;
         __syncthreads();
         // the part through the state leaving it
 #pragma unroll
-        for (int t = 0; t < K2; ++t) {
-            const Frag2<BF> kr = own_row(K, t);
-            f32x4 r3[2] = {zero4(), zero4()};
-#pragma unroll
-            for (int u = 0; u < V2; ++u)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) mma<BF>(r3[i], col_frag8<BF, L::RB>(buf, 2 * t + i, u, l16, q4), zf[u]);
+        for (int t = 0; t < T2; ++t) {
+            const Frag2<BF> kr = mix_frag<BF, L::RB>(K, row, 32 * (T2 * hf + t) + 8 * q4);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                r3[i] = r3[i] * eB;
-                xk = dot4<BF>(frag_f32<BF>(i ? kr.b : kr.a), r3[i], xk);
-                dk[2 * t + i] = dk[2 * t + i] + r3[i] * bet;
+                f32x4 r3 = zero4();
+#pragma unroll
+                for (int u = 0; u < V2; ++u)
+                    mma<BF>(r3, col_frag8<BF, L::RB>(buf, 2 * (T2 * hf + t) + i, u, l16, q4), zf[u]);
+                r3 = r3 * eB;
+                xk = dot4(frag_f32<BF>(i ? kr.b : kr.a), r3, xk);
+                dk[2 * t + i] = dk[2 * t + i] + r3 * bet;
+                tile_end();
             }
-            pair_end();
         }
         __syncthreads();
-        // inside the chunk: Z to LDS, then the 16 x 16 tiles of row tile r
+        // inside the chunk: Z to LDS, then the 16 x 16 tiles of row tile r, shared between its two waves
 #pragma unroll
-        for (int u = 0; u < V2; ++u) row_put_frag<BF, L::ZRB>(buf, row, 32 * u + 8 * q4, zf[u]);
+        for (int u = 0; u < V2; ++u)
+            if ((u & 1) == hf) row_put_frag<BF, L::ZRB>(buf, row, 32 * u + 8 * q4, zf[u]);
         __syncthreads();
 #pragma unroll 1
-        for (int c = 0; c <= r; ++c) {
+        for (int c = hf; c <= r; c += 2) {
             f32x4 kk = zero4(), qk = zero4(), w1 = zero4(), w2 = zero4();
 #pragma unroll
             for (int t = 0; t < K2; ++t) {
-                const Frag2<BF> kc = row_frag<BF, L::RB>(K, 16 * c + l16, 32 * t + 8 * q4);
-                mma<BF>(kk, kc, own_row(K, t));
-                mma<BF>(qk, kc, own_row(Q, t));
+                const Frag2<BF> kc = mix_frag<BF, L::RB>(K, 16 * c + l16, 32 * t + 8 * q4);
+                mma<BF>(kk, kc, mix_frag<BF, L::RB>(K, row, 32 * t + 8 * q4));
+                mma<BF>(qk, kc, mix_frag<BF, L::RB>(Q, row, 32 * t + 8 * q4));
             }
+            tile_end();
 #pragma unroll
             for (int u = 0; u < V2; ++u) {
-                const Frag2<BF> zc = row_frag<BF, L::ZRB>(buf, 16 * c + l16, 32 * u + 8 * q4);
+                const Frag2<BF> zc = mix_frag<BF, L::ZRB>(buf, 16 * c + l16, 32 * u + 8 * q4);
                 mma<BF>(w1, zc, dof[u]);
                 mma<BF>(w2, zc, dxf[u]);
             }
@@ -352,9 +378,7 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
                 rowsum = fmaf(b4[e], t[e], rowsum);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {  // over the tile's 16 rows: the last lane of 16 has the sum
-                t[e] = scan16_add(t[e]);
-            }
+            for (int e = 0; e < 4; ++e) t[e] = scan16_add(t[e]);  // over the tile's rows: the last of 16 lanes has it
             if (l16 == 15) *reinterpret_cast<f32x4 *>(colsum + r * C + j0) = t;
             row_put4<BF, L::MRB>(E1, row, j0, e1[0], e1[1], e1[2], e1[3]);
             row_put4<BF, L::MRB>(H, row, j0, f1[0], f1[1], f1[2], f1[3]);
@@ -364,14 +388,14 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
                 if (c < r || row > j0 + e) row_put1<BF, L::MRB>(H, j0 + e, row, f1[e]);
             wave_lds_sync();
         }
-        if ((r & 1) == 0) row_put4<BF, L::MRB>(E1, row, 16 * (r + 1) + 4 * q4, 0.f, 0.f, 0.f, 0.f);
+        if ((r & 1) == 0 && hf == 0) row_put4<BF, L::MRB>(E1, row, 16 * (r + 1) + 4 * q4, 0.f, 0.f, 0.f, 0.f);
         rowsum += __shfl_xor(rowsum, 16);
         rowsum += __shfl_xor(rowsum, 32);
         xk += __shfl_xor(xk, 16);
         xk += __shfl_xor(xk, 32);
         if (q4 == 0) {
-            rowv[row] = rowsum;
-            xv[row] = xk;
+            rowv[hf * C + row] = rowsum;
+            xv[hf * C + row] = xk;
         }
         __syncthreads();
         Frag2<BF> er[RT / 2], hr[RT / 2], ec[RT / 2];
@@ -385,37 +409,38 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
         auto products = [&](auto second) {
             constexpr int R2 = decltype(second)::value;
 #pragma unroll
-            for (int ct = 0; ct < KT; ++ct) {
+            for (int i = 0; i < 2 * T2; ++i) {
+                const int ct = 2 * T2 * hf + i;
 #pragma unroll
                 for (int u = 0; u < RT / 2; ++u) {
                     const Frag2<BF> kt = col_frag8<BF, L::RB>(K, ct, u, l16, q4);
-                    if (u <= R2) mma<BF>(dq[ct], kt, er[u]);
-                    mma<BF>(dk[ct], kt, hr[u]);
-                    if (u >= R2) mma<BF>(dk[ct], col_frag8<BF, L::RB>(Q, ct, u, l16, q4), ec[u]);
+                    if (u <= R2) mma<BF>(dq[i], kt, er[u]);
+                    mma<BF>(dk[i], kt, hr[u]);
+                    if (u >= R2) mma<BF>(dk[i], col_frag8<BF, L::RB>(Q, ct, u, l16, q4), ec[u]);
                 }
-                if (ct & 1) pair_end();
+                tile_end();
             }
         };
         if (RT > 2 && r >= 2) products(std::integral_constant<int, 1>{});
         else products(std::integral_constant<int, 0>{});
 #pragma unroll
-        for (int ct = 0; ct < KT; ++ct) mfma_settle(dq[ct], dk[ct]);
-        if (r == 0) {
+        for (int i = 0; i < 2 * T2; ++i) mfma_settle(dq[i], dk[i]);
+        if (wave == 0) {
             // gates' gradients, lane = token
             float dG = 0.f, db = 0.f, bx = 0.f;
             if (lane < C) {
                 float cs = 0.f;
                 for (int rr = lane >> 4; rr < RT; ++rr) cs += colsum[rr * C + lane];
-                const float b = gate[2 * C + lane];
-                db = cs + diag[lane] + xv[lane];
-                bx = b * xv[lane];
-                dG = rowv[lane] - b * cs - bx;
+                const float b = gate[2 * C + lane], x = xv[lane] + xv[C + lane];
+                db = cs + diag[lane] + x;
+                bx = b * x;
+                dG = rowv[lane] + rowv[C + lane] - b * cs - bx;
             }
             float end = bx;
 #pragma unroll
             for (int off = 32; off >= 1; off >>= 1) end += __shfl_xor(end, off);
             float sd = 0.f;
-            for (int i = 0; i < RT; ++i) sd += sds[i];
+            for (int i = 0; i < 2 * RT; ++i) sd += sds[i];
             if (lane == C - 1) dG += fmaf(fac[11], sd, end);
 #pragma unroll
             for (int off = 1; off < 64; off <<= 1) {
@@ -434,14 +459,14 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
             }
         }
     }
-    if (valid) {
-        IO *oq = static_cast<IO *>(gp.dq) + ((tok + row) * p.Hk + hk) * DK + 8 * q4;
-        IO *ok = static_cast<IO *>(gp.dk) + ((tok + row) * p.Hk + hk) * DK + 8 * q4;
+    const int row = 16 * r + l16;
+    if (row < clen) {
+        const int64_t at = ((tok + row) * p.Hk + hk) * DK + 32 * T2 * hf + 8 * q4;
+        IO *oq = static_cast<IO *>(gp.dq) + at, *ok = static_cast<IO *>(gp.dk) + at;
 #pragma unroll
-        for (int ct = 0; ct < KT; ++ct) {
-            const int at = 32 * (ct >> 1) + 4 * (ct & 1);
-            IoTraits<IO>::store4(oq + at, make_float4(dq[ct][0], dq[ct][1], dq[ct][2], dq[ct][3]));
-            IoTraits<IO>::store4(ok + at, make_float4(dk[ct][0], dk[ct][1], dk[ct][2], dk[ct][3]));
+        for (int t = 0; t < T2; ++t) {
+            put_row8<BF>(oq + 32 * t, dq[2 * t], dq[2 * t + 1]);
+            put_row8<BF>(ok + 32 * t, dk[2 * t], dk[2 * t + 1]);
         }
     }
 }
