@@ -32,10 +32,14 @@
 // result is subtracted (one more product on the chain, but two levels of block products and their
 // roundings less per chunk).
 //
-// Roundings to bf16 (bf16 io only; fp32 io runs the same code on fp32 operands and 32-token
-// chunks): the operands of the products that are not inputs (S, X, Z, Y, the strictly lower part of
-// the inverse, M B and P).  The unit diagonal of the inverse is applied in fp32, sums and the state
-// are fp32, cumulative gates fp64 (their differences stay exact behind a strong gate).
+// Roundings to bf16 (bf16 io only; fp32 io runs the same code on fp32 operands and 32-token chunks): the
+// operands of the products that are not inputs (S, X, Z, Y, the strictly lower part of the inverse,
+// M B and P).  The forward takes P as two bf16 terms, made and used by waves that have the time: error of
+// the output 2.3e-3 of its norm, 1.7e-3 of it the output's own rounding, where one term gives 2.9e-3.
+// X, Z and Y as two terms as well would leave the output's rounding alone (1.7e-3), but the chain
+// would wait for it: 2.57 us per chunk instead of 2.12.  The unit diagonal of the inverse is applied in
+// fp32, sums and the state are fp32, cumulative gates fp64 (their differences stay exact behind a
+// strong gate).
 #pragma once
 
 #include <type_traits>
@@ -60,6 +64,11 @@ struct Frag2 {
 template <bool BF>
 __device__ __forceinline__ void mma(f32x4 &acc, const Frag2<BF> &x, const Frag2<BF> &y) {
     mma32(acc, x.a, x.b, y.a, y.b);
+}
+
+// The rounding error of a bf16 operand, as an operand: hi + lo has 16 bits of each value.
+__device__ __forceinline__ Frag<true> frag_lo(const f32x4 &x, const Frag<true> &hi) {
+    return make_frag<true>(x[0] - bf16_lo(hi.v.x), x[1] - bf16_hi(hi.v.x), x[2] - bf16_lo(hi.v.y), x[3] - bf16_hi(hi.v.y));
 }
 
 // Position of index i (0..31) in a stored row of 32 contraction indices: a lane's eight values
@@ -156,6 +165,8 @@ struct Lds {
     static constexpr int KB = C * RB, QB = MODE == kKeep ? 0 : KB, VB = C * VRB, SB = KB + QB + VB;
     static constexpr int NBUF = 3;
     static constexpr int LS = 36;  // row stride of the fp32 blocks (floats)
+    // P, two buffers: forward in bf16 the two terms of one chunk's, else two chunks'
+    static constexpr bool PLO = BF && MODE == kFwd;
     static constexpr int P0 = NBUF * SB;
     static constexpr int PB = MODE == kKeep ? 0 : C * PRB;
     static constexpr int N0 = P0 + 2 * PB, NB = 32 * NRB;
@@ -235,110 +246,166 @@ __device__ __forceinline__ void issue_loads() {
     if constexpr (BF) __builtin_amdgcn_sched_barrier(0);
 }
 
-// A tile wave's 16 x 16 tiles of one 32 x 32 block (RB, CB) of the decayed K K^T (KK: scaled by beta into
-// M B) or of Q K^T (QK), its row tiles I0 .. I1 - 1.  Forward: rows of the stored matrices are the tokens i that are solved for;
-// reverse: transposed.  Below the diagonal tiles the decays are products of three stored factors, all
-// at most 1 (row token from its tile's start, between the tiles, column token to its tile's end);
-// inside a diagonal tile they are formed from differences of the cumulative gates, kept as two floats.
-template <bool BF, int DK, int CT, int MODE, int RB, int CB, bool KK, bool QK, int I0 = 0, int I1 = 2>
-__device__ __forceinline__ void make_tiles(char *smem, int buf, int par, int abuf, float scale, int l16, int q4) {
+// Decays inside diagonal tile r of the chunk whose cumulative gates are in LDS, as a lane's entries of make_tiles.
+template <bool BF, int DK, int CT, int MODE>
+__device__ __forceinline__ f32x4 diag_decay(const char *smem, int r, int l16, int q4) {
+    using L = Lds<BF, DK, CT, MODE>;
+    const float *Gh = reinterpret_cast<const float *>(smem + L::G0) + 16 * r, *Gl = Gh + L::C;
+    const float ho = Gh[l16], lo = Gl[l16];
+    const f32x4 h4 = load_f4(Gh + 4 * q4), l4 = load_f4(Gl + 4 * q4);
+    f32x4 gam;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool low = MODE == kRev ? 4 * q4 + e >= l16 : l16 >= 4 * q4 + e;
+        const float d = (ho - h4[e]) + (lo - l4[e]);
+        gam[e] = low ? fast_exp2(MODE == kRev ? -d : d) : 0.f;
+    }
+    return gam;
+}
+
+// Decay of tile (r, c) as a lane's four entries: forward (i, j) = (16 r + l16, 16 c + 4 q4 + e), reverse
+// (16 r + 4 q4 + e, 16 c + l16).  Below the diagonal it is a product of three stored factors, all at most 1
+// (row token from its tile's start, between the tiles, column token to its tile's end); inside a
+// diagonal tile it is formed from differences of the cumulative gates, kept as two floats.
+template <bool BF, int DK, int CT, int MODE>
+__device__ __forceinline__ f32x4 tile_decay(const char *smem, const float *gate, int r, int c, int l16, int q4) {
+    using L = Lds<BF, DK, CT, MODE>;
+    constexpr bool REV = MODE == kRev;
+    if (r == c) return diag_decay<BF, DK, CT, MODE>(smem, r, l16, q4);
+    const float *up = gate + 16 * r, *down = gate + L::C + 16 * c, *between = gate + 3 * L::C + 8;
+    const float f = r - c == 1 ? 1.f : between[r - c == 3 ? 2 : c];
+    return load_f4((REV ? up : down) + 4 * q4) * ((REV ? down : up)[l16] * f);
+}
+
+// A wave's 16 x 16 tiles of the 32 x 32 block (RB, CB) of M B: the decayed K K^T, its columns scaled by beta.
+// Forward: rows of the stored matrices are the tokens i that are solved for; reverse: transposed.
+template <bool BF, int DK, int CT, int MODE, int RB, int CB>
+__device__ __forceinline__ void make_tiles(char *smem, int buf, int par, int abuf, int l16, int q4) {
     using L = Lds<BF, DK, CT, MODE>;
     constexpr bool REV = MODE == kRev, DIAG = RB == CB;
-    const char *K = smem + buf * L::SB, *Q = K + L::KB;
-    char *P = smem + L::P0 + par * L::PB;
-    const float *Gh = reinterpret_cast<const float *>(smem + L::G0), *Gl = Gh + L::C;
-    const float *gate = reinterpret_cast<const float *>(smem + L::A0 + abuf * L::AB);
-    const float *up = gate, *down = gate + L::C, *beta = gate + 2 * L::C, *between = gate + 3 * L::C + 8;
-    Frag2<BF> kr[2][DK / 32], qr[2][DK / 32], kc[2][DK / 32];
+    const char *K = smem + buf * L::SB;
+    const float *gate = reinterpret_cast<const float *>(smem + L::A0 + abuf * L::AB), *beta = gate + 2 * L::C;
+    Frag2<BF> kr[2][DK / 32], kc[2][DK / 32];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int t = 0; t < DK / 32; ++t) {
-            if (DIAG || (KK && i >= I0 && i < I1))
-                kr[i][t] = row_frag<BF, L::RB>(K, 32 * RB + 16 * i + l16, 32 * t + 8 * q4);
-            if (QK && i >= I0 && i < I1)
-                qr[i][t] = row_frag<BF, L::RB>(Q, 32 * RB + 16 * i + l16, 32 * t + 8 * q4);
+            kr[i][t] = row_frag<BF, L::RB>(K, 32 * RB + 16 * i + l16, 32 * t + 8 * q4);
             if constexpr (!DIAG) kc[i][t] = row_frag<BF, L::RB>(K, 32 * CB + 16 * i + l16, 32 * t + 8 * q4);
         }
-    // a lane's entries: forward (i, j) = (16 r + l16, 16 c + 4 q4 + e), reverse (16 r + 4 q4 + e, 16 c + l16)
-    f32x4 gam[2][2], bet[2];
+    f32x4 gam[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const float *bj = beta + 16 * (2 * CB + j);
-        if constexpr (REV) bet[j] = f32x4{bj[l16], bj[l16], bj[l16], bj[l16]};
-        else bet[j] = load_f4(bj + 4 * q4);
+        const f32x4 bet = REV ? f32x4{bj[l16], bj[l16], bj[l16], bj[l16]} : load_f4(bj + 4 * q4);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = 2 * RB + i, c = 2 * CB + j;
-            if (c > r || i < I0 || i >= I1) continue;
-            const int own = REV ? 16 * c + l16 : 16 * r + l16, four = (REV ? 16 * r : 16 * c) + 4 * q4;
-            if (c == r) {
-                const float ho = Gh[own], lo = Gl[own];
-                const f32x4 h4 = load_f4(Gh + four), l4 = load_f4(Gl + four);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool low = REV ? four + e >= own : own >= four + e;
-                    const float d = REV ? (h4[e] - ho) + (l4[e] - lo) : (ho - h4[e]) + (lo - l4[e]);
-                    gam[i][j][e] = low ? fast_exp2(d) : 0.f;
-                }
-            } else {
-                const float f = r - c == 1 ? 1.f : between[r - c == 3 ? 2 : c];
-                gam[i][j] = load_f4((REV ? up : down) + four) * ((REV ? down : up)[own] * f);
-            }
-        }
+        for (int i = 0; i < 2; ++i)
+            if (2 * CB + j <= 2 * RB + i)
+                gam[i][j] = tile_decay<BF, DK, CT, MODE>(smem, gate, 2 * RB + i, 2 * CB + j, l16, q4) * bet;
     }
     issue_loads<BF>();
-    f32x4 kk[2][2], qk[2][2];
+    f32x4 kk[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) kk[i][j] = qk[i][j] = zero4();
+        for (int j = 0; j < 2; ++j) kk[i][j] = zero4();
 #pragma unroll
     for (int t = 0; t < DK / 32; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (2 * CB + j > 2 * RB + i || i < I0 || i >= I1) continue;
+                if (2 * CB + j > 2 * RB + i) continue;
                 const Frag2<BF> y = DIAG ? kr[j][t] : kc[j][t];
-                if constexpr (KK) {
-                    if constexpr (REV) mma<BF>(kk[i][j], kr[i][t], y);
-                    else mma<BF>(kk[i][j], y, kr[i][t]);
-                }
-                if constexpr (QK) {
-                    if constexpr (REV) mma<BF>(qk[i][j], qr[i][t], y);
-                    else mma<BF>(qk[i][j], y, qr[i][t]);
-                }
+                if constexpr (REV) mma<BF>(kk[i][j], kr[i][t], y);
+                else mma<BF>(kk[i][j], y, kr[i][t]);
             }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int r = 2 * RB + i, c = 2 * CB + j;
-            if (c > r || i < I0 || i >= I1) continue;
+            if (c > r) continue;
             const int own = REV ? 16 * c + l16 : 16 * r + l16, four = (REV ? 16 * r : 16 * c) + 4 * q4;
-            if constexpr (KK) {
-                f32x4 m = kk[i][j] * gam[i][j] * bet[j];
-                if constexpr (DIAG) {
-                    if (c == r) {
+            f32x4 m = kk[i][j] * gam[i][j];
+            if constexpr (DIAG) {
+                if (c == r) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) m[e] = own == four + e ? 0.f : m[e];
-                    }
-                    float *dst = reinterpret_cast<float *>(smem + L::F0) + RB * 32 * L::LS;
-                    if constexpr (REV) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) dst[((four + e) & 31) * L::LS + (own & 31)] = m[e];
-                    } else {
-                        *reinterpret_cast<f32x4 *>(dst + (own & 31) * L::LS + (four & 31)) = m;
-                    }
-                } else {
-                    row_put4<BF, L::NRB>(smem + L::L0 + par * L::LB, own & 31, kpos(four & 31), -m[0], -m[1], -m[2], -m[3]);
+                    for (int e = 0; e < 4; ++e) m[e] = own == four + e ? 0.f : m[e];
                 }
+                float *dst = reinterpret_cast<float *>(smem + L::F0) + RB * 32 * L::LS;
+                if constexpr (REV) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dst[((four + e) & 31) * L::LS + (own & 31)] = m[e];
+                } else {
+                    *reinterpret_cast<f32x4 *>(dst + (own & 31) * L::LS + (four & 31)) = m;
+                }
+            } else {
+                row_put4<BF, L::NRB>(smem + L::L0 + par * L::LB, own & 31, kpos(four & 31), -m[0], -m[1], -m[2], -m[3]);
             }
-            if constexpr (QK) {
-                f32x4 m = qk[i][j] * gam[i][j];
-                if constexpr (REV) m = m * scale;
-                row_put4<BF, L::PRB>(P, own, (four & ~31) + kpos(four & 31), m[0], m[1], m[2], m[3]);
+        }
+}
+
+// The tiles of P of wave W of three.  64 tokens: (0,0) (1,0) (1,1) (2,0), then (2,1) (2,2) (3,2) (3,3), and (3,0)
+// (3,1) by the wave below the diagonal; 32 tokens: all by the first.
+template <int RT, int W>
+__device__ __forceinline__ constexpr bool owns_tile(int r, int c) {
+    if (c > r || RT == 2) return c <= r && W == 0;
+    return W == (r == 3 && c < 2 ? 2 : r < 2 || (r == 2 && c == 0) ? 0 : 1);
+}
+// Forward: P, in bf16 as two terms, with the diagonal tiles' decays in diag; reverse: scale P^T.
+template <bool BF, int DK, int CT, int MODE, int W>
+__device__ __forceinline__ void make_p(char *smem, int buf, int par, int abuf, float scale, const f32x4 (&diag)[2],
+                                       int l16, int q4) {
+    using L = Lds<BF, DK, CT, MODE>;
+    constexpr bool REV = MODE == kRev;
+    constexpr int RT = L::RT, R0 = W == 0 ? 0 : W + 1, R1 = W == 0 ? (RT == 2 ? 2 : 3) : 4;  // its rows and
+    constexpr int C0 = W == 1 ? 1 : 0, C1 = W == 1 ? 4 : 2;                                  // columns of tiles
+    const char *K = smem + buf * L::SB, *Q = K + L::KB;
+    char *P = smem + L::P0 + par * L::PB;
+    const float *gate = reinterpret_cast<const float *>(smem + L::A0 + abuf * L::AB);
+    Frag2<BF> qr[R1 - R0][DK / 32], kc[C1][DK / 32];
+    f32x4 gam[R1 - R0][C1], acc[R1 - R0][C1];
+#pragma unroll
+    for (int t = 0; t < DK / 32; ++t) {
+#pragma unroll
+        for (int r = R0; r < R1; ++r) qr[r - R0][t] = row_frag<BF, L::RB>(Q, 16 * r + l16, 32 * t + 8 * q4);
+#pragma unroll
+        for (int c = C0; c < C1; ++c) kc[c][t] = row_frag<BF, L::RB>(K, 16 * c + l16, 32 * t + 8 * q4);
+    }
+#pragma unroll
+    for (int r = R0; r < R1; ++r)
+#pragma unroll
+        for (int c = C0; c < C1; ++c)
+            if (owns_tile<RT, W>(r, c)) {
+                gam[r - R0][c] = r == c && MODE == kFwd ? diag[r & 1]
+                                                        : tile_decay<BF, DK, CT, MODE>(smem, gate, r, c, l16, q4);
+                acc[r - R0][c] = zero4();
+            }
+    issue_loads<BF>();
+#pragma unroll
+    for (int t = 0; t < DK / 32; ++t)
+#pragma unroll
+        for (int r = R0; r < R1; ++r)
+#pragma unroll
+            for (int c = C0; c < C1; ++c)
+                if (owns_tile<RT, W>(r, c)) {
+                    if constexpr (REV) mma<BF>(acc[r - R0][c], qr[r - R0][t], kc[c][t]);
+                    else mma<BF>(acc[r - R0][c], kc[c][t], qr[r - R0][t]);
+                }
+#pragma unroll
+    for (int r = R0; r < R1; ++r)
+#pragma unroll
+        for (int c = C0; c < C1; ++c) {
+            if (!owns_tile<RT, W>(r, c)) continue;
+            const int own = REV ? 16 * c + l16 : 16 * r + l16, four = (REV ? 16 * r : 16 * c) + 4 * q4;
+            const int at = (four & ~31) + kpos(four & 31);
+            f32x4 m = acc[r - R0][c] * gam[r - R0][c];
+            if constexpr (REV) m = m * scale;
+            row_put4<BF, L::PRB>(P, own, at, m[0], m[1], m[2], m[3]);
+            if constexpr (L::PLO) {
+                const Frag<true> lo = frag_lo(m, frag_from_acc<true>(m));
+                *reinterpret_cast<uint2 *>(P + L::PB + row_off<L::PRB>(own, 2 * at)) = lo.v;
             }
         }
 }
@@ -718,76 +785,91 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         }
         return;
     }
-#define GDN_TILES(...) \
-    make_tiles<BF, DK, CT, MODE, __VA_ARGS__>(smem, s % L::NBUF, s & 1, s % 3, p.scale, l16, q4)
+#define GDN_TILES(RB_, CB_) make_tiles<BF, DK, CT, MODE, RB_, CB_>(smem, s % L::NBUF, s & 1, s % 3, l16, q4)
     if (wave >= L::QW0 && wave < L::QW0 + 2) {
         // ------------------------------------------------------------------ Q K^T and output waves
         if (nch == 0) return;
         const int cw = wave - L::QW0;
+        // forward: P of the step's own chunk, the decays of its diagonal tiles formed a step ahead (the cumulative
+        // gates in LDS are the next chunk's by then); reverse: P^T of the next chunk
+        f32x4 diag[2];
         auto tiles = [&](int s) {
             if constexpr (MODE != kKeep) {
-                if (cw == 0) GDN_TILES(0, 0, false, true);
+                const int par = MODE == kFwd ? 0 : s & 1;
+                if (cw == 0) make_p<BF, DK, CT, MODE, 0>(smem, s % L::NBUF, par, s % 3, p.scale, diag, l16, q4);
                 if constexpr (L::NBLK == 2) {
-                    if (cw == 0) GDN_TILES(1, 0, false, true, 0, 1);
-                    if (cw == 1) {
-                        GDN_TILES(1, 1, false, true);
-                        GDN_TILES(1, 0, false, true, 1, 2);
-                    }
+                    if (cw == 1) make_p<BF, DK, CT, MODE, 1>(smem, s % L::NBUF, par, s % 3, p.scale, diag, l16, q4);
                 }
             }
         };
+        auto next_diag = [&] {
+            if (MODE == kFwd && cw < L::NBLK) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) diag[i] = diag_decay<BF, DK, CT, MODE>(smem, 2 * cw + i, l16, q4);
+            }
+        };
         __syncthreads();
-        tiles(0);
+        if (MODE == kFwd) next_diag();
+        else tiles(0);
         __syncthreads();
         __syncthreads();
 #pragma unroll 1
         for (int s = 0; s < nch; ++s) {
-            if (s + 1 < nch) tiles(s + 1);
+            if (MODE == kFwd) {
+                tiles(s);
+                if (s + 1 < nch) next_diag();
+            } else if (s + 1 < nch) {
+                tiles(s + 1);
+            }
             __syncthreads();  // A
             if constexpr (MODE == kFwd) {
-            const int clen = min(C, w.len - s * C);
-            const char *hand = smem + L::H0 + cw * L::HB;
-            const char *Q = smem + (s % L::NBUF) * L::SB + L::KB, *P = smem + L::P0 + (s & 1) * L::PB;
-            const float *gate = reinterpret_cast<const float *>(smem + L::A0 + (s % 3) * L::AB);
-            IO *out = static_cast<IO *>(p.out) + ((w.tok0 + (int64_t)s * C) * p.Hv + w.h) * p.dv + w.col0 + 16 * cw + 4 * q4;
-            Frag2<BF> qf[RT][K2], pf[RT][RT / 2];
-            float e[RT];
+                const int clen = min(C, w.len - s * C);
+
+                const char *hand = smem + L::H0 + cw * L::HB;
+                const char *Q = smem + (s % L::NBUF) * L::SB + L::KB, *P = smem + L::P0;
+                const float *gate = reinterpret_cast<const float *>(smem + L::A0 + (s % 3) * L::AB);
+                IO *out = static_cast<IO *>(p.out) + ((w.tok0 + (int64_t)s * C) * p.Hv + w.h) * p.dv + w.col0 + 16 * cw + 4 * q4;
+                Frag2<BF> qf[RT][K2], pf[RT][RT / 2];
+                float e[RT];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
+                for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-                for (int t = 0; t < K2; ++t) qf[rt][t] = row_frag<BF, L::RB>(Q, 16 * rt + l16, 32 * t + 8 * q4);
+                    for (int t = 0; t < K2; ++t) qf[rt][t] = row_frag<BF, L::RB>(Q, 16 * rt + l16, 32 * t + 8 * q4);
 #pragma unroll
-                for (int u = 0; u <= rt / 2; ++u) pf[rt][u] = row_frag<BF, L::PRB>(P, 16 * rt + l16, 32 * u + 8 * q4);
-                e[rt] = gate[16 * rt + l16] * gate[3 * C + rt];
-            }
-            Frag2<BF> sb[K2], yp[RT / 2];
+                    for (int u = 0; u <= rt / 2; ++u) pf[rt][u] = row_frag<BF, L::PRB>(P, 16 * rt + l16, 32 * u + 8 * q4);
+                    e[rt] = gate[16 * rt + l16] * gate[3 * C + rt];
+                }
+                Frag2<BF> sb[K2], yp[RT / 2];
 #pragma unroll
-            for (int t = 0; t < K2; ++t) sb[t] = hand_get<BF>(hand, t, lane);
+                for (int t = 0; t < K2; ++t) sb[t] = hand_get<BF>(hand, t, lane);
 #pragma unroll
-            for (int u = 0; u < RT / 2; ++u) yp[u] = hand_get<BF>(hand + L::HS, u, lane);
-            issue_loads<BF>();
-            // O^T tiles: a lane holds four consecutive columns of one token
-            f32x4 o[RT];
+                for (int u = 0; u < RT / 2; ++u) yp[u] = hand_get<BF>(hand + L::HS, u, lane);
+                issue_loads<BF>();
+                // O^T tiles: a lane holds four consecutive columns of one token
+                f32x4 o[RT];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) o[rt] = zero4();
+                for (int rt = 0; rt < RT; ++rt) o[rt] = zero4();
 #pragma unroll
-            for (int t = 0; t < K2; ++t)
+                for (int t = 0; t < K2; ++t)
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) mma<BF>(o[rt], sb[t], qf[rt][t]);
+                    for (int rt = 0; rt < RT; ++rt) mma<BF>(o[rt], sb[t], qf[rt][t]);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) o[rt] = o[rt] * e[rt];
+                for (int rt = 0; rt < RT; ++rt) o[rt] = o[rt] * e[rt];
 #pragma unroll
-            for (int u = 0; u < RT / 2; ++u)
+                for (int u = 0; u < RT / 2; ++u)
 #pragma unroll
-                for (int rt = 2 * u; rt < RT; ++rt) mma<BF>(o[rt], yp[u], pf[rt][u]);
+                    for (int rt = 2 * u; rt < RT; ++rt) {
+                        mma<BF>(o[rt], yp[u], pf[rt][u]);
+                        if constexpr (L::PLO) mma<BF>(o[rt], yp[u], row_frag<BF, L::PRB>(P + L::PB, 16 * rt + l16, 32 * u + 8 * q4));
+                    }
 #pragma unroll
-            for (int rt = 0; rt < RT; rt += 2) mfma_settle(o[rt], o[rt + 1]);
+                for (int rt = 0; rt < RT; rt += 2) mfma_settle(o[rt], o[rt + 1]);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-                if (16 * rt + l16 < clen)
-                    IoTraits<IO>::store4(out + (int64_t)(16 * rt + l16) * p.Hv * p.dv,
-                                         make_float4(o[rt][0] * p.scale, o[rt][1] * p.scale, o[rt][2] * p.scale,
-                                                     o[rt][3] * p.scale));
+                for (int rt = 0; rt < RT; ++rt)
+                    if (16 * rt + l16 < clen)
+                        IoTraits<IO>::store4(out + (int64_t)(16 * rt + l16) * p.Hv * p.dv,
+                                             make_float4(o[rt][0] * p.scale, o[rt][1] * p.scale, o[rt][2] * p.scale,
+                                                         o[rt][3] * p.scale));
             }
             __syncthreads();  // B
         }
@@ -801,18 +883,28 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         gm.make(0);
         gm.put(0);
         gm.make(1);
+        const f32x4 none[2] = {zero4(), zero4()};
         auto tiles = [&](int s) {
-            if constexpr (L::NBLK == 2) GDN_TILES(1, 0, true, false);
+            if constexpr (L::NBLK == 2) GDN_TILES(1, 0);
+        };
+        auto p_tiles = [&](int s) {
+            if constexpr (L::NBLK == 2 && MODE != kKeep)
+                make_p<BF, DK, CT, MODE, 2>(smem, s % L::NBUF, MODE == kFwd ? 0 : s & 1, s % 3, p.scale, none, l16, q4);
         };
         __syncthreads();
         tiles(0);
+        if (MODE == kRev) p_tiles(0);
         __syncthreads();
         gm.put(1);
         gm.make(2);
         __syncthreads();
 #pragma unroll 1
         for (int s = 0; s < nch; ++s) {
-            if (s + 1 < nch) tiles(s + 1);
+            if (MODE == kFwd) p_tiles(s);
+            if (s + 1 < nch) {
+                tiles(s + 1);
+                if (MODE == kRev) p_tiles(s + 1);
+            }
             __syncthreads();  // A
             gm.put(s + 2);
             gm.make(s + 3);
@@ -826,9 +918,9 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         const int blk = wave - L::KW0;
         Inverse inv;
         auto tiles = [&](int s) {
-            if (blk == 0) GDN_TILES(0, 0, true, false);
+            if (blk == 0) GDN_TILES(0, 0);
             if constexpr (L::NBLK == 2) {
-                if (blk == 1) GDN_TILES(1, 1, true, false);
+                if (blk == 1) GDN_TILES(1, 1);
             }
             if (blk < L::NBLK) solve_diagonals<BF, DK, CT, MODE>(inv, smem, blk, lane);
         };
