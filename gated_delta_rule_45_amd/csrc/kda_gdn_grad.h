@@ -6,20 +6,25 @@
 //     dQ = scale Diag(e^G) dO S^T + E K
 //     dK = -Diag(e^G) dX S^T + Diag(beta e^{G_C - G}) Z dS^T + E^T Q + (F + F^T) K
 //     t_ij = Gam_ij (scale (Q K^T)_ij W1_ij - (K K^T)_ij W2_ij),   x_i = e^{G_C - G_i} k_i . (dS Z_i)
-//     dbeta_j = sum_{i > j} t_ij + scale (q_j . k_j) W1_jj + x_j
+//     dbeta_j = sum_{i > j} t_ij + scale (q_j . k_j) W1_jj + x_j = W2_jj / beta_j
 //     dG_i = sum_{j < i} beta_j t_ij - beta_i sum_{j > i} t_ji + q_i . dQ(state part)_i + k_i . dK(S part)_i - beta_i x_i
 //     dG_C += sum_i beta_i x_i + e^{G_C} <S, dS>,   dg = reverse cumulative sum of dG over the chunk
 //
-// No division (beta = 0 is exact), and the diagonal, where the gate cancels, is left out of dG rather than
-// added and subtracted.
+// dX_j is beta_j times a vector, so the quotient has no cancellation where the sums have (repeated keys: error
+// of dbeta 7e-2 of its norm by the sums, 3e-2 so); the sums serve beta = 0, so every beta has its
+// gradient.  The diagonal, where the gate cancels, is left out of dG rather than added and subtracted.
 //
 // One workgroup owns (chunk, key head) and walks the value heads that share it, so that dQ and dK are
 // summed over them in registers, in a fixed order.  Two waves own the 16 tokens of row tile r, one
 // half of the channels each: dO, dX and Z rows are operand fragments read straight from memory, dQ^T
 // and dK^T stay in accumulators (lane = token, so the gates are lane scalars and 8 consecutive channels
-// leave as 16 bytes).  S, dS, then Z with E and F + F^T take turns in one 32 KB LDS buffer beside K and Q:
-// 70 KB and at most 128 registers, two workgroups per CU, one's loads behind the other's products.
-// Bound: HBM and its latency (reads 9 and writes 2 tensors' rows per chunk).
+// leave as 16 bytes).  S, dS, then Z with E and F + F^T take turns in one 32 KB LDS buffer beside K and Q.
+//
+// Measured, 4 x 4,096 tokens x 16 heads, d = 128, bf16: 252 us, 0.75 GB, so 3.0 TB/s: bound by the latency of
+// a workgroup's chain of loads, products and barriers (16 us), with one workgroup of 8 waves per CU at
+// 253 registers.  Four waves with all channels each spilled (356 us); two workgroups per CU at 128
+// registers spill too (430 to 570 us); dO and dX loaded twice instead of kept 277 us; dS and Z loaded
+// ahead at the start 255 us.
 #pragma once
 
 #include "kda_gdn_scan.h"
@@ -151,8 +156,8 @@ struct GradLds {
     static constexpr int B0 = 2 * KB, BB = SB > ZB + 2 * MB ? SB : ZB + 2 * MB;
     static constexpr int G0 = B0 + BB;                     // up, down, beta, hi, lo [C]; 12 block factors
     static constexpr int T0 = G0 + 5 * C * 4 + 64;         // column sums [RT][C]
-    static constexpr int V0 = T0 + RT * C * 4;             // row terms and x, per channel half, and the diagonal [C]
-    static constexpr int D0 = V0 + 5 * C * 4;              // <S, dS> per wave
+    static constexpr int V0 = T0 + RT * C * 4;             // row terms and x, per channel half, and two diagonals [C]
+    static constexpr int D0 = V0 + 6 * C * 4;              // <S, dS> per wave
     static constexpr int kBytes = D0 + 2 * RT * 4;
 };
 
@@ -195,7 +200,7 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
     char *E1 = buf + L::ZB, *H = E1 + L::MB;
     float *gate = reinterpret_cast<float *>(smem + L::G0), *fac = gate + 5 * C;
     float *colsum = reinterpret_cast<float *>(smem + L::T0);
-    float *rowv = reinterpret_cast<float *>(smem + L::V0), *xv = rowv + 2 * C, *diag = xv + 2 * C;
+    float *rowv = reinterpret_cast<float *>(smem + L::V0), *xv = rowv + 2 * C, *diag = xv + 2 * C, *dxz = diag + C;
     float *sds = reinterpret_cast<float *>(smem + L::D0);
 
     {
@@ -373,7 +378,10 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
                 e1[e] = a * b4[e];
                 f1[e] = strict ? b * b4[e] : 0.f;
                 t[e] = qk[e] * a;
-                if (c == r && row == j0 + e) diag[row] = t[e];
+                if (c == r && row == j0 + e) {
+                    diag[row] = t[e];
+                    dxz[row] = w2[e];
+                }
                 t[e] = strict ? fmaf(kk[e], b, t[e]) : 0.f;
                 rowsum = fmaf(b4[e], t[e], rowsum);
             }
@@ -432,7 +440,7 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
                 float cs = 0.f;
                 for (int rr = lane >> 4; rr < RT; ++rr) cs += colsum[rr * C + lane];
                 const float b = gate[2 * C + lane], x = xv[lane] + xv[C + lane];
-                db = cs + diag[lane] + x;
+                db = b != 0.f ? dxz[lane] / b : cs + diag[lane] + x;
                 bx = b * x;
                 dG = rowv[lane] + rowv[C + lane] - b * cs - bx;
             }

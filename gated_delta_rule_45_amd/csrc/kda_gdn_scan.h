@@ -17,7 +17,7 @@
 // A scalar gate leaves K and Q themselves as the operands of every product (its factors are row
 // scalings of accumulators), so nothing has to be prepared per chunk in memory: one kernel stages
 // K, Q and the value tile of a chunk in LDS and does everything else from there.  Beta multiplies
-// columns of M, so no division by beta appears in the gradients and beta = 0 is exact.
+// columns of M, so that nothing here is divided by beta and beta = 0 is exact.
 //
 // One workgroup owns (sequence, value head, CT state columns); groups of waves run side by side, up to
 // two chunks apart, with two barriers per chunk:

@@ -448,7 +448,7 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
  *  d_initial_state  [num_seqs, Hv, d_k, d_v] state dtype, or NULL to skip it
  *  workspace        kda_gdn_chunk_bwd_workspace() bytes, 256-byte aligned: the states entering the chunks and
  *                   the gradients of those leaving them (bf16 or fp32, the io dtype) and one value tensor
- * No output may overlap anything else.  beta = 0 is exact (nothing is divided by it).  The results repeat
+ * No output may overlap anything else.  beta = 0 has its gradients like any other beta.  The results repeat
  * bit for bit.  Calls that overlap in time need a workspace each.  Errors as for kda_chunk_bwd.
  */
 kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,

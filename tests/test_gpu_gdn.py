@@ -11,6 +11,14 @@ A rounding to bf16 is uniform in half a step, at most 2^-8 of the value: u = 2^-
   relmax: 2e-2, the bar of the library's other bf16 operators
   fp32: 2^-24 per operation, at most 128 + 64 + 64 terms in a row -> 256 * 2^-24 = 1.5e-5: rel2 <= 1.5e-5,
      relmax <= 1e-4 (the bar of the library's other fp32 operators)
+  A tensor stored in bf16 whatever the operands (gates' gradients beside fp32 io): its own rounding, u.
+  One key repeated with beta = 1 (bf16): Y_t = v_t - v_{t-1}, of size sqrt(2) |v|, and the sums over a chunk's 64
+     tokens (O, the state, dQ, dK and what follows from them) telescope to one v, so that 64 independent roundings of
+     Y or Z stand against |v|: sqrt(2 * 64) u = 2.6e-2 in rel2; relmax 4 times that, the largest of some 1e4
+     such sums.  Backwards dX_t = dY_t - dY_{t+1}, where dY_t sums the on average 32 tokens behind t in its chunk
+     and dX_t is one of them: in squares 32 from rounding dZ, 32 from the inverse's entries (near -1), 2 * 32 from
+     P's entries in both terms, 32 from M B between the 32-token blocks: sqrt(160) u = 2.9e-2; the gradients of
+     beta, g and k are products of dX and Z, which carry 160 and 2 * 64 of them: sqrt(288) u = 3.8e-2
   token by token (decode): fp32 arithmetic, one rounding of a bf16 output or state: rel2 <= u = 2.3e-3 (bf16), 1.5e-5
 """
 import math
@@ -56,19 +64,23 @@ def state(n, Hv, dk, dv, dtype, std=0.3, seed=7):
     return (std * torch.randn(n, Hv, dk, dv, generator=torch.Generator().manual_seed(seed))).to(dtype).to(DEV)
 
 
-def check_fwd(x, s0=None, cu=None, scale=1.0, label="", **kw):
+U = 2 ** -8 / math.sqrt(3)
+TELESCOPING, TELESCOPING_BACK = ((math.sqrt(n) * U, 4 * math.sqrt(n) * U) for n in (2 * 64, 160 + 2 * 64))
+
+
+def check_fwd(x, s0=None, cu=None, scale=1.0, label="", bound=None, **kw):
     say(f"[{label}] q={tuple(x[0].shape)} v={tuple(x[2].shape)} {x[0].dtype} gates={x[3].dtype}")
     out, fin = kda.gdn_chunk_fwd(*x, s0, cu, scale=scale, **kw)
     torch.cuda.synchronize()
     o, f = ref.delta_rule(*x, s0, cu, scale)
-    close("out", out, o, *tol(out.dtype))
+    close("out", out, o, *(bound or tol(out.dtype)))
     if fin is not None:
         # an fp32 state of a bf16 call has bf16 products behind it
-        close("final", fin, f, *tol(x[0].dtype))
+        close("final", fin, f, *(bound or tol(x[0].dtype)))
     return out, fin
 
 
-def check_bwd(x, s0=None, dsf=None, cu=None, scale=1.0, label="", seed=11, **kw):
+def check_bwd(x, s0=None, dsf=None, cu=None, scale=1.0, label="", seed=11, bound=None, **kw):
     say(f"[{label}] q={tuple(x[0].shape)} v={tuple(x[2].shape)} {x[0].dtype} gates={x[3].dtype}")
     v = x[2]
     do = torch.randn(v.shape, generator=torch.Generator().manual_seed(seed)).to(v.dtype).to(DEV)
@@ -77,7 +89,10 @@ def check_bwd(x, s0=None, dsf=None, cu=None, scale=1.0, label="", seed=11, **kw)
     want = ref.delta_rule_grads(*x, do, s0, dsf, cu, scale)
     for key, w in want.items():
         if got[key] is not None:
-            close(key, got[key], w, *tol(v.dtype, True, w.numel()))
+            t = tol(v.dtype, True, w.numel())
+            if v.dtype == F32 and got[key].dtype == BF:
+                t = 2.3e-3, 2e-2
+            close(key, got[key], w, *(bound or t))
     return got, do
 
 
@@ -178,7 +193,7 @@ CASES = ["beta0", "some_beta0", "no_decay", "strong", "resets", "same_key", "lon
 @pytest.mark.parametrize("case", CASES)
 def test_forward_gates_and_keys(case, io):
     x = special(case, io)
-    check_fwd(x, state(1, 4, 128, 128, F32), label=case)
+    check_fwd(x, state(1, 4, 128, 128, F32), label=case, bound=TELESCOPING if io == BF and case == "same_key" else None)
 
 
 @pytest.mark.parametrize("io", [BF, F32])
@@ -188,7 +203,7 @@ def test_backward_gates_and_keys(case, io):
     s0, dsf = state(1, 4, 128, 128, F32), state(1, 4, 128, 128, F32, 0.1, 8)
     if case == "resets":  # the reference cannot differentiate e^-inf: a gate that is as good as one
         x[3].clamp_(min=-2000.0)
-    check_bwd(x, s0, dsf, label=case)
+    check_bwd(x, s0, dsf, label=case, bound=TELESCOPING_BACK if io == BF and case == "same_key" else None)
 
 
 @pytest.mark.parametrize("io", [BF, F32])
