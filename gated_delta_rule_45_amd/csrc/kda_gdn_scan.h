@@ -34,12 +34,11 @@
 //
 // Roundings to bf16 (bf16 io only; fp32 io runs the same code on fp32 operands and 32-token chunks): the
 // operands of the products that are not inputs (S, X, Z, Y, the strictly lower part of the inverse,
-// M B and P).  The forward takes P as two bf16 terms, made and used by waves that have the time: error of
-// the output 2.3e-3 of its norm, 1.7e-3 of it the output's own rounding, where one term gives 2.9e-3.
-// X, Z and Y as two terms as well would leave the output's rounding alone (1.7e-3), but the chain
-// would wait for it: 2.57 us per chunk instead of 2.12.  The unit diagonal of the inverse is applied in
-// fp32, sums and the state are fp32, cumulative gates fp64 (their differences stay exact behind a
-// strong gate).
+// M B and P).  The forward takes P and Y as two bf16 terms in P Y, a product of waves that have the time:
+// error of the output 1.8e-3 of its norm, 1.7e-3 of it the output's own rounding, where one term
+// gives 2.9e-3, in the same time.  X, Z and K^T Y with two terms as well would cost the chain 0.3 us a
+// chunk for what is then 1.7e-3.  The unit diagonal of the inverse is applied in fp32, sums and the state
+// are fp32, cumulative gates fp64 (their differences stay exact behind a strong gate).
 #pragma once
 
 #include <type_traits>
@@ -186,13 +185,39 @@ struct Walk {
     int64_t tok0, slot0;
 };
 
+// The sequence of rank r by chunks, most chunks first (ties by index): every thread ranks one sequence.
+// Workgroups start in id order, so the longest chains start first and the short ones fill the end.  Up to
+// kRanked sequences; with more of them the tail is short anyway.
+constexpr int kRanked = 256;
+template <int C>
+__device__ __forceinline__ int ranked_sequence(const GdnParams &p, int r, int *lds) {
+    const int i = threadIdx.x, N = p.num_seqs;
+    auto chunks = [&](int j) { return (p.cu[j + 1] - p.cu[j] + C - 1) / C; };
+    const int own = i < N ? chunks(i) : 0;
+    if (i < kRanked) lds[1 + i] = own;
+    __syncthreads();
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < N; ++j) {
+        const int c = lds[1 + j];
+        rank += c > own || (c == own && j < i);
+    }
+    if (i < N && rank == r) lds[0] = i;
+    __syncthreads();
+    const int n = lds[0];
+    __syncthreads();
+    return n;
+}
+
 template <int C, int CT>
-__device__ __forceinline__ Walk walk_of(const GdnParams &p) {
+__device__ __forceinline__ Walk walk_of(const GdnParams &p, char *smem) {
     Walk w;
     const int ntile = p.dv / CT, rep = p.Hv / p.Hk;
     // the tiles and the value heads that share a key head run next to each other on one XCD
     const SeqItem it = seq_item(blockIdx.x, p.num_seqs, p.Hk, rep * ntile, nullptr);
     w.n = it.n;
+    if (p.cu && p.num_seqs > 1 && p.num_seqs <= kRanked)
+        w.n = __builtin_amdgcn_readfirstlane(ranked_sequence<C>(p, it.n, reinterpret_cast<int *>(smem)));
     w.hk = it.h;
     w.h = it.h * rep + it.tile / ntile;
     w.col0 = (it.tile % ntile) * CT;
@@ -668,8 +693,18 @@ struct GateMaker {
     const Walk &w;
     char *smem;
     int lane;
-    RawGate raw{0.f, 0.f};
+    RawGate raw{0.f, 0.f}, first[3];
     Gates g{};
+    // chunk 0's gates stored, chunk 1's made; chunk 2's are on their way
+    __device__ __forceinline__ void begin() {
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+            if (s < w.nch) first[s] = load_gate<L::C>(p, w, chunk(s), lane);
+        g = make_gates<L::C>(first[0], lane);
+        put(0);
+        if (w.nch > 1) g = make_gates<L::C>(first[1], lane);
+        raw = first[2];
+    }
     __device__ __forceinline__ int chunk(int s) const { return MODE == kRev ? w.nch - 1 - s : s; }
     __device__ __forceinline__ void load(int s) {
         if (s < w.nch) raw = load_gate<L::C>(p, w, chunk(s), lane);
@@ -757,7 +792,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
     __shared__ __attribute__((aligned(16))) char smem[L::kBytes];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, q4 = lane >> 4;
-    const Walk w = walk_of<C, CT>(p);
+    const Walk w = walk_of<C, CT>(p, smem);
     const int nch = w.nch;
     // step s works on chunk ci(s); the reverse scan walks from the last chunk to the first
     auto ci = [&](int s) { return REV ? nch - 1 - s : s; };
@@ -826,6 +861,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
                 const int clen = min(C, w.len - s * C);
 
                 const char *hand = smem + L::H0 + cw * L::HB;
+                [[maybe_unused]] const char *ylo = smem + (s % L::NBUF) * L::SB + L::KB + L::QB + cw * (L::VB / 2);
                 const char *Q = smem + (s % L::NBUF) * L::SB + L::KB, *P = smem + L::P0;
                 const float *gate = reinterpret_cast<const float *>(smem + L::A0 + (s % 3) * L::AB);
                 IO *out = static_cast<IO *>(p.out) + ((w.tok0 + (int64_t)s * C) * p.Hv + w.h) * p.dv + w.col0 + 16 * cw + 4 * q4;
@@ -839,11 +875,14 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
                     for (int u = 0; u <= rt / 2; ++u) pf[rt][u] = row_frag<BF, L::PRB>(P, 16 * rt + l16, 32 * u + 8 * q4);
                     e[rt] = gate[16 * rt + l16] * gate[3 * C + rt];
                 }
-                Frag2<BF> sb[K2], yp[RT / 2];
+                Frag2<BF> sb[K2], yp[RT / 2], yl[RT / 2];
 #pragma unroll
                 for (int t = 0; t < K2; ++t) sb[t] = hand_get<BF>(hand, t, lane);
 #pragma unroll
-                for (int u = 0; u < RT / 2; ++u) yp[u] = hand_get<BF>(hand + L::HS, u, lane);
+                for (int u = 0; u < RT / 2; ++u) {
+                yp[u] = hand_get<BF>(hand + L::HS, u, lane);
+                if constexpr (L::PLO) yl[u] = hand_get<BF>(ylo, u, lane);
+            }
                 issue_loads<BF>();
                 // O^T tiles: a lane holds four consecutive columns of one token
                 f32x4 o[RT];
@@ -860,7 +899,10 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
 #pragma unroll
                     for (int rt = 2 * u; rt < RT; ++rt) {
                         mma<BF>(o[rt], yp[u], pf[rt][u]);
-                        if constexpr (L::PLO) mma<BF>(o[rt], yp[u], row_frag<BF, L::PRB>(P + L::PB, 16 * rt + l16, 32 * u + 8 * q4));
+                        if constexpr (L::PLO) {
+                            mma<BF>(o[rt], yp[u], row_frag<BF, L::PRB>(P + L::PB, 16 * rt + l16, 32 * u + 8 * q4));
+                            mma<BF>(o[rt], yl[u], pf[rt][u]);
+                        }
                     }
 #pragma unroll
                 for (int rt = 0; rt < RT; rt += 2) mfma_settle(o[rt], o[rt + 1]);
@@ -879,10 +921,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         // ------------------------------------------------------------------ block below the diagonal, gates
         if (nch == 0) return;
         GateMaker<BF, DK, CT, MODE> gm{p, w, smem, lane};
-        gm.load(0);
-        gm.make(0);
-        gm.put(0);
-        gm.make(1);
+        gm.begin();
         const f32x4 none[2] = {zero4(), zero4()};
         auto tiles = [&](int s) {
             if constexpr (L::NBLK == 2) GDN_TILES(1, 0);
@@ -948,15 +987,21 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
     const int col = w.col0 + 16 * wave + l16;
     const int64_t sbase = ((int64_t)w.n * p.Hv + w.h) * DK * p.dv + col;
     f32x4 S[KT];
+    // one branch around all the loads: one per value would wait for each (10 us of a workgroup's start)
+    auto load_state = [&](auto *src) {
 #pragma unroll
-    for (int ct = 0; ct < KT; ++ct)
+        for (int ct = 0; ct < KT; ++ct)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t at = sbase + (int64_t)state_channel(ct, q4, j) * p.dv;
-            S[ct][j] = !p.s0 ? 0.f
-                       : p.state_bf16 ? bf16_to_f32(static_cast<const uint16_t *>(p.s0)[at])
-                                      : static_cast<const float *>(p.s0)[at];
-        }
+            for (int j = 0; j < 4; ++j) S[ct][j] = elem_f32(src[sbase + (int64_t)state_channel(ct, q4, j) * p.dv]);
+    };
+    if (!p.s0) {
+#pragma unroll
+        for (int ct = 0; ct < KT; ++ct) S[ct] = zero4();
+    } else if (p.state_bf16) {
+        load_state(static_cast<const uint16_t *>(p.s0));
+    } else {
+        load_state(static_cast<const float *>(p.s0));
+    }
     if (nch > 0) {
         __syncthreads();
         __syncthreads();
@@ -1060,8 +1105,13 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
                         d[h][j] = e[j] * a[h][j];
                     }
                 }
-                if constexpr (MODE == kFwd)
-                    hand_put<BF>(hand + L::HS, u, lane, Frag2<BF>{frag_from_acc<BF>(a[0]), frag_from_acc<BF>(a[1])});
+                if constexpr (MODE == kFwd) {
+                    const Frag2<BF> yp = {frag_from_acc<BF>(a[0]), frag_from_acc<BF>(a[1])};
+                    hand_put<BF>(hand + L::HS, u, lane, yp);
+                    // the second term goes where the chunk's values were, which both chain waves have read
+                    if constexpr (BF)
+                        hand_put<BF>(V + wave * (L::VB / 2), u, lane, Frag2<BF>{frag_lo(a[0], yp.a), frag_lo(a[1], yp.b)});
+                }
                 ys[u] = {frag_from_acc<BF>(d[0]), frag_from_acc<BF>(d[1])};
             }
             issue_loads<BF>();
@@ -1178,14 +1228,14 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         // formed anew: otherwise the 64-bit addresses of the first loads stay in registers over the whole walk
         int q4b = q4;
         asm volatile("" : "+v"(q4b));
+        auto store_state = [&](auto *dst, auto convert) {
 #pragma unroll
-        for (int ct = 0; ct < KT; ++ct)
+            for (int ct = 0; ct < KT; ++ct)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t at = sbase + (int64_t)state_channel(ct, q4b, j) * p.dv;
-                if (p.state_bf16) static_cast<uint16_t *>(p.sf)[at] = f32_to_bf16(S[ct][j]);
-                else static_cast<float *>(p.sf)[at] = S[ct][j];
-            }
+                for (int j = 0; j < 4; ++j) dst[sbase + (int64_t)state_channel(ct, q4b, j) * p.dv] = convert(S[ct][j]);
+        };
+        if (p.state_bf16) store_state(static_cast<uint16_t *>(p.sf), [](float x) { return f32_to_bf16(x); });
+        else store_state(static_cast<float *>(p.sf), [](float x) { return x; });
     }
 }
 
