@@ -130,12 +130,6 @@ kda_status_t check_offsets(const kda_gdn_problem_t *p, const Shape &s, const int
     return KDA_OK;
 }
 
-// State columns per workgroup: 64 where that still gives every CU a workgroup (K and Q of a chunk are
-// then staged half as often), else 32.
-int scan_cols(const kda_gdn_problem_t *p, const Shape &s, int cus) {
-    return 32;
-}
-
 int current_cus() {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) != hipSuccess ||
@@ -163,7 +157,7 @@ kda::gdn::GdnParams params_of(const kda_gdn_problem_t *p, const Shape &s, const 
     r.dk = p->head_dim_k;
     r.dv = p->head_dim_v;
     r.gate_bf16 = p->gate_dtype == KDA_BF16;
-    r.state_bf16 = p->state_dtype == KDA_BF16;
+    r.s0_bf16 = r.sf_bf16 = p->state_dtype == KDA_BF16;
     r.scale = p->scale;
     return r;
 }
@@ -178,6 +172,45 @@ hipError_t launch_scan(const kda_gdn_problem_t *p, int mode, int cols, const kda
 // is bound by its launches either way.
 bool bwd_wide(const kda_gdn_problem_t *p, const Shape &s) {
     return p->io_dtype == KDA_BF16 && s.tokens <= 256 && s.tokens * p->num_heads_v <= 512;
+}
+
+// Segments of a forward that is split over its length: with few (sequence, head) chains most CUs idle while
+// each chain's chunks follow one another.  The maps of all segments but the last run side by side
+// (d_v + d_k columns), the join walks the segments, and the forward runs on all of them at once.  The
+// number of segments is the one with the least time by the model below (us, measured: a chunk of the
+// forward and of the maps, each per round of workgroups over the CUs; a segment of the join; the fixed
+// part of the two further launches), and the split is taken where that is a tenth less than one walk.
+// 8 heads of 128 x 128, bf16: one walk against the split 74 / 66 us at 2,048 tokens, 272 / 134 at 8,192,
+// 1,068 / 408 at 32,768; at 1,024 tokens 41 / 45, at 32 heads and 8,192 tokens 270 / 376: one walk.  Packed batches, whose
+// lengths the host does not know, are not split.
+struct Split {
+    int32_t segs = 0, seg_len = 0;
+    size_t h = 0, bytes = 0;  // offset of M, size
+};
+Split split_of(const kda_gdn_problem_t *p, const Shape &s, bool packed, int cus) {
+    Split r;
+    const bool bf = p->io_dtype == KDA_BF16;
+    const double t_fwd = bf ? 2.1 : 5.9, t_map = bf ? 1.7 : 3.4, t_join = 1.2, t_fixed = 14;
+    const int64_t cols = p->head_dim_v / 32, both = cols + p->head_dim_k / 32, C = kda::gdn::chunk_of(p->io_dtype);
+    const int64_t chains = (int64_t)s.num_seqs * p->num_heads_v, chunks = (p->seq_len + C - 1) / C;
+    if (packed || chains <= 0) return r;
+    double least = 0.9 * t_fwd * (double)chunks;
+    int64_t per = 0;
+    for (int64_t n = 2; n * chains * cols <= cus && 2 * n <= chunks; ++n) {  // one round for the forward
+        const int64_t rounds = ((n - 1) * chains * both + cus - 1) / cus, len = (chunks + n - 1) / n;
+        const double t = (double)len * (t_fwd + t_map * (double)rounds) + t_join * (double)n + t_fixed;
+        if (t < least) {
+            least = t;
+            per = len;
+        }
+    }
+    if (!per) return r;
+    r.segs = (int32_t)((chunks + per - 1) / per);
+    r.seg_len = (int32_t)(per * C);
+    const size_t n = (size_t)chains * r.segs * p->head_dim_k * sizeof(float);
+    r.h = n * p->head_dim_v;
+    r.bytes = r.h + n * p->head_dim_k;
+    return r;
 }
 
 // Workspace of the backward: S and dS per chunk slot, Z per token; on fp32 operands also the copies of the
@@ -211,7 +244,8 @@ extern "C" {
 
 kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,
                                const void *g, const void *beta, const void *initial_state, const int32_t *cu_seqlens,
-                               const int32_t *cu_seqlens_host, void *out, void *final_state, void *stream) {
+                               const int32_t *cu_seqlens_host, void *out, void *final_state, void *workspace,
+                               size_t workspace_bytes, void *stream) {
     try {
         Shape s;
         kda_status_t st = check_shape(problem, cu_seqlens != nullptr, s);
@@ -227,6 +261,7 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
             {"final_state", final_state, s.states * s.state, 16, false, true},
             {"out", out, s.tokens * s.v_row * s.io, 16, true, true},
             {"cu_seqlens", cu_seqlens, ((int64_t)s.num_seqs + 1) * 4, 4, false, false},
+            {"workspace", workspace, (int64_t)workspace_bytes, 256, false, true},
         };
         st = check_args(args, 5, 6);
         if (st == KDA_OK) st = check_offsets(problem, s, cu_seqlens, cu_seqlens_host);
@@ -236,11 +271,44 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
         r.sf = final_state;
         r.out = out;
         if (s.num_seqs == 0 || (s.tokens == 0 && !final_state)) return done(hipSuccess, "");
-        return done(launch_scan(problem, 0, scan_cols(problem, s, current_cus()), r, static_cast<hipStream_t>(stream)),
-                    "kda_gdn_chunk_fwd launch");
+        hipStream_t hs = static_cast<hipStream_t>(stream);
+        const Split split = workspace ? split_of(problem, s, cu_seqlens != nullptr, current_cus()) : Split();
+        if (split.segs > 0 && workspace_bytes >= split.bytes) {
+            float *h = static_cast<float *>(workspace);
+            r.num_seqs = s.num_seqs * split.segs;
+            r.segs = split.segs;
+            r.seg_len = split.seg_len;
+            kda::gdn::GdnParams maps = r;
+            maps.s0 = nullptr;
+            maps.out = nullptr;
+            maps.num_seqs -= s.num_seqs;
+            maps.sf = h;
+            maps.sf_bf16 = 0;
+            maps.sm = h + split.h / sizeof(float);
+            st = done(launch_scan(problem, 1, 32, maps, hs), "kda_gdn_chunk_fwd segment launch");
+            if (st != KDA_OK) return st;
+            const kda::gdn::JoinParams join{initial_state, h, maps.sm, s.num_seqs, split.segs, problem->num_heads_v,
+                                            problem->head_dim_k, problem->head_dim_v, problem->state_dtype == KDA_BF16};
+            st = done(kda::gdn::launch_join(join, hs), "kda_gdn_chunk_fwd join launch");
+            if (st != KDA_OK) return st;
+            r.s0 = h;
+            r.s0_bf16 = 0;
+        }
+        return done(launch_scan(problem, 0, 32, r, hs), "kda_gdn_chunk_fwd launch");
     } catch (...) {
         return KDA_ERR_HIP;
     }
+}
+
+kda_status_t kda_gdn_chunk_fwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes) {
+    if (!bytes) return set_error(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    *bytes = 0;
+    Shape s;
+    const bool packed = problem && problem->num_seqs > 0;
+    kda_status_t st = check_shape(problem, packed, s);
+    if (st != KDA_OK) return st;
+    *bytes = split_of(problem, s, packed, current_cus()).bytes;
+    return done(hipSuccess, "");
 }
 
 kda_status_t kda_gdn_chunk_bwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes) {
@@ -297,7 +365,6 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
         if (s.num_seqs == 0 || (s.tokens == 0 && !d_initial_state)) return done(hipSuccess, "");
         hipStream_t hs = static_cast<hipStream_t>(stream);
         char *ws = static_cast<char *>(workspace);
-        const int cols = scan_cols(problem, s, current_cus());
         kda_gdn_problem_t run = *problem;
         kda::gdn::ConvertParams in{}, back{};
         if (bwd_wide(problem, s) && s.tokens > 0) {
@@ -343,10 +410,10 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
         grad.dbeta = dbeta;
         grad.slots = b.slots;
         if (s.tokens > 0) {
-            st = done(launch_scan(&run, 1, cols, keep, hs), "kda_gdn_chunk_bwd forward launch");
+            st = done(launch_scan(&run, 1, 32, keep, hs), "kda_gdn_chunk_bwd forward launch");
             if (st != KDA_OK) return st;
         }
-        st = done(launch_scan(&run, 2, cols, rev, hs), "kda_gdn_chunk_bwd reverse launch");
+        st = done(launch_scan(&run, 2, 32, rev, hs), "kda_gdn_chunk_bwd reverse launch");
         if (st != KDA_OK || s.tokens == 0) return st;
         st = done(run.io_dtype == KDA_BF16 ? kda::gdn::launch_grad_bf16(grad, hs) : kda::gdn::launch_grad_f32(grad, hs),
                   "kda_gdn_chunk_bwd gradient launch");

@@ -8,7 +8,7 @@ namespace gdn {
 
 template <bool BF, int DK, int CT, int MODE>
 hipError_t launch_one(const GdnParams &p, hipStream_t stream) {
-    const int64_t blocks = (int64_t)p.num_seqs * p.Hv * (p.dv / CT);
+    const int64_t blocks = (int64_t)p.num_seqs * p.Hv * ((p.dv + (p.sm ? p.dk : 0)) / CT);
     if (blocks <= 0) return hipSuccess;
     hipLaunchKernelGGL((gdn_scan_kernel<BF, DK, CT, MODE>), dim3((unsigned)blocks),
                        dim3((Lds<BF, DK, CT, MODE>::NT)), 0, stream, p);

@@ -182,6 +182,7 @@ struct Lds {
 // The sequence a workgroup works on.
 struct Walk {
     int n, hk, h, col0, len, nch;
+    bool ident;  // columns of the identity instead of values
     int64_t tok0, slot0;
 };
 
@@ -212,7 +213,7 @@ __device__ __forceinline__ int ranked_sequence(const GdnParams &p, int r, int *l
 template <int C, int CT>
 __device__ __forceinline__ Walk walk_of(const GdnParams &p, char *smem) {
     Walk w;
-    const int ntile = p.dv / CT, rep = p.Hv / p.Hk;
+    const int ntile = (p.dv + (p.sm ? p.dk : 0)) / CT, rep = p.Hv / p.Hk;
     // the tiles and the value heads that share a key head run next to each other on one XCD
     const SeqItem it = seq_item(blockIdx.x, p.num_seqs, p.Hk, rep * ntile, nullptr);
     w.n = it.n;
@@ -221,7 +222,15 @@ __device__ __forceinline__ Walk walk_of(const GdnParams &p, char *smem) {
     w.hk = it.h;
     w.h = it.h * rep + it.tile / ntile;
     w.col0 = (it.tile % ntile) * CT;
-    if (p.cu) {
+    w.ident = w.col0 >= p.dv;
+    if (w.ident) w.col0 -= p.dv;
+    if (p.segs) {
+        if (p.sm) w.n += w.n / (p.segs - 1);  // the last segments are left out
+        const int at = w.n % p.segs * p.seg_len;
+        w.tok0 = (int64_t)(w.n / p.segs) * p.T + at;
+        w.len = min(p.seg_len, p.T - at);
+        w.slot0 = 0;
+    } else if (p.cu) {
         // offsets outside the tokens are cut off rather than followed
         const int a = min(max(p.cu[w.n], 0), p.T), b = min(max(p.cu[w.n + 1], a), p.T);
         w.tok0 = a;
@@ -255,7 +264,7 @@ __device__ __forceinline__ void stage_chunk(const GdnParams &p, const Walk &w, i
             load_lds16(src + min(row, clen - 1) * ld + ((slot ^ slot_key<L::RB>(row)) << 4), dst + part * L::KB + i * 1024);
         }
     }
-    const char *src = static_cast<const char *>(p.v) + (t0 * p.ldv + (int64_t)w.h * p.dv + w.col0) * L::E;
+    const char *src = static_cast<const char *>(p.v) + (t0 * p.ldv + (int64_t)w.h * p.dv + (w.ident ? 0 : w.col0)) * L::E;
 #pragma unroll
     for (int i = 0; i < L::VB / 1024; ++i) {
         const int piece = 64 * i + lane, row = piece / VSPR;
@@ -985,19 +994,23 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
     // ------------------------------------------------------------------ chain waves
     __builtin_amdgcn_s_setprio(2);  // the chain is what every other wave waits for
     const int col = w.col0 + 16 * wave + l16;
-    const int64_t sbase = ((int64_t)w.n * p.Hv + w.h) * DK * p.dv + col;
+    // the state's place: rows of `width` columns
+    const int width = w.ident ? DK : p.dv;
+    const int64_t sbase = ((int64_t)w.n * p.Hv + w.h) * DK * width + col;
     f32x4 S[KT];
     // one branch around all the loads: one per value would wait for each (10 us of a workgroup's start)
     auto load_state = [&](auto *src) {
 #pragma unroll
         for (int ct = 0; ct < KT; ++ct)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) S[ct][j] = elem_f32(src[sbase + (int64_t)state_channel(ct, q4, j) * p.dv]);
+            for (int j = 0; j < 4; ++j) S[ct][j] = elem_f32(src[sbase + (int64_t)state_channel(ct, q4, j) * width]);
     };
-    if (!p.s0) {
+    if (w.ident || !p.s0) {
 #pragma unroll
-        for (int ct = 0; ct < KT; ++ct) S[ct] = zero4();
-    } else if (p.state_bf16) {
+        for (int ct = 0; ct < KT; ++ct)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[ct][j] = w.ident && state_channel(ct, q4, j) == col ? 1.f : 0.f;
+    } else if (p.s0_bf16) {
         load_state(static_cast<const uint16_t *>(p.s0));
     } else {
         load_state(static_cast<const float *>(p.s0));
@@ -1018,6 +1031,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
 #pragma unroll
             for (int t = 0; t < K2; ++t) kf[rt][t] = row_frag<BF, L::RB>(K, 16 * rt + l16, 32 * t + 8 * q4);
             vf[rt] = value_frag<BF, L::VRB>(V, wave, rt, l16, q4);
+            if (MODE == kKeep && w.ident) vf[rt] = make_frag<BF>(0.f, 0.f, 0.f, 0.f);
         }
     };
     // (not in reverse, which has no registers left for them)
@@ -1041,7 +1055,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         if constexpr (MODE == kFwd) {
 #pragma unroll
             for (int t = 0; t < K2; ++t) hand_put<BF>(hand, t, lane, Sb[t]);
-        } else {
+        } else if (p.hs) {
             // the state entering (reverse: the gradient of the state leaving) the chunk, [dv][d_k]
             IO *dst = static_cast<IO *>(p.hs) + (((w.slot0 + c) * p.Hv + w.h) * p.dv + col) * DK + 8 * q4;
 #pragma unroll
@@ -1127,7 +1141,7 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
             for (int u = 0; u < RT / 2; ++u)
 #pragma unroll
                 for (int ct = 0; ct < KT; ++ct) mma<BF>(S[ct], kt[ct][u], ys[u]);
-            if constexpr (MODE == kKeep)
+            if (MODE == kKeep && p.zs)
                 put_value_rows<BF, L::VRB, RT>(V, static_cast<IO *>(p.zs) + (tok * p.Hv + w.h) * p.dv + w.col0,
                                                (int64_t)p.Hv * p.dv, wave, x, clen, lane);
         } else {
@@ -1224,17 +1238,20 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         if (!REV && s + 1 < nch) fetch(s + 1);
         __syncthreads();  // B
     }
-    if (p.sf) {
+    const bool part = p.segs && !p.sm;  // the state of a sequence is its last segment's
+    if ((p.sf || w.ident) && (!part || w.n % p.segs == p.segs - 1)) {
         // formed anew: otherwise the 64-bit addresses of the first loads stay in registers over the whole walk
         int q4b = q4;
         asm volatile("" : "+v"(q4b));
+        const int64_t at = part ? ((int64_t)(w.n / p.segs) * p.Hv + w.h) * DK * width + col : sbase;
         auto store_state = [&](auto *dst, auto convert) {
 #pragma unroll
             for (int ct = 0; ct < KT; ++ct)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) dst[sbase + (int64_t)state_channel(ct, q4b, j) * p.dv] = convert(S[ct][j]);
+                for (int j = 0; j < 4; ++j) dst[at + (int64_t)state_channel(ct, q4b, j) * width] = convert(S[ct][j]);
         };
-        if (p.state_bf16) store_state(static_cast<uint16_t *>(p.sf), [](float x) { return f32_to_bf16(x); });
+        if (w.ident) store_state(p.sm, [](float x) { return x; });
+        else if (p.sf_bf16) store_state(static_cast<uint16_t *>(p.sf), [](float x) { return f32_to_bf16(x); });
         else store_state(static_cast<float *>(p.sf), [](float x) { return x; });
     }
 }

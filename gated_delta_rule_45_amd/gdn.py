@@ -28,7 +28,8 @@ class GdnProblem(ctypes.Structure):
 
 def declare(lib: ctypes.CDLL) -> None:
     prob = ctypes.POINTER(GdnProblem)
-    lib.kda_gdn_chunk_fwd.argtypes = [prob] + [_P] * 11
+    lib.kda_gdn_chunk_fwd.argtypes = [prob] + [_P] * 11 + [ctypes.c_size_t, _P]
+    lib.kda_gdn_chunk_fwd_workspace.argtypes = [prob, ctypes.POINTER(ctypes.c_size_t)]
     lib.kda_gdn_decode.argtypes = [prob] + [_P] * 6 + [ctypes.c_int64] + [_P] * 6
     lib.kda_norm_gate_bwd.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_float] + [_P] * 8 + \
         [ctypes.c_size_t, _P]
@@ -36,7 +37,8 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.kda_norm_gate_bwd_workspace.restype = ctypes.c_size_t
     lib.kda_gdn_chunk_bwd.argtypes = [prob] + [_P] * 17 + [ctypes.c_size_t, _P]
     lib.kda_gdn_chunk_bwd_workspace.argtypes = [prob, ctypes.POINTER(ctypes.c_size_t)]
-    for f in (lib.kda_gdn_chunk_bwd, lib.kda_gdn_chunk_bwd_workspace, lib.kda_gdn_chunk_fwd, lib.kda_gdn_decode, lib.kda_norm_gate_bwd):
+    for f in (lib.kda_gdn_chunk_bwd, lib.kda_gdn_chunk_bwd_workspace, lib.kda_gdn_chunk_fwd, lib.kda_gdn_chunk_fwd_workspace,
+              lib.kda_gdn_decode, lib.kda_norm_gate_bwd):
         f.restype = ctypes.c_int
 
 
@@ -85,6 +87,15 @@ def _rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
     return ld
 
 
+def _room(workspace, device):
+    """A workspace's pointer and bytes."""
+    if workspace is None or workspace.numel() == 0:
+        return None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
 def _host_i32(x, n: int, name: str):
     if x is None:
         return None
@@ -123,11 +134,13 @@ def gdn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
                   initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, *,
                   cu_seqlens_host=None, scale: float = 1.0, out: Optional[torch.Tensor] = None,
                   final_state: Optional[torch.Tensor] = None, output_final_state: bool = True,
-                  state_dtype: Optional[torch.dtype] = None, stream=None):
+                  state_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """Chunkwise forward.  q, k: [B, T, Hk, d_k]; v: [B, T, Hv, d_v] (bf16 or fp32); g, beta: [B, T, Hv]
     (fp32 or bf16); initial_state: [N, Hv, d_k, d_v] (fp32 or bf16) or None; cu_seqlens: int32 [N+1]
     (B == 1) or None.  The states' dtype is that of the state given, else state_dtype, else fp32;
-    final_state may be initial_state.  Returns (out, final_state)."""
+    final_state may be initial_state.  workspace: uint8, as long as kda_gdn_chunk_fwd_workspace says, for long
+    sequences on few heads (allocated here when None and needed; an empty tensor: do without).  Returns
+    (out, final_state)."""
     given = initial_state if initial_state is not None else final_state
     sdt = given.dtype if given is not None else state_dtype or torch.float32
     p, n = _problem(q, k, v, g, beta, cu_seqlens, sdt, scale)
@@ -144,10 +157,23 @@ def gdn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
             _need(final_state, "final_state", sdt, states, dev)
         elif output_final_state:
             final_state = torch.empty(states, dtype=sdt, device=dev)
+        if workspace is None and cu_seqlens is None and q.shape[1] >= _SPLIT_TOKENS:
+            need = _fwd_workspace(p)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        room, size = _room(workspace, dev)
         _check(library().kda_gdn_chunk_fwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                            _ptr(initial_state), _ptr(cu_seqlens), _ptr(host), _ptr(out),
-                                           _ptr(final_state), handle))
+                                           _ptr(final_state), room, size, handle))
     return out, final_state
+
+
+_SPLIT_TOKENS = 256  # shorter sequences are not split
+
+
+def _fwd_workspace(p: GdnProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check(library().kda_gdn_chunk_fwd_workspace(ctypes.byref(p), ctypes.byref(n)))
+    return n.value
 
 
 def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -185,11 +211,11 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
             need = ctypes.c_size_t(0)
             _check(lib.kda_gdn_chunk_bwd_workspace(ctypes.byref(p), ctypes.byref(need)))
             workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        room, size = _room(workspace, dev)
         _check(lib.kda_gdn_chunk_bwd(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(initial_state),
                                      _ptr(cu_seqlens), _ptr(host), _ptr(d_out), _ptr(d_final_state), _ptr(out["dq"]),
                                      _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
-                                     _ptr(out.get("d_initial_state")), _ptr(workspace),
-                                     workspace.numel() * workspace.element_size(), handle))
+                                     _ptr(out.get("d_initial_state")), room, size, handle))
     return out
 
 
@@ -233,8 +259,8 @@ def norm_gate_bwd(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, d_o
     with _Launch(dev, stream) as handle:
         if workspace is None and need:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        room, size = _room(workspace, dev)
         d_o, d_gate, d_weight = torch.empty_like(o), torch.empty_like(o), torch.empty_like(weight)
         _check(lib.kda_norm_gate_bwd(rows, d, io, eps, _ptr(o), _ptr(gate), _ptr(weight), _ptr(d_out), _ptr(d_o),
-                                     _ptr(d_gate), _ptr(d_weight), _ptr(workspace),
-                                     0 if workspace is None else workspace.numel() * workspace.element_size(), handle))
+                                     _ptr(d_gate), _ptr(d_weight), room, size, handle))
     return d_o, d_gate, d_weight

@@ -427,13 +427,22 @@ typedef struct {
  *                                  written); they may be the same buffer
  *  cu_seqlens, cu_seqlens_host     as for kda_chunk_fwd; offsets outside the tokens are cut off
  *  out   [tokens, Hv, d_v]         io dtype, dense
- * No workspace is used and nothing is allocated: the call can be captured and run on several streams
- * at once.  bf16 io: products take bf16 operands and accumulate in fp32.  Any other overlap of an
- * output with an argument is refused.  Errors as for kda_chunk_fwd.
+ *  workspace       optional, 256-byte aligned: with at least kda_gdn_chunk_fwd_workspace() bytes, where that is not
+ *                  0, a plain batch of few sequences and heads is split over its length (the segments' maps of
+ *                  the state side by side, joined, then the segments); otherwise it is not used
+ * Nothing is allocated: the call can be captured, and run on several streams at once with a workspace each.
+ * A NaN or infinity reaches the results of its own sequence only, from the start of its chunk (64 tokens in
+ * bf16, 32 in fp32) on.
+ * bf16 io: products take bf16 operands and accumulate in fp32.  Any other overlap of an output with an
+ * argument is refused.  Errors as for kda_chunk_fwd.
  */
 kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,
                                const void *g, const void *beta, const void *initial_state, const int32_t *cu_seqlens,
-                               const int32_t *cu_seqlens_host, void *out, void *final_state, void *stream);
+                               const int32_t *cu_seqlens_host, void *out, void *final_state, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/* Workspace bytes kda_gdn_chunk_fwd can use on the current device (a packed batch where problem->num_seqs > 0: 0). */
+kda_status_t kda_gdn_chunk_fwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes);
 
 /*
  * kda_gdn_chunk_bwd -- gradients of kda_gdn_chunk_fwd for L = sum(d_out * out) + sum(d_final_state * final_state)

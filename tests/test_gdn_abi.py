@@ -21,9 +21,10 @@ def prob(**kw):
     return GdnProblem(**base)
 
 
-def fwd(p, q=at(0), k=at(1), v=at(2), g=at(3), beta=at(4), s0=None, cu=None, cu_host=None, out=at(5), sf=None):
+def fwd(p, q=at(0), k=at(1), v=at(2), g=at(3), beta=at(4), s0=None, cu=None, cu_host=None, out=at(5), sf=None, ws=None,
+        n=0):
     return kda.library().kda_gdn_chunk_fwd(None if p is None else ctypes.byref(p), q, k, v, g, beta, s0, cu, cu_host,
-                                           out, sf, None)
+                                           out, sf, ws, n, None)
 
 
 def bwd(p, q=at(0), k=at(1), v=at(2), g=at(3), beta=at(4), s0=None, cu=None, d_out=at(5), dsf=None, dq=at(6), dk=at(7),

@@ -519,3 +519,62 @@ def test_two_streams_at_once():
         for (a, b), (c, d) in zip(got, want):
             assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1])
             assert all(torch.equal(b[k], d[k]) for k in b)
+
+
+@pytest.mark.parametrize("io,sdt", [(BF, F32), (BF, BF), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T", [8192, 4096 + 1])
+def test_forward_split_over_its_length(io, sdt, dk, dv, T):
+    # long sequences on few heads: with room the walk is split; mild decays, so the first segment's state is seen
+    # in the last one
+    x = ref.inputs(2, T, 1, 2, dk, dv, io, seed=T + dk, device=DEV)
+    x[3].mul_(0.05)
+    s0 = state(2, 2, dk, dv, sdt)
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    a = kda.gdn_chunk_fwd(*x, s0, scale=dk ** -0.5, workspace=none)
+    o, f = ref.delta_rule(*x, s0, scale=dk ** -0.5)
+    for name, got in (("one walk", a), ("split", kda.gdn_chunk_fwd(*x, s0, scale=dk ** -0.5))):
+        close(name + " out", got[0], o, *tol(io))
+        close(name + " final", got[1], f, *tol(BF if sdt == BF else io))
+    assert not torch.equal(a[0], got[0])  # two ways of summing
+    inplace = s0.clone()
+    again = kda.gdn_chunk_fwd(*x, inplace, scale=dk ** -0.5, final_state=inplace)
+    assert torch.equal(again[0], got[0]) and torch.equal(inplace, got[1])
+    assert torch.equal(kda.gdn_chunk_fwd(*x, s0, scale=dk ** -0.5, output_final_state=False)[0], got[0])
+
+
+def test_split_forward_keeps_a_bad_value_behind_it():
+    x = ref.inputs(1, 8192, 1, 2, 128, 128, BF, seed=3, device=DEV)
+    want = kda.gdn_chunk_fwd(*x)  # within a chunk of 64 tokens (here from 4992) a NaN meets the zeros of the causal mask
+    x[2][0, 5000, 0, 7] = float("nan")
+    x[2][0, 8191, 1, 9] = float("inf")
+    out, fin = kda.gdn_chunk_fwd(*x)
+    assert torch.equal(out[:, :4992], want[0][:, :4992])
+    assert torch.equal(out[:, :8128, 1], want[0][:, :8128, 1])
+    other = [i for i in range(128) if i != 7]
+    assert torch.equal(out[:, :, 0, other], want[0][:, :, 0, other]) and torch.equal(fin[0, 0][:, other], want[1][0, 0][:, other])
+    assert out[0, 5000:, 0, 7].isnan().all() and fin[0, 0, :, 7].isnan().all()
+
+
+def test_split_forward_captured_and_workspaces_of_the_caller():
+    x = ref.inputs(1, 8192, 1, 2, 128, 128, BF, seed=3, device=DEV)
+    want = [t.clone() for t in kda.gdn_chunk_fwd(*x)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = kda.gdn_chunk_fwd(*x)
+    for i in range(4):
+        for t in got:
+            t.fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+        assert all(torch.equal(a, b) for a, b in zip(kda.gdn_chunk_fwd(*x), want)), i
+    with pytest.raises(ValueError):
+        kda.gdn_chunk_fwd(*x, workspace=torch.empty(1 << 24, dtype=torch.uint8))  # on the host
+    with pytest.raises(kda.KdaError):
+        kda.gdn_chunk_fwd(*x, workspace=want[0].view(torch.uint8).flatten(), out=want[0])  # is the output
+    with pytest.raises(kda.KdaError):
+        kda.gdn_chunk_fwd(*x, workspace=torch.empty(1 << 24, dtype=torch.uint8, device=DEV)[4:])  # alignment
+    small = torch.empty(256, dtype=torch.uint8, device=DEV)  # too little room: as without
+    none = torch.empty(0, dtype=torch.uint8, device=DEV)
+    a, b = kda.gdn_chunk_fwd(*x, workspace=small), kda.gdn_chunk_fwd(*x, workspace=none)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
