@@ -55,14 +55,15 @@ __global__ void __launch_bounds__(kThreads) norm_gate_bwd_kernel(int64_t rows, f
         float dn[N], dot = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float s = 1.0f / (1.0f + expf(-g[i]));
+            // s and 1 - s from one exponential of -|z| <= 0, without overflow or cancellation
+            const float e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(g[i])), u = __builtin_amdgcn_rcpf(1.0f + e);
+            const float big = u, small = e * u, s = g[i] >= 0.f ? big : small;
             x[i] *= r;
             const float ys = y[i] * s;
             acc[i] = fmaf(ys, x[i], acc[i]);
             dn[i] = ys * w[i];
             dot = fmaf(dn[i], x[i], dot);
-            // 1 - s as sigmoid(-z): no cancellation for large z
-            g[i] = dn[i] * x[i] / (1.0f + expf(g[i]));
+            g[i] = dn[i] * x[i] * (g[i] >= 0.f ? small : big);
         }
 #pragma unroll
         for (int off = LPR / 2; off >= 1; off >>= 1) dot += __shfl_xor(dot, off);
