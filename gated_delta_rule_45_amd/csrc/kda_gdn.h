@@ -44,9 +44,8 @@ struct GdnParams {
 };
 
 // Walks every sequence's chunks.  mode: 0 forward, 1 forward that keeps states and Z (no output), 2 reverse.
-// cols: state columns per workgroup, 32 or 64.
-hipError_t launch_scan_bf16(int mode, int cols, const GdnParams &p, hipStream_t stream);
-hipError_t launch_scan_f32(int mode, int cols, const GdnParams &p, hipStream_t stream);
+hipError_t launch_scan_bf16(int mode, const GdnParams &p, hipStream_t stream);
+hipError_t launch_scan_f32(int mode, const GdnParams &p, hipStream_t stream);
 
 // Gradients inside the chunks, after a keeping forward and a reverse scan.
 struct GradParams {

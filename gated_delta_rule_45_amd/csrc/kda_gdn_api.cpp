@@ -162,8 +162,8 @@ kda::gdn::GdnParams params_of(const kda_gdn_problem_t *p, const Shape &s, const 
     return r;
 }
 
-hipError_t launch_scan(const kda_gdn_problem_t *p, int mode, int cols, const kda::gdn::GdnParams &r, hipStream_t s) {
-    return p->io_dtype == KDA_BF16 ? kda::gdn::launch_scan_bf16(mode, cols, r, s) : kda::gdn::launch_scan_f32(mode, cols, r, s);
+hipError_t launch_scan(const kda_gdn_problem_t *p, int mode, const kda::gdn::GdnParams &r, hipStream_t s) {
+    return p->io_dtype == KDA_BF16 ? kda::gdn::launch_scan_bf16(mode, r, s) : kda::gdn::launch_scan_f32(mode, r, s);
 }
 
 // Whether the gradients of a bf16 call are computed on fp32 operands.  With few gates' gradients the
@@ -285,7 +285,7 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
             maps.sf = h;
             maps.sf_bf16 = 0;
             maps.sm = h + split.h / sizeof(float);
-            st = done(launch_scan(problem, 1, 32, maps, hs), "kda_gdn_chunk_fwd segment launch");
+            st = done(launch_scan(problem, 1, maps, hs), "kda_gdn_chunk_fwd segment launch");
             if (st != KDA_OK) return st;
             const kda::gdn::JoinParams join{initial_state, h, maps.sm, s.num_seqs, split.segs, problem->num_heads_v,
                                             problem->head_dim_k, problem->head_dim_v, problem->state_dtype == KDA_BF16};
@@ -294,7 +294,7 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
             r.s0 = h;
             r.s0_bf16 = 0;
         }
-        return done(launch_scan(problem, 0, 32, r, hs), "kda_gdn_chunk_fwd launch");
+        return done(launch_scan(problem, 0, r, hs), "kda_gdn_chunk_fwd launch");
     } catch (...) {
         return KDA_ERR_HIP;
     }
@@ -410,10 +410,10 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
         grad.dbeta = dbeta;
         grad.slots = b.slots;
         if (s.tokens > 0) {
-            st = done(launch_scan(&run, 1, 32, keep, hs), "kda_gdn_chunk_bwd forward launch");
+            st = done(launch_scan(&run, 1, keep, hs), "kda_gdn_chunk_bwd forward launch");
             if (st != KDA_OK) return st;
         }
-        st = done(launch_scan(&run, 2, 32, rev, hs), "kda_gdn_chunk_bwd reverse launch");
+        st = done(launch_scan(&run, 2, rev, hs), "kda_gdn_chunk_bwd reverse launch");
         if (st != KDA_OK || s.tokens == 0) return st;
         st = done(run.io_dtype == KDA_BF16 ? kda::gdn::launch_grad_bf16(grad, hs) : kda::gdn::launch_grad_f32(grad, hs),
                   "kda_gdn_chunk_bwd gradient launch");

@@ -3,8 +3,8 @@
 
 namespace kda {
 namespace gdn {
-hipError_t launch_scan_bf16(int mode, int cols, const GdnParams &p, hipStream_t stream) {
-    return launch_scan<true>(mode, cols, p, stream);
+hipError_t launch_scan_bf16(int mode, const GdnParams &p, hipStream_t stream) {
+    return launch_scan<true>(mode, p, stream);
 }
 }  // namespace gdn
 }  // namespace kda

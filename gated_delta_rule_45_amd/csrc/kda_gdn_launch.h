@@ -16,9 +16,9 @@ hipError_t launch_one(const GdnParams &p, hipStream_t stream) {
 }
 
 template <bool BF>
-hipError_t launch_scan(int mode, int cols, const GdnParams &p, hipStream_t stream) {
+hipError_t launch_scan(int mode, const GdnParams &p, hipStream_t stream) {
 #define GDN_CASE(DK_, CT_, M_) \
-    if (p.dk == DK_ && cols == CT_ && mode == M_) return launch_one<BF, DK_, CT_, M_>(p, stream);
+    if (p.dk == DK_ && mode == M_) return launch_one<BF, DK_, CT_, M_>(p, stream);
 #define GDN_MODES(DK_, CT_) GDN_CASE(DK_, CT_, kFwd) GDN_CASE(DK_, CT_, kKeep) GDN_CASE(DK_, CT_, kRev)
     GDN_MODES(64, 32)
     GDN_MODES(128, 32)

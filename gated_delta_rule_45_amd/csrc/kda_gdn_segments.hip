@@ -5,6 +5,8 @@
 //
 // One workgroup owns (sequence, value head, 16 columns), each wave a row tile.  M_p (64 KB at d_k = 128) and
 // H_p are read straight into operands, a segment ahead; S goes through LDS, transposed.  All in fp32.
+// 65,536 tokens x 8 heads of 128 x 128, 8 segments: 20 us of 874 (the maps 507, the forward on the segments
+// 330; one walk 2,389).
 #include "kda_device.h"
 #include "kda_gdn.h"
 
