@@ -3,9 +3,11 @@
 // without launching anything (and works on machines without a GPU).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <vector>
 
 #include "kda.h"
 #include "kda_gdn.h"
@@ -457,14 +459,18 @@ kda_status_t kda_gdn_decode(const kda_gdn_problem_t *problem, const void *q, con
         if (state_slots_host) {
             if (!state_slots) return set_error(KDA_ERR_INVALID_ARGUMENT, "state_slots_host given without state_slots");
             // each slot once: two sequences in one slot would race for it
+            std::vector<int32_t> used;
+            used.reserve((size_t)s.num_seqs);
             for (int32_t i = 0; i < s.num_seqs; ++i) {
                 const int32_t x = state_slots_host[i];
                 if (x >= num_slots)
                     return set_error(KDA_ERR_INVALID_ARGUMENT, "state_slots[%d] = %d, there are %lld", i, x, (long long)num_slots);
-                for (int32_t j = 0; x >= 0 && j < i; ++j)
-                    if (state_slots_host[j] == x)
-                        return set_error(KDA_ERR_INVALID_ARGUMENT, "state_slots[%d] and [%d] are both %d", j, i, x);
+                if (x >= 0) used.push_back(x);
             }
+            std::sort(used.begin(), used.end());
+            const auto twice = std::adjacent_find(used.begin(), used.end());
+            if (twice != used.end())
+                return set_error(KDA_ERR_INVALID_ARGUMENT, "state_slots names slot %d twice", *twice);
         }
         if (s.num_seqs == 0 || s.tokens == 0 || num_slots == 0) return done(hipSuccess, "");
         kda::gdn::DecodeParams r{};

@@ -429,7 +429,8 @@ typedef struct {
  *  out   [tokens, Hv, d_v]         io dtype, dense
  *  workspace       optional, 256-byte aligned: with at least kda_gdn_chunk_fwd_workspace() bytes, where that is not
  *                  0, a plain batch of few sequences and heads is split over its length (the segments' maps of
- *                  the state side by side, joined, then the segments); otherwise it is not used
+ *                  the state side by side, joined, then the segments; the results then differ in their
+ *                  rounding from one walk's); otherwise it is not used
  * Nothing is allocated: the call can be captured, and run on several streams at once with a workspace each.
  * A NaN or infinity reaches the results of its own sequence only, from the start of its chunk (64 tokens in
  * bf16, 32 in fp32) on.
