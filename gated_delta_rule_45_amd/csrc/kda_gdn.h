@@ -35,12 +35,12 @@ struct GdnParams {
     int32_t gate_bf16;
     int32_t s0_bf16, sf_bf16; // types of s0 and of sf
     float scale;
-    // A walk split over its length (segs > 0): sequence n is segment n % segs, of seg_len tokens, of the T tokens
-    // n / segs, and only the last segment's state goes to sf, at n / segs.  With sm the sequences are all but
-    // the last segments, each one's state goes to sf, and d_k more columns, started from the identity
-    // and without values, to sm.
-    int32_t segs = 0, seg_len = 0;
-    float *sm = nullptr;  // [sequences, segs, Hv, d_k, d_k]
+    // A walk split over its length (segs > 0): "sequence" n is segment seg_first + n % seg_run, of seg_len tokens, of
+    // the T tokens n / seg_run; states at s0 are [batch, segs, ..], and only the state that ends the whole
+    // walk goes to sf, [batch, ..].  With maps set each segment's goes to sf, [batch, segs, ..], and (keeping
+    // forward) d_k more columns, started from the identity and without values, to sm.
+    int32_t segs = 0, seg_len = 0, seg_first = 0, seg_run = 0, maps = 0;
+    float *sm = nullptr;  // [batch, segs, Hv, d_k, d_k]
 };
 
 // Walks every sequence's chunks.  mode: 0 forward, 1 forward that keeps states and Z (no output), 2 reverse.
@@ -72,10 +72,11 @@ hipError_t launch_convert(bool widen, const ConvertParams &p, hipStream_t stream
 
 // The states entering the segments of split walks (kda_gdn_segments.hip).
 struct JoinParams {
-    const void *s0;  // [batch, Hv, d_k, dv] fp32 or bf16, or null (zero)
-    float *h;        // [batch, segs, Hv, d_k, dv]: H (but the last segment's) on entry, the states on return
-    const float *m;  // [batch, segs, Hv, d_k, d_k], the last one not read
+    const void *s0;  // [batch, Hv, d_k, dv] fp32 or bf16, or null (zero): what enters the first segment walked
+    float *h;        // [batch, segs, Hv, d_k, dv]: H (but of the last segment walked) on entry, the states on return
+    const float *m;  // [batch, segs, Hv, d_k, d_k]
     int32_t batch, segs, Hv, dk, dv, state_bf16;
+    int32_t reverse; // gradients: from the last segment to the first, M transposed
 };
 hipError_t launch_join(const JoinParams &p, hipStream_t stream);
 

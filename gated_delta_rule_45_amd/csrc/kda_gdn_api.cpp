@@ -176,31 +176,38 @@ bool bwd_wide(const kda_gdn_problem_t *p, const Shape &s) {
     return p->io_dtype == KDA_BF16 && s.tokens <= 256 && s.tokens * p->num_heads_v <= 512;
 }
 
-// Segments of a forward that is split over its length: with few (sequence, head) chains most CUs idle while
+// Segments of walks that are split over their length: with few (sequence, head) chains most CUs idle while
 // each chain's chunks follow one another.  The maps of all segments but the last run side by side
 // (d_v + d_k columns), the join walks the segments, and the forward runs on all of them at once.  The
 // number of segments is the one with the least time by the model below (us, measured: a chunk of the
 // forward and of the maps, each per round of workgroups over the CUs; a segment of the join; the fixed
 // part of the two further launches), and the split is taken where that is a tenth less than one walk.
+// The gradients split the keeping forward in the same way, and the reverse scan: a segment takes the
+// gradient of the state that leaves it to M^T dS + H', H' by one more reverse scan from zero.
 // 8 heads of 128 x 128, bf16: one walk against the split 74 / 66 us at 2,048 tokens, 272 / 134 at 8,192,
-// 1,068 / 408 at 32,768; at 1,024 tokens 41 / 45, at 32 heads and 8,192 tokens 270 / 376: one walk.  Packed batches, whose
+// 1,068 / 408 at 32,768; at 1,024 tokens 41 / 45, at 32 heads and 8,192 tokens 270 / 376: one walk.
+// Gradients, the same heads: 241 / 203 at 2,048 tokens, 644 / 329 at 8,192; at 1,024 171 / 179: one walk; fp32
+// 790 / 417 at 2,048.  Packed batches, whose
 // lengths the host does not know, are not split.
 struct Split {
     int32_t segs = 0, seg_len = 0;
     size_t h = 0, bytes = 0;  // offset of M, size
 };
-Split split_of(const kda_gdn_problem_t *p, const Shape &s, bool packed, int cus) {
+Split split_of(const kda_gdn_problem_t *p, const Shape &s, bool packed, int cus, bool bwd) {
     Split r;
     const bool bf = p->io_dtype == KDA_BF16;
-    const double t_fwd = bf ? 2.1 : 5.9, t_map = bf ? 1.7 : 3.4, t_join = 1.2, t_fixed = 14;
+    // a chunk of the walks that are split (gradients: the keeping forward and the reverse scan), of the maps
+    // and of the reverse scan of the segments
+    const double t_walk = bwd ? (bf ? 5.9 : 10.0) : bf ? 2.1 : 5.9, t_map = bf ? 1.7 : 3.4,
+                 t_rev = bwd ? (bf ? 3.2 : 6.5) : 0, t_join = bwd ? 2.4 : 1.2, t_fixed = bwd ? 42 : 14;
     const int64_t cols = p->head_dim_v / 32, both = cols + p->head_dim_k / 32, C = kda::gdn::chunk_of(p->io_dtype);
     const int64_t chains = (int64_t)s.num_seqs * p->num_heads_v, chunks = (p->seq_len + C - 1) / C;
     if (packed || chains <= 0) return r;
-    double least = 0.9 * t_fwd * (double)chunks;
+    double least = 0.9 * t_walk * (double)chunks;
     int64_t per = 0;
-    for (int64_t n = 2; n * chains * cols <= cus && 2 * n <= chunks; ++n) {  // one round for the forward
-        const int64_t rounds = ((n - 1) * chains * both + cus - 1) / cus, len = (chunks + n - 1) / n;
-        const double t = (double)len * (t_fwd + t_map * (double)rounds) + t_join * (double)n + t_fixed;
+    for (int64_t n = 2; n * chains * cols <= cus && 2 * n <= chunks; ++n) {  // one round for the walks themselves
+        const int64_t maps = bwd ? n : n - 1, rounds = (maps * chains * both + cus - 1) / cus, len = (chunks + n - 1) / n;
+        const double t = (double)len * (t_walk + t_map * (double)rounds + t_rev) + t_join * (double)n + t_fixed;
         if (t < least) {
             least = t;
             per = len;
@@ -215,11 +222,40 @@ Split split_of(const kda_gdn_problem_t *p, const Shape &s, bool packed, int cus)
     return r;
 }
 
+// The `maps` of segments first .. first + run - 1 of the walk r (mode 1 or 2) into h and m, and the states that
+// enter every segment into h, as the walk's starting states.
+kda_status_t enter_segments(const kda_gdn_problem_t *p, const Split &split, int mode, int first, int run, float *h,
+                            const void *s0, kda::gdn::GdnParams &r, hipStream_t hs) {
+    const int batch = r.num_seqs;
+    r.segs = r.seg_run = split.segs;
+    r.seg_len = split.seg_len;
+    r.num_seqs = batch * split.segs;
+    kda::gdn::GdnParams maps = r;
+    maps.maps = 1;
+    maps.seg_first = first;
+    maps.seg_run = run;
+    maps.num_seqs = batch * run;
+    maps.s0 = nullptr;
+    maps.out = maps.hs = maps.zs = nullptr;
+    maps.sf = h;
+    maps.sf_bf16 = 0;
+    float *m = h + split.h / sizeof(float);
+    if (mode == 1) maps.sm = m;
+    kda_status_t st = done(launch_scan(p, mode, maps, hs), "kda_gdn segment launch");
+    if (st != KDA_OK) return st;
+    const kda::gdn::JoinParams join{s0,    h, m, batch, split.segs, p->num_heads_v, p->head_dim_k, p->head_dim_v,
+                                    p->state_dtype == KDA_BF16, mode == 2};
+    r.s0 = h;
+    r.s0_bf16 = 0;
+    return done(kda::gdn::launch_join(join, hs), "kda_gdn join launch");
+}
+
 // Workspace of the backward: S and dS per chunk slot, Z per token; on fp32 operands also the copies of the
-// tensors in bf16 (q, k, v, d_out, dq, dk, dv).
+// tensors in bf16 (q, k, v, d_out, dq, dk, dv); where the walks are split, the segments' maps.
 struct BwdLayout {
     int64_t slots = 0;
-    size_t dhs = 0, zs = 0, copies = 0, qk = 0, vo = 0, bytes = 0;
+    size_t dhs = 0, zs = 0, copies = 0, qk = 0, vo = 0, maps = 0, bytes = 0;
+    Split split;
 };
 kda_status_t bwd_layout(const kda_gdn_problem_t *p, const Shape &s, bool packed, BwdLayout &b) {
     const bool wide = bwd_wide(p, s);
@@ -237,6 +273,11 @@ kda_status_t bwd_layout(const kda_gdn_problem_t *p, const Shape &s, bool packed,
         b.vo = align(s.tokens * s.v_row * 4);
         b.bytes += 4 * b.qk + 3 * b.vo;
     }
+    kda_gdn_problem_t run = *p;
+    if (wide) run.io_dtype = KDA_F32;
+    b.split = split_of(&run, s, packed, current_cus(), true);
+    b.maps = b.bytes;
+    b.bytes += b.split.bytes;
     return KDA_OK;
 }
 
@@ -274,27 +315,10 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
         r.out = out;
         if (s.num_seqs == 0 || (s.tokens == 0 && !final_state)) return done(hipSuccess, "");
         hipStream_t hs = static_cast<hipStream_t>(stream);
-        const Split split = workspace ? split_of(problem, s, cu_seqlens != nullptr, current_cus()) : Split();
+        const Split split = workspace ? split_of(problem, s, cu_seqlens != nullptr, current_cus(), false) : Split();
         if (split.segs > 0 && workspace_bytes >= split.bytes) {
-            float *h = static_cast<float *>(workspace);
-            r.num_seqs = s.num_seqs * split.segs;
-            r.segs = split.segs;
-            r.seg_len = split.seg_len;
-            kda::gdn::GdnParams maps = r;
-            maps.s0 = nullptr;
-            maps.out = nullptr;
-            maps.num_seqs -= s.num_seqs;
-            maps.sf = h;
-            maps.sf_bf16 = 0;
-            maps.sm = h + split.h / sizeof(float);
-            st = done(launch_scan(problem, 1, maps, hs), "kda_gdn_chunk_fwd segment launch");
+            st = enter_segments(problem, split, 1, 0, split.segs - 1, static_cast<float *>(workspace), initial_state, r, hs);
             if (st != KDA_OK) return st;
-            const kda::gdn::JoinParams join{initial_state, h, maps.sm, s.num_seqs, split.segs, problem->num_heads_v,
-                                            problem->head_dim_k, problem->head_dim_v, problem->state_dtype == KDA_BF16};
-            st = done(kda::gdn::launch_join(join, hs), "kda_gdn_chunk_fwd join launch");
-            if (st != KDA_OK) return st;
-            r.s0 = h;
-            r.s0_bf16 = 0;
         }
         return done(launch_scan(problem, 0, r, hs), "kda_gdn_chunk_fwd launch");
     } catch (...) {
@@ -309,7 +333,7 @@ kda_status_t kda_gdn_chunk_fwd_workspace(const kda_gdn_problem_t *problem, size_
     const bool packed = problem && problem->num_seqs > 0;
     kda_status_t st = check_shape(problem, packed, s);
     if (st != KDA_OK) return st;
-    *bytes = split_of(problem, s, packed, current_cus()).bytes;
+    *bytes = split_of(problem, s, packed, current_cus(), false).bytes;
     return done(hipSuccess, "");
 }
 
@@ -401,7 +425,7 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
         rev.out = dv;
         rev.hs = ws + b.dhs;
         kda::gdn::GradParams grad{};
-        grad.f = rev;
+        grad.f = rev;  // before the walk is split
         grad.hs = keep.hs;
         grad.dhs = rev.hs;
         grad.zs = keep.zs;
@@ -411,8 +435,17 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
         grad.dg = dg;
         grad.dbeta = dbeta;
         grad.slots = b.slots;
+        float *maps = reinterpret_cast<float *>(ws + b.maps);
         if (s.tokens > 0) {
+            if (b.split.segs > 0) {
+                st = enter_segments(&run, b.split, 1, 0, b.split.segs, maps, initial_state, keep, hs);
+                if (st != KDA_OK) return st;
+            }
             st = done(launch_scan(&run, 1, keep, hs), "kda_gdn_chunk_bwd forward launch");
+            if (st != KDA_OK) return st;
+        }
+        if (b.split.segs > 0) {  // the segments' M serve again, transposed
+            st = enter_segments(&run, b.split, 2, 1, b.split.segs - 1, maps, d_final_state, rev, hs);
             if (st != KDA_OK) return st;
         }
         st = done(launch_scan(&run, 2, rev, hs), "kda_gdn_chunk_bwd reverse launch");
@@ -470,7 +503,7 @@ kda_status_t kda_gdn_decode(const kda_gdn_problem_t *problem, const void *q, con
             std::sort(used.begin(), used.end());
             const auto twice = std::adjacent_find(used.begin(), used.end());
             if (twice != used.end())
-                return set_error(KDA_ERR_INVALID_ARGUMENT, "state_slots names slot %d twice", *twice);
+                return set_error(KDA_ERR_INVALID_ARGUMENT, "state_slots: two sequences' slots are both %d", *twice);
         }
         if (s.num_seqs == 0 || s.tokens == 0 || num_slots == 0) return done(hipSuccess, "");
         kda::gdn::DecodeParams r{};

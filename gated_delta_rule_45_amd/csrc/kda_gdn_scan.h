@@ -225,11 +225,11 @@ __device__ __forceinline__ Walk walk_of(const GdnParams &p, char *smem) {
     w.ident = w.col0 >= p.dv;
     if (w.ident) w.col0 -= p.dv;
     if (p.segs) {
-        if (p.sm) w.n += w.n / (p.segs - 1);  // the last segments are left out
-        const int at = w.n % p.segs * p.seg_len;
-        w.tok0 = (int64_t)(w.n / p.segs) * p.T + at;
+        const int seq = w.n / p.seg_run, seg = p.seg_first + w.n % p.seg_run, at = seg * p.seg_len;
+        w.n = seq * p.segs + seg;
+        w.tok0 = (int64_t)seq * p.T + at;
         w.len = min(p.seg_len, p.T - at);
-        w.slot0 = 0;
+        w.slot0 = (int64_t)seq * ((p.T + C - 1) / C) + at / C;
     } else if (p.cu) {
         // offsets outside the tokens are cut off rather than followed
         const int a = min(max(p.cu[w.n], 0), p.T), b = min(max(p.cu[w.n + 1], a), p.T);
@@ -1229,7 +1229,8 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
             for (int u = 0; u < RT / 2; ++u)
 #pragma unroll
                 for (int ct = 0; ct < KT; ++ct) mma<BF>(S[ct], kt[ct][u], dx[u]);
-            put_value_rows<BF, L::VRB, RT>(V, static_cast<IO *>(p.out) + (tok * p.Hv + w.h) * p.dv + w.col0,
+            if (p.out)
+                put_value_rows<BF, L::VRB, RT>(V, static_cast<IO *>(p.out) + (tok * p.Hv + w.h) * p.dv + w.col0,
                                            (int64_t)p.Hv * p.dv, wave, x, clen, lane);
         }
 #pragma unroll
@@ -1238,8 +1239,8 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
         if (!REV && s + 1 < nch) fetch(s + 1);
         __syncthreads();  // B
     }
-    const bool part = p.segs && !p.sm;  // the state of a sequence is its last segment's
-    if ((p.sf || w.ident) && (!part || w.n % p.segs == p.segs - 1)) {
+    const bool part = p.segs && !p.maps;  // a sequence's state is that of the last segment walked
+    if ((p.sf || w.ident) && (!part || w.n % p.segs == (MODE == kRev ? 0 : p.segs - 1))) {
         // formed anew: otherwise the 64-bit addresses of the first loads stay in registers over the whole walk
         int q4b = q4;
         asm volatile("" : "+v"(q4b));

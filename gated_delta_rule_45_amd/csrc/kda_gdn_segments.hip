@@ -1,4 +1,5 @@
-// Joins the segments of a walk that was split over its length.  A chunk takes the state S to
+// Joins the segments of a walk that was split over its length.  (Gradients: the same with M transposed, from the
+// last segment to the first, H from a reverse walk of each segment.)  A chunk takes the state S to
 // (e^{G_C} I - ..) S + .., a linear map, so a whole segment takes it to M S + H.  One scan over the segments
 // side by side gives H (from a zero state) and M (from the identity and no values); this kernel then walks
 // the few segments, S <- M_p S + H_p, and leaves the state entering each of them where H_p was.
@@ -14,7 +15,7 @@ namespace kda {
 namespace gdn {
 namespace {
 
-template <int DK>
+template <int DK, bool REV>
 __global__ void __launch_bounds__(4 * DK) gdn_join_kernel(JoinParams p) {
     constexpr int KT = DK / 16, LD = DK + 4;
     __shared__ __attribute__((aligned(16))) float St[2][16 * LD];
@@ -35,12 +36,19 @@ __global__ void __launch_bounds__(4 * DK) gdn_join_kernel(JoinParams p) {
         Frag<false> m[KT];
         f32x4 h;
     };
-    auto at = [&](int s) { return (b * p.segs + s) * p.Hv + h; };
+    auto at = [&](int s) { return (b * p.segs + (REV ? p.segs - 1 - s : s)) * p.Hv + h; };
     auto load = [&](Maps &x, int s) {
-        const float *M = p.m + at(s) * DK * DK + (16 * wave + l16) * DK + 4 * q4;
+        const float *M = p.m + at(s) * DK * DK + (REV ? 4 * q4 * DK + 16 * wave + l16 : (16 * wave + l16) * DK + 4 * q4);
         const float *H = p.h + (at(s) * DK + row) * p.dv + col;
 #pragma unroll
-        for (int t = 0; t < KT; ++t) x.m[t].v = *reinterpret_cast<const float4 *>(M + 16 * t);
+        for (int t = 0; t < KT; ++t) {
+            if constexpr (REV) {
+                const float *m = M + 16 * t * DK;
+                x.m[t].v = make_float4(m[0], m[DK], m[2 * DK], m[3 * DK]);
+            } else {
+                x.m[t].v = *reinterpret_cast<const float4 *>(M + 16 * t);
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) x.h[j] = H[(int64_t)j * p.dv];
     };
@@ -80,9 +88,12 @@ __global__ void __launch_bounds__(4 * DK) gdn_join_kernel(JoinParams p) {
 hipError_t launch_join(const JoinParams &p, hipStream_t stream) {
     const int64_t blocks = (int64_t)p.batch * p.Hv * (p.dv / 16);
     if (blocks <= 0) return hipSuccess;
-    if (p.dk == 64) hipLaunchKernelGGL((gdn_join_kernel<64>), dim3((unsigned)blocks), dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL((gdn_join_kernel<128>), dim3((unsigned)blocks), dim3(512), 0, stream, p);
-    return hipGetLastError();
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3((unsigned)(4 * p.dk)), 0, stream, p);
+        return hipGetLastError();
+    };
+    if (p.dk == 64) return p.reverse ? go(gdn_join_kernel<64, true>) : go(gdn_join_kernel<64, false>);
+    return p.reverse ? go(gdn_join_kernel<128, true>) : go(gdn_join_kernel<128, false>);
 }
 
 }  // namespace gdn

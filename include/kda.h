@@ -457,7 +457,9 @@ kda_status_t kda_gdn_chunk_fwd_workspace(const kda_gdn_problem_t *problem, size_
  *  dg, dbeta        [tokens, Hv] gate dtype
  *  d_initial_state  [num_seqs, Hv, d_k, d_v] state dtype, or NULL to skip it
  *  workspace        kda_gdn_chunk_bwd_workspace() bytes, 256-byte aligned: the states entering the chunks and
- *                   the gradients of those leaving them (bf16 or fp32, the io dtype) and one value tensor
+ *                   the gradients of those leaving them (bf16 or fp32, the io dtype) and one value tensor; a
+ *                   plain batch of few sequences and heads is split over its length as in the forward, and
+ *                   the segments' maps are here too
  * No output may overlap anything else.  beta = 0 has its gradients like any other beta.  The results repeat
  * bit for bit.  Calls that overlap in time need a workspace each.  Errors as for kda_chunk_bwd.
  */
@@ -467,7 +469,7 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
                                void *dk, void *dv, void *dg, void *dbeta, void *d_initial_state, void *workspace,
                                size_t workspace_bytes, void *stream);
 
-/* Workspace bytes kda_gdn_chunk_bwd needs (a packed batch where problem->num_seqs > 0); *bytes = 0 on error. */
+/* Workspace bytes kda_gdn_chunk_bwd needs on the current device (a packed batch where problem->num_seqs > 0); *bytes = 0 on error. */
 kda_status_t kda_gdn_chunk_bwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes);
 
 /*

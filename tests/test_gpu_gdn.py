@@ -578,3 +578,37 @@ def test_split_forward_captured_and_workspaces_of_the_caller():
     none = torch.empty(0, dtype=torch.uint8, device=DEV)
     a, b = kda.gdn_chunk_fwd(*x, workspace=small), kda.gdn_chunk_fwd(*x, workspace=none)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("io,sdt", [(BF, F32), (BF, BF), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T", [2048, 1300 + 1])
+def test_backward_split_over_its_length(io, sdt, dk, dv, T):
+    x = ref.inputs(1, T, 1, 2, dk, dv, io, seed=T + dk, device=DEV)
+    x[3].mul_(0.05)
+    s0, dsf = state(1, 2, dk, dv, sdt), state(1, 2, dk, dv, sdt, seed=8)
+    got, do = check_bwd(x, s0, dsf, scale=dk ** -0.5, label=f"split T{T}")
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)  # the same as a packed batch: one walk
+    one = kda.gdn_chunk_bwd(*x, do, s0, dsf, cu, scale=dk ** -0.5)
+    assert not torch.equal(one["dk"], got["dk"])  # two ways of summing
+    again = kda.gdn_chunk_bwd(*x, do, s0, dsf, scale=dk ** -0.5)
+    assert all(torch.equal(again[k], got[k]) for k in got)
+    bare, _ = check_bwd(x, scale=dk ** -0.5, label="without states", need_d_initial_state=False)
+    assert bare["d_initial_state"] is None
+
+
+def test_backward_split_with_many_sequences_and_captured():
+    x = ref.inputs(3, 2100, 2, 4, 128, 64, BF, seed=4, device=DEV)
+    x[3].mul_(0.05)
+    got, do = check_bwd(x, state(3, 4, 128, 64, F32), state(3, 4, 128, 64, F32, seed=9), label="three sequences")
+    want = kda.gdn_chunk_bwd(*x, do)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        caught = kda.gdn_chunk_bwd(*x, do)
+    for i in range(4):
+        for t in caught.values():
+            t.fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(caught[k], want[k]) for k in want), i
+        eager = kda.gdn_chunk_bwd(*x, do)
+        assert all(torch.equal(eager[k], want[k]) for k in want), i
