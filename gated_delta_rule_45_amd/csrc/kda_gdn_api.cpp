@@ -170,8 +170,8 @@ hipError_t launch_scan(const kda_gdn_problem_t *p, int mode, const kda::gdn::Gdn
 
 // Whether the gradients of a bf16 call are computed on fp32 operands.  With few gates' gradients the
 // roundings of the products' operands do not average out (260 values: the norm of the error of dg up
-// to 5.7e-3 of dg's, 3e-3 for thousands of values and about 1e-6 on fp32 operands), and so short a call
-// is bound by its launches either way.
+// to 5.7e-3 of dg's, 3e-3 for thousands of values and about 1e-6 on fp32 operands).  It costs 123 against
+// about 50 us at 256 tokens of one head.
 bool bwd_wide(const kda_gdn_problem_t *p, const Shape &s) {
     return p->io_dtype == KDA_BF16 && s.tokens <= 256 && s.tokens * p->num_heads_v <= 512;
 }
@@ -187,8 +187,7 @@ bool bwd_wide(const kda_gdn_problem_t *p, const Shape &s) {
 // 8 heads of 128 x 128, bf16: one walk against the split 74 / 66 us at 2,048 tokens, 272 / 134 at 8,192,
 // 1,068 / 408 at 32,768; at 1,024 tokens 41 / 45, at 32 heads and 8,192 tokens 270 / 376: one walk.
 // Gradients, the same heads: 241 / 203 at 2,048 tokens, 644 / 329 at 8,192; at 1,024 171 / 179: one walk; fp32
-// 790 / 417 at 2,048.  Packed batches, whose
-// lengths the host does not know, are not split.
+// 790 / 417 at 2,048.  Packed batches, whose lengths the host does not know, are not split.
 struct Split {
     int32_t segs = 0, seg_len = 0;
     size_t h = 0, bytes = 0;  // offset of M, size
