@@ -15,7 +15,7 @@ from typing import Optional
 
 import torch
 
-from . import _P, _check, _io_code, _need, _ptr, library
+from . import _P, _check, _io_code, _need, library
 
 __all__ = ["gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode", "norm_gate_bwd"]
 
@@ -49,13 +49,15 @@ class _Launch:
     def __init__(self, device: torch.device, stream):
         if device.type != "cuda":
             raise ValueError(f"tensors must be on a GPU, got {device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, expected {device}")
         cur = torch.cuda.current_stream(device)
         self.other = None
         if stream is not None and stream != cur:
             self.other = torch.cuda.stream(stream)
         elif device.index is not None and device.index != torch.cuda.current_device():
             self.other = torch.cuda.device(device)
-        self.handle = ctypes.c_void_p((stream if stream is not None else cur).cuda_stream)
+        self.handle = (stream if stream is not None else cur).cuda_stream
 
     def __enter__(self):
         if self.other is not None:
@@ -65,6 +67,22 @@ class _Launch:
     def __exit__(self, *exc):
         if self.other is not None:
             self.other.__exit__(*exc)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _dense(t, dtype, shape, like: torch.Tensor) -> bool:
+    """The checks of a call in one go (a few us of host time are most of a small call); what fails here is
+    named by the slower ones."""
+    return (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == like.get_device()
+            and t.is_contiguous())
+
+
+def _want(t, name: str, dtype, shape, like: torch.Tensor) -> None:
+    if not _dense(t, dtype, shape, like):
+        _need(t, name, dtype, shape, like.device)
 
 
 def _rows(t: torch.Tensor, name: str, dtype, shape, device) -> int:
@@ -107,16 +125,19 @@ def _host_i32(x, n: int, name: str):
 
 def _problem(q, k, v, g, beta, cu_seqlens, state_dtype, scale):
     """Checks of the inputs that every call shares."""
-    if q.dim() != 4 or v.dim() != 4:
+    qs, vs, gate = q.shape, v.shape, g.dtype
+    if len(qs) != 4 or len(vs) != 4:
         raise ValueError("q, k and v must be [B, T, heads, d]")
-    B, T, Hk, dk = q.shape
-    Hv, dv = v.shape[2], v.shape[3]
-    dev, dt = q.device, q.dtype
+    B, T, Hk, dk = qs
+    Hv, dv = vs[2], vs[3]
+    dt = q.dtype
     io = _io_code(dt)
-    lq, lk = _rows(q, "q", dt, q.shape, dev), _rows(k, "k", dt, q.shape, dev)
-    lv = _rows(v, "v", dt, (B, T, Hv, dv), dev)
-    _need(g, "g", g.dtype, (B, T, Hv), dev)
-    _need(beta, "beta", g.dtype, (B, T, Hv), dev)
+    # 0: dense
+    lq = 0 if q.is_contiguous() else _rows(q, "q", dt, qs, q.device)
+    lk = 0 if _dense(k, dt, qs, q) else _rows(k, "k", dt, qs, q.device)
+    lv = 0 if _dense(v, dt, (B, T, Hv, dv), q) else _rows(v, "v", dt, (B, T, Hv, dv), q.device)
+    _want(g, "g", gate, (B, T, Hv), q)
+    _want(beta, "beta", gate, (B, T, Hv), q)
     n = B
     if cu_seqlens is not None:
         if B != 1:
@@ -124,8 +145,8 @@ def _problem(q, k, v, g, beta, cu_seqlens, state_dtype, scale):
         n = cu_seqlens.numel() - 1
         if n < 0:
             raise ValueError("cu_seqlens needs at least one entry")
-        _need(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev)
-    p = GdnProblem(B, T, n if cu_seqlens is not None else 0, Hk, Hv, dk, dv, io, _io_code(g.dtype),
+        _want(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), q)
+    p = GdnProblem(B, T, n if cu_seqlens is not None else 0, Hk, Hv, dk, dv, io, _io_code(gate),
                    _io_code(state_dtype), scale, lq, lk, lv)
     return p, n
 
@@ -146,15 +167,15 @@ def gdn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     p, n = _problem(q, k, v, g, beta, cu_seqlens, sdt, scale)
     dev, shape, states = q.device, v.shape, (n, v.shape[2], q.shape[3], v.shape[3])
     if initial_state is not None:
-        _need(initial_state, "initial_state", sdt, states, dev)
+        _want(initial_state, "initial_state", sdt, states, q)
     host = _host_i32(cu_seqlens_host, n + 1, "cu_seqlens_host")
     with _Launch(dev, stream) as handle:
         if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=dev)
+            out = q.new_empty(shape)
         else:
-            _need(out, "out", q.dtype, shape, dev)
+            _want(out, "out", q.dtype, shape, q)
         if final_state is not None:
-            _need(final_state, "final_state", sdt, states, dev)
+            _want(final_state, "final_state", sdt, states, q)
         elif output_final_state:
             final_state = torch.empty(states, dtype=sdt, device=dev)
         if workspace is None and cu_seqlens is None and q.shape[1] >= _SPLIT_TOKENS:
@@ -190,11 +211,11 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     sdt = given.dtype if given is not None else torch.float32
     p, n = _problem(q, k, v, g, beta, cu_seqlens, sdt, scale)
     dev, states = q.device, (n, v.shape[2], q.shape[3], v.shape[3])
-    _need(d_out, "d_out", q.dtype, v.shape, dev)
+    _want(d_out, "d_out", q.dtype, v.shape, q)
     if initial_state is not None:
-        _need(initial_state, "initial_state", sdt, states, dev)
+        _want(initial_state, "initial_state", sdt, states, q)
     if d_final_state is not None:
-        _need(d_final_state, "d_final_state", sdt, states, dev)
+        _want(d_final_state, "d_final_state", sdt, states, q)
     host = _host_i32(cu_seqlens_host, n + 1, "cu_seqlens_host")
     lib = library()
     want = {"dq": (q.shape, q.dtype), "dk": (q.shape, q.dtype), "dv": (v.shape, q.dtype), "dg": (g.shape, g.dtype),
@@ -206,7 +227,7 @@ def gdn_chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
         else:
             for name, (s, t) in want.items():
                 if name != "d_initial_state" or out.get(name) is not None:
-                    _need(out[name], name, t, s, dev)
+                    _want(out[name], name, t, s, q)
         if workspace is None:
             need = ctypes.c_size_t(0)
             _check(lib.kda_gdn_chunk_bwd_workspace(ctypes.byref(p), ctypes.byref(need)))
@@ -229,16 +250,16 @@ def gdn_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
     most once; a slot outside the pool marks a padded row, whose outputs are not written.  Returns out."""
     p, n = _problem(q, k, v, g, beta, cu_seqlens, state.dtype, scale)
     dev, shape = q.device, v.shape
-    _need(state, "state", state.dtype, (state.shape[0], shape[2], q.shape[3], shape[3]), dev)
+    _want(state, "state", state.dtype, (state.shape[0], shape[2], q.shape[3], shape[3]), q)
     if state_slots is not None:
-        _need(state_slots, "state_slots", torch.int32, (n,), dev)
+        _want(state_slots, "state_slots", torch.int32, (n,), q)
     host = _host_i32(cu_seqlens_host, n + 1, "cu_seqlens_host")
     slots_host = _host_i32(state_slots_host, n, "state_slots_host")
     with _Launch(dev, stream) as handle:
         if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=dev)
+            out = q.new_empty(shape)
         else:
-            _need(out, "out", q.dtype, shape, dev)
+            _want(out, "out", q.dtype, shape, q)
         _check(library().kda_gdn_decode(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
                                         state.shape[0], _ptr(state_slots), _ptr(slots_host), _ptr(cu_seqlens),
                                         _ptr(host), _ptr(out), handle))
@@ -249,11 +270,11 @@ def norm_gate_bwd(o: torch.Tensor, gate: torch.Tensor, weight: torch.Tensor, d_o
                   workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients of norm_gate (o: its input) for L = sum(d_out * out).  o, gate, d_out: same shape and dtype
     (bf16 or fp32), contiguous; weight: fp32 [d].  Returns (d_o, d_gate, d_weight)."""
-    dev, d, shape = o.device, o.shape[-1], tuple(o.shape)
-    _need(o, "o", o.dtype, shape, dev)
-    _need(gate, "gate", o.dtype, shape, dev)
-    _need(d_out, "d_out", o.dtype, shape, dev)
-    _need(weight, "weight", torch.float32, (d,), dev)
+    dev, d, shape = o.device, o.shape[-1], o.shape
+    _want(o, "o", o.dtype, shape, o)
+    _want(gate, "gate", o.dtype, shape, o)
+    _want(d_out, "d_out", o.dtype, shape, o)
+    _want(weight, "weight", torch.float32, (d,), o)
     rows, io, lib = o.numel() // d if d else 0, _io_code(o.dtype), library()
     need = lib.kda_norm_gate_bwd_workspace(rows, d, io)
     with _Launch(dev, stream) as handle:

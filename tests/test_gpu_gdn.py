@@ -612,3 +612,18 @@ def test_backward_split_with_many_sequences_and_captured():
         assert all(torch.equal(caught[k], want[k]) for k in want), i
         eager = kda.gdn_chunk_bwd(*x, do)
         assert all(torch.equal(eager[k], want[k]) for k in want), i
+
+
+def test_arguments_are_named_in_errors():
+    x = ref.inputs(1, 40, 2, 4, 64, 64, BF, seed=3, device=DEV)
+    q, k, v, g, b = x
+    for args, name in (((q, k.float(), v, g, b), "k"), ((q, k, v.cpu(), g, b), "v"), ((q, k, v, g[:, :39], b), "g"),
+                       ((q, k, v, g, b.to(torch.float64)), "beta"), ((q, k, v[..., :32], g, b), "v"),
+                       ((q, k[:, ::2], v, g, b), "k"), ((q, k, v.transpose(1, 2), g, b), "v")):
+        with pytest.raises((TypeError, ValueError), match=f"^{name}\\b"):
+            kda.gdn_chunk_fwd(*args)
+    with pytest.raises(ValueError, match="^initial_state"):
+        kda.gdn_chunk_fwd(*x, torch.zeros(2, 4, 64, 64, device=DEV))
+    with pytest.raises(TypeError, match="^state_slots"):
+        kda.gdn_decode(*[t[:, :1].contiguous() for t in x], torch.zeros(3, 4, 64, 64, device=DEV),
+                       torch.zeros(1, dtype=torch.int64, device=DEV))
