@@ -430,7 +430,8 @@ typedef struct {
  *  workspace       optional, 256-byte aligned: with at least kda_gdn_chunk_fwd_workspace() bytes, where that is not
  *                  0, a plain batch of few sequences and heads is split over its length (the segments' maps of
  *                  the state side by side, joined, then the segments; the results then differ in their
- *                  rounding from one walk's); otherwise it is not used
+ *                  rounding from one walk's, and a recurrence that grows, beta |k|^2 > 2, may overflow in a
+ *                  map where it does not in the walk); otherwise it is not used
  * Nothing is allocated: the call can be captured, and run on several streams at once with a workspace each.
  * A NaN or infinity reaches the results of its own sequence only, from the start of its chunk (64 tokens in
  * bf16, 32 in fp32) on.
