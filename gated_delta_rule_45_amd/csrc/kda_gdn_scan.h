@@ -1015,13 +1015,10 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
     } else {
         load_state(static_cast<const float *>(p.s0));
     }
-    if (nch > 0) {
-        __syncthreads();
-        __syncthreads();
-        __syncthreads();
-    }
     // K's and the values' fragments of a chunk are read before the barrier that opens its step: they have been in
-    // LDS for a step by then
+    // LDS for a step by then.  In the forward each chain wave stores over half of both waves' values (the second terms
+    // of Y) before the step's middle barrier, so a barrier must stand between these reads and its step: B of
+    // the step before, and for chunk 0, which the first opening barrier puts in LDS, the third.
     Frag2<BF> kf[RT][K2];
     Frag<BF> vf[RT];
     auto fetch = [&](int s) {
@@ -1034,8 +1031,13 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
             if (MODE == kKeep && w.ident) vf[rt] = make_frag<BF>(0.f, 0.f, 0.f, 0.f);
         }
     };
-    // (not in reverse, which has no registers left for them)
-    if (!REV && nch > 0) fetch(0);
+    // (not in reverse, which has no registers left for them, and where a wave stores over its own columns only)
+    if (nch > 0) {
+        __syncthreads();
+        if (!REV) fetch(0);
+        __syncthreads();
+        __syncthreads();
+    }
 #pragma unroll 1
     for (int s = 0; s < nch; ++s) {
         const int c = ci(s), clen = min(C, w.len - c * C);
@@ -1122,7 +1124,8 @@ __global__ void __launch_bounds__((Lds<BF, DK, CT, MODE>::NT)) gdn_scan_kernel(G
                 if constexpr (MODE == kFwd) {
                     const Frag2<BF> yp = {frag_from_acc<BF>(a[0]), frag_from_acc<BF>(a[1])};
                     hand_put<BF>(hand + L::HS, u, lane, yp);
-                    // the second term goes where the chunk's values were, which both chain waves have read
+                    // the second term goes where the chunk's values were, which both chain waves have read before
+                    // the barrier that opened this step
                     if constexpr (BF)
                         hand_put<BF>(V + wave * (L::VB / 2), u, lane, Frag2<BF>{frag_lo(a[0], yp.a), frag_lo(a[1], yp.b)});
                 }
