@@ -1,0 +1,81 @@
+"""GPU tests of the scalar-gate delta rule at values and sizes that a program meets seldom: a NaN among the gates."""
+import math
+
+import pytest
+import torch
+
+import gdn_reference as ref
+import gated_delta_rule_45_amd as kda
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+KEYS = ("dq", "dk", "dv", "dg", "dbeta", "d_initial_state")
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def states(n, Hv, dk, dv, dtype=F32, std=0.3, seed=7):
+    return (std * torch.randn(n, Hv, dk, dv, generator=torch.Generator().manual_seed(seed))).to(dtype).to(DEV)
+
+
+def like(x, seed=11):
+    return torch.randn(x.shape, generator=torch.Generator().manual_seed(seed)).to(x.dtype).to(DEV)
+
+
+# ---------------------------------------------------------------------------------- a NaN gate --
+@pytest.mark.parametrize("io,gates", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("T,at", [(1, 0), (70, 3), (200, 100), (200, 199)])
+def test_a_nan_gate_reaches_its_results(io, gates, T, at):
+    """Wherever the definition gives a NaN, so do the kernels; other heads and sequences keep their bits."""
+    say(f"[{io} gates {gates}] T={T} at {at}")
+    x = ref.inputs(2, T, 2, 4, 64, 64, io, gates, seed=T, device=DEV)
+    s0, dsf, do = states(2, 4, 64, 64), states(2, 4, 64, 64, seed=8), like(x[2])
+    bad = [t.clone() for t in x]
+    bad[3][1, at, 2] = float("nan")  # value head 2, with head 3 on key head 1
+    (o, f), (ob, fb) = kda.gdn_chunk_fwd(*x, s0), kda.gdn_chunk_fwd(*bad, s0)
+    assert ob[1, at:, 2].isnan().all() and fb[1, 2].isnan().all()
+    assert torch.equal(ob[0], o[0]) and torch.equal(fb[0], f[0])
+    for h in (0, 1, 3):
+        assert torch.equal(ob[1, :, h], o[1, :, h]) and torch.equal(fb[1, h], f[1, h])
+    d, db = kda.gdn_chunk_bwd(*x, do, s0, dsf), kda.gdn_chunk_bwd(*bad, do, s0, dsf)
+    want = ref.delta_rule_grads(*bad, do, s0, dsf)
+    assert want["dq"].isnan().any() and want["dg"].isnan().any()  # (dv not, where the gate is the first token's)
+    for key in KEYS:
+        lost = want[key].isnan() & ~db[key].isnan()
+        assert not lost.any(), (key, int(lost.sum()))
+        assert torch.equal(db[key][0], d[key][0]), key
+    for key in ("dv", "dg", "dbeta"):
+        for h in (0, 1, 3):
+            assert torch.equal(db[key][1, :, h], d[key][1, :, h]), (key, h)
+    for key in ("dq", "dk"):
+        assert torch.equal(db[key][1, :, 0], d[key][1, :, 0]), key
+    # and the recurrent form agrees
+    pool, pool_b = s0.clone(), s0.clone()
+    y, yb = kda.gdn_decode(*x, pool), kda.gdn_decode(*bad, pool_b)
+    assert yb[1, at:, 2].isnan().all() and pool_b[1, 2].isnan().all()
+    assert torch.equal(yb[1, :, 3], y[1, :, 3]) and torch.equal(pool_b[0], pool[0])
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_a_nan_gate_in_a_split_walk(io):
+    T, at = 8192, 5000
+    start = at - at % (64 if io == BF else 32)
+    x = ref.inputs(1, T, 1, 2, 64, 64, io, F32, seed=3, device=DEV)
+    x[3].mul_(0.05)
+    do = like(x[2])
+    o, f = kda.gdn_chunk_fwd(*x)
+    d = kda.gdn_chunk_bwd(*x, do)
+    x[3][0, at, 1] = float("nan")
+    ob, fb = kda.gdn_chunk_fwd(*x)
+    assert ob[0, at:, 1].isnan().all() and fb[0, 1].isnan().all()
+    assert torch.equal(ob[0, :start, 1], o[0, :start, 1])
+    assert torch.equal(ob[0, :, 0], o[0, :, 0]) and torch.equal(fb[0, 0], f[0, 0])
+    db = kda.gdn_chunk_bwd(*x, do)
+    assert db["dg"][0, :at + 1, 1].isnan().all() and db["dv"][0, :at + 1, 1].isnan().all()
+    assert db["dq"][0, at:].isnan().all() and db["d_initial_state"][0, 1].isnan().all()
+    for key in ("dv", "dg", "dbeta"):
+        assert torch.equal(db[key][0, :, 0], d[key][0, :, 0]), key
