@@ -11,8 +11,10 @@
 //     dG_C += sum_i beta_i x_i + e^{G_C} <S, dS>,   dg = reverse cumulative sum of dG over the chunk
 //
 // dX_j is beta_j times a vector, so the quotient has no cancellation where the sums have (repeated keys: error
-// of dbeta 7e-2 of its norm by the sums, 3e-2 so); the sums serve beta = 0, so every beta has its
-// gradient.  The diagonal, where the gate cancels, is left out of dG rather than added and subtracted.
+// of dbeta 7e-2 of its norm by the sums, 3e-2 so).  The sums serve |beta| < 2^-64, so every beta has its
+// gradient: there dX nears the smallest normal number, where it loses its bits (beta = 1e-38: dbeta half off)
+// or is 0.  Repeated keys cancel only as far as beta is near 1.  The diagonal, where the gate cancels, is left
+// out of dG rather than added and subtracted.
 //
 // One workgroup owns (chunk, key head) and walks the value heads that share it, so that dQ and dK are
 // summed over them in registers, in a fixed order.  Two waves own the 16 tokens of row tile r, one
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
                 float cs = 0.f;
                 for (int rr = lane >> 4; rr < RT; ++rr) cs += colsum[rr * C + lane];
                 const float b = gate[2 * C + lane], x = xv[lane] + xv[C + lane];
-                db = b != 0.f ? dxz[lane] / b : cs + diag[lane] + x;
+                db = fabsf(b) < 0x1p-64f ? cs + diag[lane] + x : dxz[lane] / b;
                 bx = b * x;
                 dG = rowv[lane] + rowv[C + lane] - b * cs - bx;
             }

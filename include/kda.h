@@ -461,7 +461,7 @@ kda_status_t kda_gdn_chunk_fwd_workspace(const kda_gdn_problem_t *problem, size_
  *                   the gradients of those leaving them (bf16 or fp32, the io dtype) and one value tensor; a
  *                   plain batch of few sequences and heads is split over its length as in the forward, and
  *                   the segments' maps are here too
- * No output may overlap anything else.  beta = 0 has its gradients like any other beta.  The results repeat
+ * No output may overlap anything else.  beta of 0, or near it, has its gradients like any other.  The results repeat
  * bit for bit.  Calls that overlap in time need a workspace each.  Errors as for kda_chunk_bwd.
  */
 kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,

@@ -1,4 +1,5 @@
-"""GPU tests of the scalar-gate delta rule at values and sizes that a program meets seldom: a NaN among the gates."""
+"""GPU tests of the scalar-gate delta rule at values and sizes that a program meets seldom: a NaN among the
+gates, betas near the smallest number."""
 import math
 
 import pytest
@@ -79,3 +80,33 @@ def test_a_nan_gate_in_a_split_walk(io):
     assert db["dq"][0, at:].isnan().all() and db["d_initial_state"][0, 1].isnan().all()
     for key in ("dv", "dg", "dbeta"):
         assert torch.equal(db[key][0, :, 0], d[key][0, :, 0]), key
+
+
+# ------------------------------------------------------------------------------- tiny betas --
+def close(name, got, want, rel2):
+    g, w = got.double(), want.double()
+    assert torch.isfinite(g).all(), f"{name}: non-finite values"
+    r2 = float((g - w).norm() / w.norm())
+    say(f"  {name}: rel2={r2:.2e}")
+    assert r2 <= rel2, f"{name}: rel2 {r2:.3e} > {rel2}"
+
+
+@pytest.mark.parametrize("io,gates", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("T", [60, 300])
+@pytest.mark.parametrize("tiny", [2.0 ** -63, 2.0 ** -65, 1e-30, 1e-37, 1e-38, 1e-40])
+def test_a_tiny_beta_has_its_gradient(io, gates, T, tiny):
+    """dbeta does not depend on how small its own beta is: what a token with beta near the smallest normal number
+    (or below it) would have written is weighed as for beta = 0.  Bounds as for the other gradients (nine
+    roundings to bf16, 256 fp32 terms)."""
+    say(f"[{io} gates {gates}] T={T} beta={tiny:.2g}")
+    x = ref.inputs(1, T, 2, 4, 64, 64, io, gates, seed=5, device=DEV)
+    x[4][:, ::3] = tiny
+    s0, dsf, do = states(1, 4, 64, 64), states(1, 4, 64, 64, seed=8), like(x[2])
+    got, want = kda.gdn_chunk_bwd(*x, do, s0, dsf), ref.delta_rule_grads(*x, do, s0, dsf)
+    bound = 8e-3 if io == BF or gates == BF else 1.5e-5
+    for key in KEYS:
+        close(key, got[key], want[key], bound)
+    close("dbeta of the tiny ones", got["dbeta"][:, ::3], want["dbeta"][:, ::3], 2e-2 if io == BF else bound)
+    x[4].fill_(tiny)
+    got, want = kda.gdn_chunk_bwd(*x, do, s0, dsf), ref.delta_rule_grads(*x, do, s0, dsf)
+    close("dbeta, all tiny", got["dbeta"], want["dbeta"], bound)
