@@ -66,6 +66,9 @@ struct ConvertRows {
 struct ConvertParams {
     ConvertRows t[4];
     int32_t n;
+    // a packed batch: only the rows of its sequences, cu[0] .. cu[num_seqs] of T, are written; else null
+    const int32_t *cu;
+    int32_t num_seqs, T;
 };
 // widen: bf16 -> fp32, else fp32 -> bf16
 hipError_t launch_convert(bool widen, const ConvertParams &p, hipStream_t stream);

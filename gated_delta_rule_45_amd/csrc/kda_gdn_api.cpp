@@ -407,6 +407,9 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
             dq = copy(back, dq, s.qk_row, s.qk_row, b.qk);
             dk = copy(back, dk, s.qk_row, s.qk_row, b.qk);
             dv = copy(back, dv, s.v_row, s.v_row, b.vo);
+            back.cu = cu_seqlens;  // rows that no sequence owns have no gradients in the copies either
+            back.num_seqs = s.num_seqs;
+            back.T = problem->seq_len;
             run.io_dtype = KDA_F32;
             s.ldq = s.ldk = s.qk_row;
             s.ldv = s.v_row;

@@ -10,8 +10,14 @@ namespace {
 template <bool WIDEN>
 __global__ void __launch_bounds__(256) convert_kernel(ConvertParams p) {
     const ConvertRows t = p.t[blockIdx.y];
-    const int64_t per = t.cols / 8, n = t.rows * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t per = t.cols / 8;
+    int64_t first = 0, n = t.rows * per;
+    if (p.cu) {
+        const int a = min(max(p.cu[0], 0), p.T), b = min(max(p.cu[p.num_seqs], a), p.T);
+        first = a * per;
+        n = b * per;
+    }
+    for (int64_t i = first + (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / per, c = i % per * 8;
         uint16_t *b = static_cast<uint16_t *>(t.bf16) + row * t.ld + c;
         float *f = static_cast<float *>(t.f32) + row * t.cols + c;

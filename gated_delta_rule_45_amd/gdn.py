@@ -7,6 +7,10 @@ of libkda.so.
 q, k have Hk heads, v, g, beta, out and the states Hv (a multiple of Hk); value head h reads key head
 h // (Hv // Hk).  q, k and v may be slices of one projection's output: the heads of a token dense, the
 tokens a constant multiple of 16 bytes apart.  g and beta are both fp32 or both bf16, states fp32 or bf16.
+
+Rows that no sequence of cu_seqlens owns (a padded packed batch) and the rows of padded slots are not written: in
+tensors allocated here they hold whatever the memory held.  Where they are read later (a weight's gradient
+sums over all rows of dq, dk and dv), pass `out` with what they are to hold, zeros for instance.
 """
 from __future__ import annotations
 

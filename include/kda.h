@@ -426,6 +426,8 @@ typedef struct {
  *  initial_state, final_state      [num_seqs, Hv, d_k, d_v] state dtype, either may be NULL (zero, not
  *                                  written); they may be the same buffer
  *  cu_seqlens, cu_seqlens_host     as for kda_chunk_fwd; offsets outside the tokens are cut off
+ *                                  (without the host copy the sequences may end before seq_len: rows of out,
+ *                                  or of gradients, that none of them owns are left as they are)
  *  out   [tokens, Hv, d_v]         io dtype, dense
  *  workspace       optional, 256-byte aligned: with at least kda_gdn_chunk_fwd_workspace() bytes, where that is not
  *                  0, a plain batch of few sequences and heads is split over its length (the segments' maps of

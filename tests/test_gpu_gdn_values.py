@@ -1,5 +1,5 @@
 """GPU tests of the scalar-gate delta rule at values and sizes that a program meets seldom: a NaN among the
-gates, betas near the smallest number."""
+gates, betas near the smallest number, rows that no sequence owns."""
 import math
 
 import pytest
@@ -110,3 +110,23 @@ def test_a_tiny_beta_has_its_gradient(io, gates, T, tiny):
     x[4].fill_(tiny)
     got, want = kda.gdn_chunk_bwd(*x, do, s0, dsf), ref.delta_rule_grads(*x, do, s0, dsf)
     close("dbeta, all tiny", got["dbeta"], want["dbeta"], bound)
+
+
+# ------------------------------------------------------------------ rows that no sequence owns --
+@pytest.mark.parametrize("gates", [BF, F32])
+def test_rows_of_a_small_packed_batch_that_no_sequence_owns_are_left_alone(gates):
+    """As for larger batches (few gates: bf16 gradients on fp32 operands)."""
+    lens, extra = [20, 0, 3, 40], 17
+    n = sum(lens)
+    x = ref.inputs(1, n + extra, 2, 4, 64, 64, BF, gates, seed=14, device=DEV)
+    do = like(x[2])
+    for t in (*x, do):
+        t[:, n:] = float("nan")
+    cu = ref.packed(lens, DEV)
+    out = {k: torch.full_like(t, 7.0) for k, t in zip(KEYS, x)} | {"d_initial_state": None}
+    room = torch.full((1 << 22,), 255, dtype=torch.uint8, device=DEV)  # NaN whatever the type
+    got = kda.gdn_chunk_bwd(*x, do, None, None, cu, need_d_initial_state=False, out=out, workspace=room)
+    alone = kda.gdn_chunk_bwd(*[t[:, :n].contiguous() for t in x], do[:, :n].contiguous(), None, None, cu)
+    for key in KEYS[:5]:
+        assert torch.equal(got[key][:, :n], alone[key]), key
+        assert (got[key][:, n:] == 7).all(), key
