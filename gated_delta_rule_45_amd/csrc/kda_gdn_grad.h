@@ -156,7 +156,7 @@ struct GradLds {
     static constexpr int RB = DK * E, ZRB = DV * E, MRB = C * E;
     static constexpr int KB = C * RB, SB = DV * RB, ZB = C * ZRB, MB = C * MRB;
     static constexpr int B0 = 2 * KB, BB = SB > ZB + 2 * MB ? SB : ZB + 2 * MB;
-    static constexpr int G0 = B0 + BB;                     // up, down, beta, hi, lo [C]; 12 block factors
+    static constexpr int G0 = B0 + BB;                     // up, down, beta, hi, lo [C]; 12 block factors, resets
     static constexpr int T0 = G0 + 5 * C * 4 + 64;         // column sums [RT][C]
     static constexpr int V0 = T0 + RT * C * 4;             // row terms and x, per channel half, and two diagonals [C]
     static constexpr int D0 = V0 + 6 * C * 4;              // <S, dS> per wave
@@ -256,7 +256,9 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
             w.tok0 = tok;
             w.len = clen;
             w.h = h;
-            const Gates gt = make_gates<C>(load_gate<C>(p, w, 0, lane), lane);
+            const RawGate raw = load_gate<C>(p, w, 0, lane);
+            const Gates gt = make_gates<C>(raw, lane);
+            const uint64_t resets = __ballot(raw.g <= kNoGate);
             if (lane < C) {
                 gate[lane] = gt.up;
                 gate[C + lane] = gt.down;
@@ -270,6 +272,7 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
                 if (lane == 0) {
 #pragma unroll
                     for (int i = 2; i < 6; ++i) fac[6 + i] = gt.f[i];
+                    *reinterpret_cast<uint64_t *>(fac + 12) = resets;
                 }
             }
         }
@@ -457,6 +460,8 @@ __global__ void __launch_bounds__((GradLds<BF, DK, DV>::NT), (BF ? 2 : 1)) gdn_g
                 const float o = __shfl_down(dG, off);
                 dG += lane + off < 64 ? o : 0.f;
             }
+            // at a gate that is as good as e^g = 0 the sum cancels: 0 rather than what is left of it (a NaN stays)
+            if (*reinterpret_cast<const uint64_t *>(fac + 12) >> lane & 1) dG *= 0.f;
             if (lane < clen) {
                 const int64_t at = (tok + lane) * p.Hv + h;
                 if (p.gate_bf16) {

@@ -615,6 +615,7 @@ __device__ __forceinline__ RawGate load_gate(const GdnParams &p, const Walk &w, 
 }
 // Cumulative gate of the chunk in fp64 (log2 units; a gate below -1e4 is as good as e^g = 0 and keeps the
 // differences finite; a NaN is below nothing and stays one).
+constexpr float kNoGate = -1e4f;
 __device__ __forceinline__ double lane_value(double x, int lane) {
     const long long b = __double_as_longlong(x);
     const unsigned lo = __builtin_amdgcn_readlane((int)b, lane), hi = __builtin_amdgcn_readlane((int)(b >> 32), lane);
@@ -632,7 +633,7 @@ struct GateScan {
 };
 __device__ __forceinline__ GateScan gate_scan(float g) {
     GateScan r;
-    double s = (double)(g < -1e4f ? -1e4f : g) * 1.4426950408889634;
+    double s = (double)(g < kNoGate ? kNoGate : g) * 1.4426950408889634;
     s += row_shr64<1>(s);
     s += row_shr64<2>(s);
     s += row_shr64<4>(s);

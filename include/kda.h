@@ -457,7 +457,7 @@ kda_status_t kda_gdn_chunk_fwd_workspace(const kda_gdn_problem_t *problem, size_
  *  d_final_state    [num_seqs, Hv, d_k, d_v] state dtype, or NULL for zero
  *  dq, dk           [tokens, Hk, d_k] io dtype, dense: summed over the value heads of a key head, in a fixed order
  *  dv               [tokens, Hv, d_v] io dtype, dense
- *  dg, dbeta        [tokens, Hv] gate dtype
+ *  dg, dbeta        [tokens, Hv] gate dtype; dg is 0 at a reset
  *  d_initial_state  [num_seqs, Hv, d_k, d_v] state dtype, or NULL to skip it
  *  workspace        kda_gdn_chunk_bwd_workspace() bytes, 256-byte aligned: the states entering the chunks and
  *                   the gradients of those leaving them (bf16 or fp32, the io dtype) and one value tensor; a

@@ -1,5 +1,5 @@
 """GPU tests of the scalar-gate delta rule at values and sizes that a program meets seldom: a NaN among the
-gates, betas near the smallest number, rows that no sequence owns."""
+gates, betas near the smallest number, rows that no sequence owns, resets."""
 import math
 
 import pytest
@@ -130,3 +130,21 @@ def test_rows_of_a_small_packed_batch_that_no_sequence_owns_are_left_alone(gates
     for key in KEYS[:5]:
         assert torch.equal(got[key][:, :n], alone[key]), key
         assert (got[key][:, n:] == 7).all(), key
+
+
+# -------------------------------------------------------------------------------- resets --
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("T", [60, 150])
+def test_gradients_at_resets(io, T):
+    """g = -inf forgets what came before: dg is 0 there, not what is left of sums that cancel."""
+    say(f"[{io}] T={T}")
+    x = ref.inputs(1, T, 2, 4, 128, 128, io, F32, seed=9, device=DEV)
+    at = [t for t in (0, 5, 31, 63, 64, 100) if t < T]
+    x[3][:, at] = -math.inf
+    s0, dsf, do = states(1, 4, 128, 128), states(1, 4, 128, 128, seed=8), like(x[2])
+    got, want = kda.gdn_chunk_bwd(*x, do, s0, dsf), ref.delta_rule_grads(*x, do, s0, dsf)
+    assert (want["dg"][:, at] == 0).all() and (want["d_initial_state"] == 0).all()
+    for key in KEYS[:5]:
+        close(key, got[key], want[key], 8e-3 if io == BF else 1.5e-5)
+    say("  dg at the resets:", float(got["dg"][:, at].abs().max()), "of", float(want["dg"].abs().max()))
+    assert (got["dg"][:, at] == 0).all() and (got["d_initial_state"] == 0).all()
