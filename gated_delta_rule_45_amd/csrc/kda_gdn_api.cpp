@@ -280,6 +280,25 @@ kda_status_t bwd_layout(const kda_gdn_problem_t *p, const Shape &s, bool packed,
     return KDA_OK;
 }
 
+// Workspace of a problem before it is known whether cu_seqlens will come with it: `need` of the plain batch and,
+// where num_seqs > 0 sequences may be packed in one row, the larger of both (without cu_seqlens num_seqs may hold anything).
+template <typename Need>
+kda_status_t workspace_of(const kda_gdn_problem_t *p, size_t *bytes, Need need) {
+    if (!bytes) return set_error(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    *bytes = 0;
+    Shape s;
+    size_t n = 0, packed = 0;
+    kda_status_t st = check_shape(p, false, s);
+    if (st == KDA_OK) st = need(s, false, n);
+    if (st != KDA_OK) return st;
+    if (p->batch == 1 && p->num_seqs > 0) {
+        Shape t;
+        if (check_shape(p, true, t) == KDA_OK && need(t, true, packed) == KDA_OK) n = std::max(n, packed);
+    }
+    *bytes = n;
+    return done(hipSuccess, "");
+}
+
 }  // namespace
 
 extern "C" {
@@ -326,27 +345,19 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
 }
 
 kda_status_t kda_gdn_chunk_fwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes) {
-    if (!bytes) return set_error(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    *bytes = 0;
-    Shape s;
-    const bool packed = problem && problem->num_seqs > 0;
-    kda_status_t st = check_shape(problem, packed, s);
-    if (st != KDA_OK) return st;
-    *bytes = split_of(problem, s, packed, current_cus(), false).bytes;
-    return done(hipSuccess, "");
+    return workspace_of(problem, bytes, [&](const Shape &s, bool packed, size_t &n) {
+        n = split_of(problem, s, packed, current_cus(), false).bytes;
+        return KDA_OK;
+    });
 }
 
 kda_status_t kda_gdn_chunk_bwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes) {
-    if (!bytes) return set_error(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    *bytes = 0;
-    Shape s;
-    const bool packed = problem && problem->num_seqs > 0;
-    kda_status_t st = check_shape(problem, packed, s);
-    BwdLayout b;
-    if (st == KDA_OK) st = bwd_layout(problem, s, packed, b);
-    if (st != KDA_OK) return st;
-    *bytes = b.bytes;
-    return done(hipSuccess, "");
+    return workspace_of(problem, bytes, [&](const Shape &s, bool packed, size_t &n) {
+        BwdLayout b;
+        const kda_status_t st = bwd_layout(problem, s, packed, b);
+        n = b.bytes;
+        return st;
+    });
 }
 
 kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,

@@ -445,7 +445,8 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
                                const int32_t *cu_seqlens_host, void *out, void *final_state, void *workspace,
                                size_t workspace_bytes, void *stream);
 
-/* Workspace bytes kda_gdn_chunk_fwd can use on the current device (a packed batch where problem->num_seqs > 0: 0). */
+/* Workspace bytes kda_gdn_chunk_fwd can use for the problem as a plain batch on the current device (a packed batch uses
+ * none); *bytes = 0 on error. */
 kda_status_t kda_gdn_chunk_fwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes);
 
 /*
@@ -472,7 +473,8 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
                                void *dk, void *dv, void *dg, void *dbeta, void *d_initial_state, void *workspace,
                                size_t workspace_bytes, void *stream);
 
-/* Workspace bytes kda_gdn_chunk_bwd needs on the current device (a packed batch where problem->num_seqs > 0); *bytes = 0 on error. */
+/* Workspace bytes kda_gdn_chunk_bwd needs for the problem on the current device, as a plain batch and, where batch is 1
+ * and num_seqs > 0, also as a packed one; *bytes = 0 on error. */
 kda_status_t kda_gdn_chunk_bwd_workspace(const kda_gdn_problem_t *problem, size_t *bytes);
 
 /*

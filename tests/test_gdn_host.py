@@ -1,0 +1,45 @@
+"""Host side of the scalar-gate delta rule without a GPU: sizes of workspaces."""
+import ctypes
+
+import pytest
+
+import gated_delta_rule_45_amd as kda
+from gated_delta_rule_45_amd.gdn import GdnProblem
+
+
+def prob(**kw):
+    base = dict(batch=1, seq_len=15, num_seqs=0, num_heads_k=2, num_heads_v=4, head_dim_k=64, head_dim_v=64,
+                io_dtype=kda.KDA_BF16, gate_dtype=kda.KDA_F32, state_dtype=kda.KDA_F32, scale=1.0, stride_q=0,
+                stride_k=0, stride_v=0)
+    base.update(kw)
+    return GdnProblem(**base)
+
+
+def size(query, p):
+    n = ctypes.c_size_t(7)
+    st = getattr(kda.library(), query)(ctypes.byref(p), ctypes.byref(n))
+    return st, n.value
+
+
+QUERIES = ["kda_gdn_chunk_fwd_workspace", "kda_gdn_chunk_bwd_workspace"]
+SHAPES = [dict(batch=3, seq_len=1000), dict(batch=2, seq_len=8192, num_heads_k=1, num_heads_v=2), dict(seq_len=8192),
+          dict(seq_len=8191, io_dtype=kda.KDA_F32), dict(seq_len=60), dict(batch=0), dict(seq_len=0)]
+
+
+@pytest.mark.parametrize("query", QUERIES)
+@pytest.mark.parametrize("kw", SHAPES)
+@pytest.mark.parametrize("num_seqs", [-1, 1, 2, 3, 17])
+def test_a_plain_batch_may_carry_any_num_seqs(query, kw, num_seqs):
+    """num_seqs is ignored without cu_seqlens, by the workspace queries too: what they say is enough for the plain batch."""
+    st, need = size(query, prob(**kw))
+    assert st == kda.KDA_OK
+    st, said = size(query, prob(**kw, num_seqs=num_seqs))
+    assert st == kda.KDA_OK and said >= need
+    if num_seqs < 1 or kw.get("batch", 1) != 1:  # cannot be a packed batch
+        assert said == need
+
+
+def test_a_packed_batch_has_room_for_its_chunks():
+    # 40 sequences of up to 8,192 tokens in all: a chunk slot more for each
+    st, need = size("kda_gdn_chunk_bwd_workspace", prob(seq_len=8192, num_seqs=40))
+    assert st == kda.KDA_OK and need >= 2 * (8192 // 64 + 40) * 4 * 64 * 64 * 2 + 8192 * 4 * 64 * 2
