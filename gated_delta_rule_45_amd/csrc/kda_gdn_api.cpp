@@ -72,7 +72,7 @@ kda_status_t check_shape(const kda_gdn_problem_t *p, bool packed, Shape &s) {
         if (*ld[i] < rows[i])
             return set_error(KDA_ERR_INVALID_ARGUMENT, "stride_%c %lld is smaller than a token's %lld elements", "qkv"[i],
                              (long long)*ld[i], (long long)rows[i]);
-        if (*ld[i] * s.io % 16 != 0)
+        if (*ld[i] % (16 / s.io) != 0)
             return set_error(KDA_ERR_INVALID_ARGUMENT, "stride_%c %lld is not a multiple of 16 bytes", "qkv"[i],
                              (long long)*ld[i]);
         if (s.tokens > 0 && *ld[i] > (1LL << 60) / s.tokens) return set_error(KDA_ERR_UNSUPPORTED, "tensor too large");
