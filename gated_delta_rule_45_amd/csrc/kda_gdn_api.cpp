@@ -1,6 +1,7 @@
 // Host side of the scalar-gate delta rule: argument checks, launch choices and the C ABI.  As for the other
-// entry points everything is checked before HIP is touched, so an invalid call returns a status
-// without launching anything (and works on machines without a GPU).
+// entry points the arguments are checked before HIP is touched, so an invalid call returns a status
+// without launching anything (and works on machines without a GPU).  Only the gradients' workspace is checked
+// after a look at the device, whose number of CUs its size goes by (256 where there is none).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -369,12 +370,9 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
         Shape s;
         kda_status_t st = check_shape(problem, cu_seqlens != nullptr, s);
         if (st != KDA_OK) return st;
-        BwdLayout b;
-        st = bwd_layout(problem, s, cu_seqlens != nullptr, b);
-        if (st != KDA_OK) return st;
         const int64_t gates = s.tokens * problem->num_heads_v * s.gate, qk = s.tokens * s.qk_row * s.io,
                       vo = s.tokens * s.v_row * s.io, states = s.states * s.state;
-        const Arg args[] = {
+        Arg args[] = {
             {"q", q, s.span(s.ldq, s.qk_row), 16, true, false},
             {"k", k, s.span(s.ldk, s.qk_row), 16, true, false},
             {"v", v, s.span(s.ldv, s.v_row), 16, true, false},
@@ -390,10 +388,15 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
             {"dg", dg, gates, (size_t)s.gate, true, true},
             {"dbeta", dbeta, gates, (size_t)s.gate, true, true},
             {"d_initial_state", d_initial_state, states, 16, false, true},
-            {"workspace", workspace, (int64_t)b.bytes, 256, false, true},
+            {"workspace", workspace, 0, 256, false, true},
         };
         st = check_args(args);
         if (st == KDA_OK) st = check_offsets(problem, s, cu_seqlens, cu_seqlens_host);
+        if (st != KDA_OK) return st;
+        BwdLayout b;  // asks for the device's CUs
+        st = bwd_layout(problem, s, cu_seqlens != nullptr, b);
+        args[15].bytes = (int64_t)b.bytes;
+        if (st == KDA_OK) st = check_args(args);
         if (st != KDA_OK) return st;
         if (b.bytes > 0 && (!workspace || workspace_bytes < b.bytes))
             return set_error(KDA_ERR_WORKSPACE, "kda_gdn_chunk_bwd needs a 256-byte aligned workspace of %zu bytes (got %zu at %p)",

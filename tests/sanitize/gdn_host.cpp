@@ -14,6 +14,13 @@
 
 #include "kda.h"
 
+// Takes the runtime's place: a refused call asks nothing of it.
+static int g_device_queries = 0;
+extern "C" int hipGetDevice(int *) {
+    ++g_device_queries;
+    return 1;
+}
+
 namespace {
 
 int g_failures = 0, g_checks = 0;
@@ -189,9 +196,12 @@ void fuzz(int n) {
         if (next_u64() & 1) a.s0 = dev(21);
         if (next_u64() & 1) a.ds0 = dev(22);
         if (next_u64() & 1) a.slots = nullptr;
+        const int queries = g_device_queries;
         EXPECT(fwd(p, a) != KDA_OK && bwd(p, a) != KDA_OK && decode(p, a) != KDA_OK);
+        EXPECT(g_device_queries == queries);
         EXPECT(std::strlen(kda_last_error()) > 0);
     }
+    EXPECT(n == 0 || g_device_queries > 0);  // by the workspace queries
     EXPECT(n < 1000 || accepted > n / 1000);  // the queries' arithmetic is reached
     std::printf("%d of %d problems accepted by the queries\n", accepted, n);
 }
