@@ -38,7 +38,10 @@ struct Shape {
     int64_t span(int64_t ld, int64_t row) const { return tokens > 0 ? ((tokens - 1) * ld + row) * io : 0; }
 };
 
-kda_status_t check_shape(const kda_gdn_problem_t *p, bool packed, Shape &s) {
+// Work-items of a launch (HIP's limit) and those that the scans and decode spend on 32 columns of a (sequence, head).
+constexpr int64_t kMostItems = 0xffffffffLL, kScanItems = 512, kDecodeItems = 64;
+
+kda_status_t check_shape(const kda_gdn_problem_t *p, bool packed, Shape &s, int64_t items = kScanItems) {
     if (!p) return set_error(KDA_ERR_INVALID_ARGUMENT, "problem is NULL");
     if (p->batch < 0 || p->seq_len < 0 || p->num_heads_k < 1 || p->num_heads_v < 1)
         return set_error(KDA_ERR_INVALID_ARGUMENT, "bad sizes: batch=%d seq_len=%d num_heads_k=%d num_heads_v=%d",
@@ -78,9 +81,9 @@ kda_status_t check_shape(const kda_gdn_problem_t *p, bool packed, Shape &s) {
                              (long long)*ld[i]);
         if (s.tokens > 0 && *ld[i] > (1LL << 60) / s.tokens) return set_error(KDA_ERR_UNSUPPORTED, "tensor too large");
     }
-    // workgroups, and elements of a chunk's states, stay in range
-    if ((int64_t)s.num_seqs * p->num_heads_v > 0x7fffffffLL / 4)
-        return set_error(KDA_ERR_UNSUPPORTED, "too many (sequence, head) pairs");
+    // (decode rounds up to workgroups of four waves)
+    if ((int64_t)s.num_seqs * p->num_heads_v > (kMostItems - 3 * kDecodeItems) / (items * (p->head_dim_v / 32)))
+        return set_error(KDA_ERR_UNSUPPORTED, "too many (sequence, head) pairs: %d x %d", s.num_seqs, p->num_heads_v);
     s.states = (int64_t)s.num_seqs * p->num_heads_v * p->head_dim_k * p->head_dim_v;
     return KDA_OK;
 }
@@ -262,7 +265,8 @@ kda_status_t bwd_layout(const kda_gdn_problem_t *p, const Shape &s, bool packed,
     const int64_t C = kda::gdn::chunk_of(wide ? KDA_F32 : p->io_dtype), per = (int64_t)p->seq_len / C;
     b.slots = packed ? per + s.num_seqs : (int64_t)s.num_seqs * (per + (p->seq_len % C != 0));
     const int64_t row = s.v_row * (wide ? 4 : s.io);
-    if (b.slots > 0x7fffffffLL / p->num_heads_k || b.slots > (1LL << 60) / (row * p->head_dim_k))
+    // a workgroup of the gradients (8 threads a token) per chunk and key head
+    if (b.slots > kMostItems / (8 * C * p->num_heads_k) || b.slots > (1LL << 60) / (row * p->head_dim_k))
         return set_error(KDA_ERR_UNSUPPORTED, "too many chunks");
     auto align = [](int64_t x) { return (size_t)((x + 255) / 256 * 256); };
     b.dhs = align(b.slots * row * p->head_dim_k);
@@ -481,7 +485,7 @@ kda_status_t kda_gdn_decode(const kda_gdn_problem_t *problem, const void *q, con
                             void *out, void *stream) {
     try {
         Shape s;
-        kda_status_t st = check_shape(problem, cu_seqlens != nullptr, s);
+        kda_status_t st = check_shape(problem, cu_seqlens != nullptr, s, kDecodeItems);
         if (st != KDA_OK) return st;
         if (num_slots < 0 || num_slots > 0x7fffffffLL)
             return set_error(KDA_ERR_INVALID_ARGUMENT, "num_slots %lld out of range", (long long)num_slots);

@@ -43,3 +43,25 @@ def test_a_packed_batch_has_room_for_its_chunks():
     # 40 sequences of up to 8,192 tokens in all: a chunk slot more for each
     st, need = size("kda_gdn_chunk_bwd_workspace", prob(seq_len=8192, num_seqs=40))
     assert st == kda.KDA_OK and need >= 2 * (8192 // 64 + 40) * 4 * 64 * 64 * 2 + 8192 * 4 * 64 * 2
+
+
+NULL = [None] * 12
+
+
+def test_launches_stay_in_range():
+    """A launch has at most 2^32 - 1 work-items: more (sequence, head, columns) than that are refused by name."""
+    lib = kda.library()
+    fwd = lambda p: lib.kda_gdn_chunk_fwd(ctypes.byref(p), *NULL[:11], 0, None)  # noqa: E731
+    bwd = lambda p: lib.kda_gdn_chunk_bwd(ctypes.byref(p), *NULL, *NULL[:5], 0, None)  # noqa: E731
+    decode = lambda p: lib.kda_gdn_decode(ctypes.byref(p), *NULL[:6], 1 << 30, *NULL[:6])  # noqa: E731
+    # a workgroup of 512 for 32 columns of a head
+    kw = dict(seq_len=1, num_heads_k=8, num_heads_v=32, head_dim_v=128)
+    for call in (fwd, bwd):
+        assert call(prob(batch=65535, **kw)) == kda.KDA_ERR_INVALID_ARGUMENT  # these pointers are missing
+        assert b"is NULL" in lib.kda_last_error()
+        assert call(prob(batch=65536, **kw)) == kda.KDA_ERR_UNSUPPORTED
+    for query in QUERIES:
+        assert size(query, prob(batch=65536, **kw)) == (kda.KDA_ERR_UNSUPPORTED, 0)
+    # a wave of 64
+    assert decode(prob(batch=65536, **kw)) == kda.KDA_ERR_INVALID_ARGUMENT and b"is NULL" in lib.kda_last_error()
+    assert decode(prob(batch=8 * 65536, **kw)) == kda.KDA_ERR_UNSUPPORTED
