@@ -192,7 +192,7 @@ def gdn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     return out, final_state
 
 
-_SPLIT_TOKENS = 256  # shorter sequences are not split
+_SPLIT_TOKENS = 225  # the library splits no shorter sequence: a small call is spared the question
 
 
 def _fwd_workspace(p: GdnProblem) -> int:

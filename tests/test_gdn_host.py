@@ -1,9 +1,10 @@
-"""Host side of the scalar-gate delta rule without a GPU: sizes of workspaces."""
+"""Host side of the scalar-gate delta rule without a GPU: sizes of workspaces, ranges of launches."""
 import ctypes
 
 import pytest
 
 import gated_delta_rule_45_amd as kda
+from gated_delta_rule_45_amd import gdn
 from gated_delta_rule_45_amd.gdn import GdnProblem
 
 
@@ -65,3 +66,20 @@ def test_launches_stay_in_range():
     # a wave of 64
     assert decode(prob(batch=65536, **kw)) == kda.KDA_ERR_INVALID_ARGUMENT and b"is NULL" in lib.kda_last_error()
     assert decode(prob(batch=8 * 65536, **kw)) == kda.KDA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("io", [kda.KDA_BF16, kda.KDA_F32])
+def test_the_binding_asks_for_a_workspace_wherever_the_library_uses_one(io):
+    """Below the binding's least length the library splits nothing, whatever the heads."""
+    least = []
+    for batch, heads, dk, dv in ((1, 1, 64, 64), (1, 2, 128, 64), (2, 2, 64, 128), (1, 8, 128, 128), (1, 32, 64, 64)):
+        for T in range(1, 300):
+            st, need = size("kda_gdn_chunk_fwd_workspace",
+                            prob(batch=batch, seq_len=T, num_heads_k=1, num_heads_v=heads, head_dim_k=dk, head_dim_v=dv, io_dtype=io))
+            assert st == kda.KDA_OK
+            if need:
+                least.append(T)
+                break
+    assert all(T >= gdn._SPLIT_TOKENS for T in least)
+    if io == kda.KDA_F32:
+        assert min(least) == gdn._SPLIT_TOKENS

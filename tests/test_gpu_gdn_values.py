@@ -148,3 +148,18 @@ def test_gradients_at_resets(io, T):
         close(key, got[key], want[key], 8e-3 if io == BF else 1.5e-5)
     say("  dg at the resets:", float(got["dg"][:, at].abs().max()), "of", float(want["dg"].abs().max()))
     assert (got["dg"][:, at] == 0).all() and (got["d_initial_state"] == 0).all()
+
+
+# ------------------------------------------------------------------------ the shortest split walk --
+@pytest.mark.parametrize("T,split", [(224, False), (225, True), (255, True)])
+def test_the_binding_gives_room_to_every_split(T, split):
+    x = ref.inputs(1, T, 1, 2, 64, 64, F32, seed=T, device=DEV)
+    s0 = states(1, 2, 64, 64)
+    room = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    a, b = kda.gdn_chunk_fwd(*x, s0), kda.gdn_chunk_fwd(*x, s0, workspace=room)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    o, f = ref.delta_rule(*x, s0)
+    close("out", a[0], o, 1.5e-5)
+    close("final", a[1], f, 1.5e-5)
+    one = kda.gdn_chunk_fwd(*x, s0, workspace=room[:0])
+    assert torch.equal(one[0], a[0]) != split  # two ways of summing
