@@ -345,7 +345,7 @@ kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, 
         }
         return done(launch_scan(problem, 0, r, hs), "kda_gdn_chunk_fwd launch");
     } catch (...) {
-        return KDA_ERR_HIP;
+        return set_error(KDA_ERR_HIP, "unexpected exception in argument checks");
     }
 }
 
@@ -475,7 +475,7 @@ kda_status_t kda_gdn_chunk_bwd(const kda_gdn_problem_t *problem, const void *q, 
         if (st != KDA_OK || back.n == 0) return st;
         return done(kda::gdn::launch_convert(false, back, hs), "kda_gdn_chunk_bwd narrowing launch");
     } catch (...) {
-        return KDA_ERR_HIP;
+        return set_error(KDA_ERR_HIP, "unexpected exception in argument checks");
     }
 }
 
@@ -552,7 +552,7 @@ kda_status_t kda_gdn_decode(const kda_gdn_problem_t *problem, const void *q, con
         return done(kda::gdn::launch_decode(problem->io_dtype == KDA_BF16, r, static_cast<hipStream_t>(stream)),
                     "kda_gdn_decode launch");
     } catch (...) {
-        return KDA_ERR_HIP;
+        return set_error(KDA_ERR_HIP, "unexpected exception in argument checks");
     }
 }
 
@@ -594,7 +594,7 @@ kda_status_t kda_norm_gate_bwd(int64_t rows, int32_t d, int32_t io_dtype, float 
                                               static_cast<hipStream_t>(stream)),
                     "kda_norm_gate_bwd launch");
     } catch (...) {
-        return KDA_ERR_HIP;
+        return set_error(KDA_ERR_HIP, "unexpected exception in argument checks");
     }
 }
 

@@ -10,6 +10,7 @@
 #include <cstring>
 #include <limits>
 #include <memory>
+#include <new>
 #include <vector>
 
 #include "kda.h"
@@ -20,6 +21,15 @@ extern "C" int hipGetDevice(int *) {
     ++g_device_queries;
     return 1;
 }
+
+static bool g_no_memory = false;
+void *operator new(size_t n) {
+    void *p = g_no_memory ? nullptr : std::malloc(n);
+    if (!p) throw std::bad_alloc();
+    return p;
+}
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, size_t) noexcept { std::free(p); }
 
 namespace {
 
@@ -132,6 +142,20 @@ void host_arrays() {
     }
 }
 
+void out_of_memory() {
+    kda_gdn_problem_t p = problem();
+    Args a;
+    const auto at = host({5, 7});
+    a.slots_host = at.get();
+    a.q = dev(0, 8);
+    EXPECT(decode(p, a) == KDA_ERR_INVALID_ARGUMENT && std::strstr(kda_last_error(), "aligned"));
+    a.q = dev(0);
+    g_no_memory = true;  // for the list of the slots: what is thrown stays inside, and the message is this call's
+    const kda_status_t st = decode(p, a);
+    g_no_memory = false;
+    EXPECT(st == KDA_ERR_HIP && !std::strstr(kda_last_error(), "aligned") && std::strlen(kda_last_error()) > 0);
+}
+
 void empty() {
     for (int i = 0; i < 2; ++i) {
         kda_gdn_problem_t p = problem();
@@ -211,6 +235,7 @@ void fuzz(int n) {
 int main(int argc, char **argv) {
     refusals();
     host_arrays();
+    out_of_memory();
     empty();
     norm();
     fuzz(argc > 1 ? std::atoi(argv[1]) : 1000);
