@@ -172,10 +172,11 @@ hipError_t launch_scan(const kda_gdn_problem_t *p, int mode, const kda::gdn::Gdn
     return p->io_dtype == KDA_BF16 ? kda::gdn::launch_scan_bf16(mode, r, s) : kda::gdn::launch_scan_f32(mode, r, s);
 }
 
-// Whether the gradients of a bf16 call are computed on fp32 operands.  With few gates' gradients the
-// roundings of the products' operands do not average out (260 values: the norm of the error of dg up
-// to 5.7e-3 of dg's, 3e-3 for thousands of values and about 1e-6 on fp32 operands).  It costs 123 against
-// about 50 us at 256 tokens of one head.
+// Whether the gradients of a bf16 call are computed on fp32 operands.  Every value has the same error whatever the
+// call's size, but over few values the roundings of the products' operands do not average out in the norm (260
+// gates: error of dg up to 5.7e-3 of its norm, 3e-3 for thousands of them, about 4e-7 on fp32 operands).  The
+// price grows with every chunk of the walk, hence the limit of tokens beside that of gates: d = 128, 256 tokens
+// of one head 118 us, 257 on bf16 operands 47; 128 tokens of 4 heads 81, 129 39.
 bool bwd_wide(const kda_gdn_problem_t *p, const Shape &s) {
     return p->io_dtype == KDA_BF16 && s.tokens <= 256 && s.tokens * p->num_heads_v <= 512;
 }
@@ -183,15 +184,19 @@ bool bwd_wide(const kda_gdn_problem_t *p, const Shape &s) {
 // Segments of walks that are split over their length: with few (sequence, head) chains most CUs idle while
 // each chain's chunks follow one another.  The maps of all segments but the last run side by side
 // (d_v + d_k columns), the join walks the segments, and the forward runs on all of them at once.  The
-// number of segments is the one with the least time by the model below (us, measured: a chunk of the
-// forward and of the maps, each per round of workgroups over the CUs; a segment of the join; the fixed
-// part of the two further launches), and the split is taken where that is a tenth less than one walk.
+// number of segments is the one with the least time by the model below (us: a chunk of the forward and of
+// the maps, each per round of workgroups over the CUs; a segment of the join; the fixed part of the two
+// further launches), and the split is taken where that is a tenth less than one walk.  Its constants were measured
+// at 128 x 128 with few workgroups.  With one on every CU, as the split may have, a chunk takes a fifth more (2.6
+// us forward, 2.0 maps), and at 64 x 64 less (forward 1.8 bf16, 3.4 fp32), so that the choice is not the best one
+// everywhere, but it was at no loss for 1 to 32 heads of 64 and 128 around the shortest lengths that are split.
 // The gradients split the keeping forward in the same way, and the reverse scan: a segment takes the
 // gradient of the state that leaves it to M^T dS + H', H' by one more reverse scan from zero.
-// 8 heads of 128 x 128, bf16: one walk against the split 74 / 66 us at 2,048 tokens, 272 / 134 at 8,192,
-// 1,068 / 408 at 32,768; at 1,024 tokens 41 / 45, at 32 heads and 8,192 tokens 270 / 376: one walk.
-// Gradients, the same heads: 241 / 203 at 2,048 tokens, 644 / 329 at 8,192; at 1,024 171 / 179: one walk; fp32
-// 790 / 417 at 2,048.  Packed batches, whose lengths the host does not know, are not split.
+// 8 heads of 128 x 128, bf16: one walk against the split 73 / 62 us at 2,048 tokens, 272 / 131 at 8,192,
+// 1,070 / 408 at 32,768; at 1,024 tokens 41 / 45, at 32 heads and 8,192 tokens 270 / 376: one walk.
+// Gradients, the same heads: 172 / 130 at 2,048 tokens, 646 / 303 at 8,192; at 1,024 97: one walk; fp32 684 / 308
+// at 2,048.  Packed batches are not split, for which their segments would have to be listed (one prompt of 65,536
+// tokens x 8 heads: 2,440 us packed, 866 as a plain batch of one).
 struct Split {
     int32_t segs = 0, seg_len = 0;
     size_t h = 0, bytes = 0;  // offset of M, size

@@ -35,10 +35,14 @@
 // Roundings to bf16 (bf16 io only; fp32 io runs the same code on fp32 operands and 32-token chunks): the
 // operands of the products that are not inputs (S, X, Z, Y, the strictly lower part of the inverse,
 // M B and P).  The forward takes P and Y as two bf16 terms in P Y, a product of waves that have the time:
-// error of the output 1.8e-3 of its norm, 1.7e-3 of it the output's own rounding, where one term
-// gives 2.9e-3, in the same time.  X, Z and K^T Y with two terms as well would cost the chain 0.3 us a
-// chunk for what is then 1.7e-3.  The unit diagonal of the inverse is applied in fp32, sums and the state
+// error of the output 1.8e-3 of its norm with ordinary decays, 1.7e-3 of it the output's own rounding, where one
+// term gives 2.9e-3, in the same time; up to 2.6e-3 with long memories, whose state is rounded as an operand
+// in every chunk.  X, Z and K^T Y with two terms as well would cost the chain 0.3 us a chunk for what is then
+// 1.7e-3 with ordinary decays.  The unit diagonal of the inverse is applied in fp32, sums and the state
 // are fp32, cumulative gates fp64 (their differences stay exact behind a strong gate).
+//
+// Registers: every mode at d_k = 128 is near the 256 that eight waves leave a lane (bf16 forward 252, reverse 251),
+// and two are over: the keeping forward in bf16 and the reverse walk in fp32 keep 12 bytes a lane in scratch.
 #pragma once
 
 #include <type_traits>

@@ -164,8 +164,8 @@ def gdn_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Te
     (fp32 or bf16); initial_state: [N, Hv, d_k, d_v] (fp32 or bf16) or None; cu_seqlens: int32 [N+1]
     (B == 1) or None.  The states' dtype is that of the state given, else state_dtype, else fp32;
     final_state may be initial_state.  workspace: uint8, as long as kda_gdn_chunk_fwd_workspace says, for long
-    sequences on few heads (allocated here when None and needed; an empty tensor: do without).  Returns
-    (out, final_state)."""
+    sequences on few heads (allocated here when None and needed; an empty tensor: do without), of which a packed
+    batch makes no use.  Returns (out, final_state)."""
     given = initial_state if initial_state is not None else final_state
     sdt = given.dtype if given is not None else state_dtype or torch.float32
     p, n = _problem(q, k, v, g, beta, cu_seqlens, sdt, scale)

@@ -437,8 +437,8 @@ typedef struct {
  * Nothing is allocated: the call can be captured, and run on several streams at once with a workspace each.
  * A NaN or infinity reaches the results of its own sequence only, from the start of its chunk (64 tokens in
  * bf16, 32 in fp32) on.
- * bf16 io: products take bf16 operands and accumulate in fp32.  Any other overlap of an output with an
- * argument is refused.  Errors as for kda_chunk_fwd.
+ * bf16 io: products take bf16 operands and accumulate in fp32.  A packed batch is not split: one long prompt is
+ * faster as a plain batch of one.  Any other overlap of an output with an argument is refused.  Errors as for kda_chunk_fwd.
  */
 kda_status_t kda_gdn_chunk_fwd(const kda_gdn_problem_t *problem, const void *q, const void *k, const void *v,
                                const void *g, const void *beta, const void *initial_state, const int32_t *cu_seqlens,
@@ -464,6 +464,8 @@ kda_status_t kda_gdn_chunk_fwd_workspace(const kda_gdn_problem_t *problem, size_
  *                   the gradients of those leaving them (bf16 or fp32, the io dtype) and one value tensor; a
  *                   plain batch of few sequences and heads is split over its length as in the forward, and
  *                   the segments' maps are here too
+ * bf16 io: calls of at most 256 tokens and 512 (token, value head) pairs are computed on fp32 operands, larger ones
+ * on bf16 operands as the forward is: the same sequence may come out with other roundings in a larger call.
  * No output may overlap anything else.  beta of 0, or near it, has its gradients like any other.  The results repeat
  * bit for bit.  Calls that overlap in time need a workspace each.  Errors as for kda_chunk_bwd.
  */
