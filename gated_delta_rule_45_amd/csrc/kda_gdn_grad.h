@@ -29,9 +29,9 @@
 //
 // Measured, 4 x 4,096 tokens x 16 heads, d = 128, bf16: 245 us, 0.76 GB of HBM traffic, so 3.1 TB/s, the waves
 // waiting 61 % of their time and the matrix units busy 8 %: bound by the latency of a workgroup's chain of
-// loads, products and barriers (16 us), with one workgroup of 8 waves per CU at 256 registers.  Four waves with all channels each spilled (356 us); two workgroups per CU at 128
-// registers spill too (430 to 570 us); dO and dX loaded twice instead of kept 277 us; dS and Z loaded
-// ahead at the start 255 us.
+// loads, products and barriers (16 us), with one workgroup of 8 waves per CU at 256 registers.  Four waves with
+// all channels each spilled (356 us); two workgroups per CU at 128 registers spill too (430 to 570 us); dO and
+// dX loaded twice instead of kept 277 us; dS and Z loaded ahead at the start 255 us.
 #pragma once
 
 #include "kda_gdn_scan.h"
