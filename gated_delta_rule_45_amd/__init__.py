@@ -16,6 +16,8 @@ Entry points (same names as the C ABI):
 * ``gdn_chunk_fwd``, ``gdn_chunk_bwd``, ``gdn_decode`` -- the delta rule with one log-gate per head and
                        grouped heads: prefill, gradients, and new tokens on a pool of state slots (``gdn.py``)
 * ``norm_gate_bwd`` -- gradients of the output epilogue
+* ``rope``, ``rope_bwd``, ``rope_frequencies``, ``paged_append``, ``paged_attention`` -- a hybrid's full-attention
+                       layers: rotary positions, the paged key-value cache, and attention of new tokens over it (``paged.py``)
 """
 from __future__ import annotations
 
@@ -26,7 +28,8 @@ from typing import Optional, Tuple
 import torch
 
 __all__ = ["chunk_fwd", "chunk_fwd_prologue", "chunk_fwd_noalloc", "noalloc_scratch_bytes", "chunk_bwd", "dplr_chunk_fwd", "recurrent_fwd", "decode_step", "decode_step_gated", "prologue", "norm_gate", "query", "tune", "KdaError",
-           "LIB_PATH", "library", "gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode", "norm_gate_bwd"]
+           "LIB_PATH", "library", "gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode", "norm_gate_bwd", "rope",
+           "rope_bwd", "rope_frequencies", "paged_append", "paged_attention"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libkda.so")
 
@@ -117,6 +120,7 @@ def library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_last_error.argtypes = []
     gdn.declare(lib)
+    paged.declare(lib)
     _lib = lib
     return lib
 
@@ -644,3 +648,5 @@ def query(batch: int, seq_len: int, num_heads: int, head_dim_k: int, head_dim_v:
 
 from . import gdn  # noqa: E402  (it uses the helpers above)
 from .gdn import gdn_chunk_bwd, gdn_chunk_fwd, gdn_decode, norm_gate_bwd  # noqa: E402
+from . import paged  # noqa: E402
+from .paged import paged_append, paged_attention, rope, rope_bwd, rope_frequencies  # noqa: E402

@@ -11,22 +11,14 @@
 #include <vector>
 
 #include "kda.h"
+#include "kda_args.h"
 #include "kda_gdn.h"
 #include "kda_internal.h"
 
 namespace {
 
+using namespace kda::args;
 using kda::set_error;
-
-bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-bool dtype_ok(int32_t t) { return t == KDA_F32 || t == KDA_BF16; }
-int64_t bytes_of(int32_t t) { return t == KDA_BF16 ? 2 : 4; }
-
-kda_status_t done(hipError_t e, const char *what) {
-    if (e != hipSuccess) return set_error(KDA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-    set_error(KDA_OK, "%s", "");
-    return KDA_OK;
-}
 
 // A problem that has passed the checks, with its sizes worked out.
 struct Shape {
@@ -38,8 +30,8 @@ struct Shape {
     int64_t span(int64_t ld, int64_t row) const { return tokens > 0 ? ((tokens - 1) * ld + row) * io : 0; }
 };
 
-// Work-items of a launch (HIP's limit) and those that the scans and decode spend on 32 columns of a (sequence, head).
-constexpr int64_t kMostItems = 0xffffffffLL, kScanItems = 512, kDecodeItems = 64;
+// Work-items that the scans and decode spend on 32 columns of a (sequence, head).
+constexpr int64_t kScanItems = 512, kDecodeItems = 64;
 
 kda_status_t check_shape(const kda_gdn_problem_t *p, bool packed, Shape &s, int64_t items = kScanItems) {
     if (!p) return set_error(KDA_ERR_INVALID_ARGUMENT, "problem is NULL");
@@ -88,60 +80,8 @@ kda_status_t check_shape(const kda_gdn_problem_t *p, bool packed, Shape &s, int6
     return KDA_OK;
 }
 
-// One tensor argument of a call.
-struct Arg {
-    const char *name;
-    const void *p;
-    int64_t bytes;
-    size_t align;
-    bool needed, written;
-};
-
-// Pointers: given, aligned, and no written range meets another one (`twin`: the pair of arguments
-// that may be the same buffer).
-template <int N>
-kda_status_t check_args(const Arg (&a)[N], int twin0 = -1, int twin1 = -1) {
-    for (const Arg &x : a) {
-        if (!x.p && x.needed && x.bytes > 0) return set_error(KDA_ERR_INVALID_ARGUMENT, "%s is NULL", x.name);
-        if (x.p && !aligned(x.p, x.align))
-            return set_error(KDA_ERR_INVALID_ARGUMENT, "%s is not %zu-byte aligned", x.name, x.align);
-    }
-    for (int i = 0; i < N; ++i) {
-        if (!a[i].written || !a[i].p || a[i].bytes <= 0) continue;
-        const uintptr_t b = reinterpret_cast<uintptr_t>(a[i].p), e = b + (uintptr_t)a[i].bytes;
-        for (int j = 0; j < N; ++j) {
-            if (j == i || !a[j].p || a[j].bytes <= 0) continue;
-            const uintptr_t c = reinterpret_cast<uintptr_t>(a[j].p), f = c + (uintptr_t)a[j].bytes;
-            if (b == c && ((i == twin0 && j == twin1) || (i == twin1 && j == twin0))) continue;
-            if (b < f && c < e) return set_error(KDA_ERR_INVALID_ARGUMENT, "%s aliases %s", a[i].name, a[j].name);
-        }
-    }
-    return KDA_OK;
-}
-
 kda_status_t check_offsets(const kda_gdn_problem_t *p, const Shape &s, const int32_t *cu, const int32_t *host) {
-    if (!cu) {
-        if (host) return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens_host given without cu_seqlens");
-        return KDA_OK;
-    }
-    if (!aligned(cu, 4)) return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens is not 4-byte aligned");
-    if (!host) return KDA_OK;
-    if (host[0] != 0) return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens[0] = %d, expected 0", host[0]);
-    for (int32_t i = 0; i < s.num_seqs; ++i)
-        if (host[i + 1] < host[i])
-            return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens decreases at %d (%d -> %d)", i, host[i], host[i + 1]);
-    if (host[s.num_seqs] != p->seq_len)
-        return set_error(KDA_ERR_INVALID_ARGUMENT, "cu_seqlens[%d] = %d, expected seq_len %d", s.num_seqs,
-                         host[s.num_seqs], p->seq_len);
-    return KDA_OK;
-}
-
-int current_cus() {
-    int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0)
-        return 256;
-    return n;
+    return kda::args::check_offsets(p->seq_len, s.num_seqs, cu, host);
 }
 
 kda::gdn::GdnParams params_of(const kda_gdn_problem_t *p, const Shape &s, const void *q, const void *k, const void *v,

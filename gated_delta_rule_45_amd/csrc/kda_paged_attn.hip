@@ -1,0 +1,394 @@
+// Attention of a few rows over a paged cache: single and drafted tokens of bf16 calls, all fp32 calls; and the kernel
+// that joins the parts of long rows of cells.
+//
+// One pass over the cells with a running maximum m and sum l per row:  p_j = 2^(s_j - m),  o = sum p_j v_j / l.
+//
+// A tile is 16 rows (tokens x heads that share a key head), the width of the matrix instruction.  Four waves take the
+// 32-cell quarters of each 128-cell block by themselves and are added at the end, so nothing is staged in LDS and
+// the loop has no barrier: with few rows each cell is used once per wave, and the kernel is bound by the cache's bytes.
+//
+// Layouts (lane = 16 g + c).  S^T = K Q^T leaves lane (g, c) the scores of row c for cells 4 g + j of each 16: a lane holds
+// 8 cells of one row, the contraction slots of the next product (which may come in any order), so P feeds O^T = V^T P^T
+// from the registers it was computed in, statistics are per lane (cells meet across g twice a block, for m only), and
+// the rescaling factor of a row belongs to the lane that holds the row's sums.  V^T needs 8 cells of one column in a
+// lane: a lane loads d_v / 16 columns of its 8 cells (a cell's row is one run over 16 lanes) and pairs them up with
+// byte permutes, one per two values.
+#include "kda_paged_work.h"
+
+namespace kda {
+namespace paged {
+namespace {
+
+constexpr int kM = 16, kKB = 128;
+
+__device__ __forceinline__ float max_groups(float x) {  // over the lanes that differ in g
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// mfma_settle for all of a wave's sums: one wait, and every sum passes behind it.
+template <int N>
+__device__ __forceinline__ void settle(f32x4 (&o)[N]) {
+    mfma_settle(o[0]);
+#pragma unroll
+    for (int i = 1; i < N; ++i) asm volatile("" : "+v"(o[i]));
+}
+
+// The keys, queries and values of a wave in either type.
+template <typename IO, int DK, int DV>
+struct Ops;
+
+template <int DK, int DV>
+struct Ops<uint16_t, DK, DV> {
+    static constexpr int KK = DK / 32, VW = DV / 16;
+    using Row = __attribute__((ext_vector_type(VW / 2))) unsigned;
+    u32x4 q[KK], k[2][KK];
+    Row v[8];
+    __device__ __forceinline__ void load_q(const uint16_t *row, int g, bool live, bool flip) {
+#pragma unroll
+        for (int i = 0; i < KK; ++i) {
+            q[i] = live ? *reinterpret_cast<const u32x4 *>(row + 32 * i + 8 * g) : u32x4{0, 0, 0, 0};
+            if (flip) q[i] ^= 0x80008000u;
+        }
+    }
+    __device__ __forceinline__ void load_k(int s, const uint16_t *row, int g) {
+#pragma unroll
+        for (int i = 0; i < KK; ++i) k[s][i] = *reinterpret_cast<const u32x4 *>(row + 32 * i + 8 * g);
+    }
+    __device__ __forceinline__ void load_v(int j, const uint16_t *row, int c) {
+        v[j] = *reinterpret_cast<const Row *>(row + VW * c);
+    }
+    __device__ __forceinline__ void clear_v(int j) { v[j] = Row(0u); }
+    __device__ __forceinline__ bool odd_v(int j) const {  // infinities or NaN among them
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < VW / 2; ++i)
+            bad |= (v[j][i] & 0x7f80u) == 0x7f80u || (v[j][i] & 0x7f800000u) == 0x7f800000u;
+        return bad;
+    }
+    __device__ __forceinline__ f32x4 scores(int s) const {
+        f32x4 a = zero4();
+#pragma unroll
+        for (int i = 0; i < KK; ++i)
+            a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[s][i]), __builtin_bit_cast(bf16x8, q[i]), a,
+                                                        0, 0, 0);
+        return a;
+    }
+    __device__ __forceinline__ void add(f32x4 (&o)[VW], const float (&p)[8]) const {
+        const u32x4 pp = {pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7])};
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            u32x4 a;
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+                a[d] = __builtin_amdgcn_perm(v[2 * d + 1][i / 2], v[2 * d][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, pp), o[i], 0,
+                                                           0, 0);
+        }
+    }
+};
+
+template <int DK, int DV>
+struct Ops<float, DK, DV> {
+    static constexpr int KK = DK / 16, VW = DV / 16;
+    f32x4 q[KK], k[2][KK], v[8][VW / 4];
+    __device__ __forceinline__ void load_q(const float *row, int g, bool live, bool flip) {
+#pragma unroll
+        for (int i = 0; i < KK; ++i) {
+            q[i] = live ? *reinterpret_cast<const f32x4 *>(row + 16 * i + 4 * g) : zero4();
+            if (flip) q[i] = -q[i];
+        }
+    }
+    __device__ __forceinline__ void load_k(int s, const float *row, int g) {
+#pragma unroll
+        for (int i = 0; i < KK; ++i) k[s][i] = *reinterpret_cast<const f32x4 *>(row + 16 * i + 4 * g);
+    }
+    __device__ __forceinline__ void load_v(int j, const float *row, int c) {
+#pragma unroll
+        for (int i = 0; i < VW / 4; ++i) v[j][i] = *reinterpret_cast<const f32x4 *>(row + VW * c + 4 * i);
+    }
+    __device__ __forceinline__ void clear_v(int j) {
+#pragma unroll
+        for (int i = 0; i < VW / 4; ++i) v[j][i] = zero4();
+    }
+    __device__ __forceinline__ bool odd_v(int j) const {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < VW; ++i) bad |= (__float_as_uint(v[j][i / 4][i % 4]) & 0x7f800000u) == 0x7f800000u;
+        return bad;
+    }
+    __device__ __forceinline__ f32x4 scores(int s) const {
+        f32x4 a = zero4();
+#pragma unroll
+        for (int i = 0; i < KK; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a = __builtin_amdgcn_mfma_f32_16x16x4f32(k[s][i][e], q[i][e], a, 0, 0, 0);
+        return a;
+    }
+    __device__ __forceinline__ void add(f32x4 (&o)[VW], const float (&p)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) o[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[j][i / 4][i % 4], p[j], o[i], 0, 0, 0);
+    }
+};
+
+// A wave's walk over its 16-cell groups: pages are looked up 64 groups at a time, a lane each, so that the loads of
+// keys and values do not wait for a table entry each.
+struct Pages {
+    int entry;  // of group `lane` from the last refill on; -1: no page
+    __device__ __forceinline__ void refill(const Cache &c, int n, int b, int wave, int lane, int hi, int b1) {
+        const int bb = b + (lane >> 1), cell = bb * kKB + 32 * wave + 16 * (lane & 1);
+        entry = -1;
+        if (bb < b1 && cell < hi) {
+            entry = c.table[n * c.table_ld + (cell >> c.page_shift)];
+            if (entry >= c.num_pages) entry = -1;
+        }
+    }
+    __device__ __forceinline__ int get(int i) const { return __builtin_amdgcn_readlane(entry, i & 63); }
+};
+
+template <typename IO, int DK, int DV>
+__global__ void __launch_bounds__(256) attn_rows_kernel(AttnParams p) {
+    constexpr int VW = DV / 16, PAD = DV + 4;
+    __shared__ union {
+        PlanLds plan;
+        struct {
+            float o[4][kM][PAD], m[4][kM], l[4][kM];
+        } sum;
+    } lds;
+    Work w;
+    if (!find_work(p, kM, kKB, w, lds.plan)) return;
+    const Cache &c = p.c;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4,
+              col = lane & 15;
+
+    Ops<IO, DK, DV> x;
+    const int row = w.row0 + min(col, w.rows - 1);  // this lane's row
+    x.load_q(static_cast<const IO *>(p.q) + (w.seq.t0 + row / p.G) * p.ldq + (w.head * p.G + row % p.G) * DK, g, col < w.rows,
+             p.flip);
+    const int pos = w.pos(row, p.G), from = w.first(pos, p.window);
+    // cells that every row of the tile sees
+    const int all_lo = w.first(w.pos(w.row0 + w.rows - 1, p.G), p.window), all_hi = min(w.pos(w.row0, p.G) + 1, w.cells);
+    const bool ragged = all_lo != w.lo || all_hi != w.hi;  // rows see different cells
+    const IO *kp = static_cast<const IO *>(c.k) + w.head * c.k_head, *vp = static_cast<const IO *>(c.v) + w.head * c.v_head;
+    const int mask = (1 << c.page_shift) - 1;
+
+    f32x4 o[VW];
+#pragma unroll
+    for (int i = 0; i < VW; ++i) o[i] = zero4();
+    float m = -INFINITY, l = 0.f;
+
+    Pages pages;
+    auto load_k = [&](int i, int b) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int page = pages.get(2 * i + s), cell = b * kKB + 32 * wave + 16 * s;
+            const int64_t at = page < 0 ? 0 : page * c.k_page + (cell & mask) * c.k_cell;
+            x.load_k(s, kp + at + col * c.k_cell, g);
+        }
+    };
+    pages.refill(c, w.n, w.b0, wave, lane, w.hi, w.b1);
+    if (w.b0 < w.b1) load_k(0, w.b0);
+#pragma unroll 1
+    for (int b = w.b0; b < w.b1; ++b) {
+        const int i = (b - w.b0) & 31, cell0 = b * kKB + 32 * wave;
+        const int page0 = pages.get(2 * i), page1 = pages.get(2 * i + 1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int page = s ? page1 : page0;
+            const int64_t at = page < 0 ? 0 : page * c.v_page + ((cell0 + 16 * s) & mask) * c.v_cell;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x.load_v(4 * s + j, vp + at + (4 * g + j) * c.v_cell, col);
+        }
+        f32x4 s0 = x.scores(0), s1 = x.scores(1);
+        mfma_settle(s0, s1);
+        // the next block's keys
+        if (i == 31) pages.refill(c, w.n, b + 1, wave, lane, w.hi, w.b1);
+        if (b + 1 < w.b1) load_k(i + 1, b + 1);
+        const bool edge = page0 < 0 || page1 < 0 || cell0 < all_lo || cell0 + 32 > all_hi;
+        bool odd = false;
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int cell = cell0 + (j < 4 ? 0 : 16) + 4 * g + (j & 3);
+                const bool there = (j < 4 ? page0 : page1) >= 0 && cell < w.cells;
+                if (!there || cell > pos || cell < from) (j < 4 ? s0 : s1)[j & 3] = -INFINITY;
+                if (!there || cell >= w.hi || cell < w.lo) x.clear_v(j);
+                if (ragged) odd |= x.odd_v(j);
+            }
+        }
+        float t = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])), fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
+        t = max_groups(t) * p.scale;
+        // the maximum is let run ahead by up to 2^8 before the sums are rescaled
+        if (__any(t > m + 8.f)) {
+            const float m1 = fmaxf(m, t), r = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m1);
+            m = m1;
+            l *= r;
+#pragma unroll
+            for (int k = 0; k < VW; ++k) o[k] *= r;
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        float e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            e[j] = __builtin_amdgcn_exp2f(fmaf(j < 4 ? s0[j & 3] : s1[j & 3], p.scale, -base));
+            l += e[j];
+        }
+        if (__builtin_expect(edge && __any(odd), 0)) {
+            // infinities or NaN in cells that some rows see and others do not: a weight of 0 does not hide them, so
+            // each row adds only the cells that it sees
+#pragma unroll 1
+            for (int k = 0; k < 32; ++k) {
+                const int j = (k >> 4) * 4 + (k & 3), cell = cell0 + k, page = k < 16 ? page0 : page1;
+                float mine = e[0];
+#pragma unroll
+                for (int y = 1; y < 8; ++y) mine = j == y ? e[y] : mine;
+                const float weight = __shfl(mine, ((k & 15) >> 2) * 16 + col, 64);
+                if (page < 0 || cell > pos || cell < from || cell >= w.cells) continue;
+                const IO *v = vp + page * c.v_page + (cell & mask) * c.v_cell;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int y = 0; y < VW; ++y) o[y][r] = fmaf(weight, IoTraits<IO>::load1(v + VW * (4 * g + r) + y), o[y][r]);
+            }
+        } else {
+            x.add(o, e);
+        }
+        settle(o);
+    }
+
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    __syncthreads();  // the plan's LDS has been read
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < VW; i += 4)
+            *reinterpret_cast<f32x4 *>(&lds.sum.o[wave][col][VW * (4 * g + r) + i]) =
+                f32x4{o[i][r], o[i + 1][r], o[i + 2][r], o[i + 3][r]};
+    if (g == 0) {
+        lds.sum.m[wave][col] = m;
+        lds.sum.l[wave][col] = l;
+    }
+    __syncthreads();
+    const int out = tid >> 4, c16 = tid & 15;
+    float top = -INFINITY, sum = 0.f, y[VW];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, lds.sum.m[k][out]);
+#pragma unroll
+    for (int i = 0; i < VW; ++i) y[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float r = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(lds.sum.m[k][out] - top);
+        sum = fmaf(lds.sum.l[k][out], r, sum);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) y[i] = fmaf(lds.sum.o[k][out][VW * c16 + i], r, y[i]);
+    }
+    put_row<IO, DV, kM>(p, w, out, c16, y, top, sum);
+}
+
+// Joins the splits of a tile.  Bound: the latency of reading them, so a workgroup takes few rows, a row's splits go
+// to 256 / (RJ * DV / 4) groups of threads side by side, and there is a workgroup for every RJ rows.
+template <typename IO, int DV, int RJ>
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p, int M) {
+    constexpr int LPR = DV / 4, SG = 256 / (RJ * LPR);
+    static_assert(SG >= 1);
+    const int per = (M + RJ - 1) / RJ;
+    const int64_t tile = blockIdx.x / (unsigned)per;
+    const int chunk = blockIdx.x % (unsigned)per;
+    if (tile >= (int64_t)p.desc[0] * p.Hk) return;
+    const int32_t *d = p.desc + kDesc * (1 + tile);
+    const int n = d[0], head = d[1], row0 = d[2], rows = d[3], splits = d[4];
+    const int tid = threadIdx.x, lane = tid % LPR, sg = tid / LPR % SG, rj = tid / (LPR * SG);
+    const int row = chunk * RJ + rj;
+    // (what no workgroup has written, as offsets that overlap leave it, is no row either)
+    if (n < 0 || n >= p.c.num_seqs || head < 0 || head >= p.Hk || row0 < 0 || rows > M || splits < 2 || d[5] < 0 ||
+        d[5] > p.slots - splits || chunk * RJ >= rows)
+        return;
+    const Seq s = sequence(p.c, n);
+    if (row0 > s.len * p.G - rows) return;
+    const int64_t stride = (int64_t)p.Hk * M * (DV + 2);
+    const float *part = p.part + ((int64_t)d[5] * p.Hk + head) * M * (DV + 2);
+    __shared__ float so[SG][RJ][DV + 4], sm[SG][RJ], sl[SG][RJ];
+    float m = -INFINITY, l = 0.f;
+    f32x4 o = zero4();
+    if (row < rows) {
+#pragma unroll 4
+        for (int i = sg; i < splits; i += SG) {
+            const float *q = part + i * stride;
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(q + row * DV + 4 * lane);
+            const float ms = q[M * DV + row], ls = q[M * DV + M + row];
+            const float m1 = fmaxf(m, ms), base = m1 == -INFINITY ? 0.f : m1;
+            const float a = __builtin_amdgcn_exp2f(m - base), b = __builtin_amdgcn_exp2f(ms - base);
+            m = m1;
+            l = l * a + ls * b;
+            o = o * a + v * b;
+        }
+    }
+    if constexpr (SG > 1) {
+        *reinterpret_cast<f32x4 *>(&so[sg][rj][4 * lane]) = o;
+        if (lane == 0) {
+            sm[sg][rj] = m;
+            sl[sg][rj] = l;
+        }
+        __syncthreads();
+        if (sg > 0) return;
+#pragma unroll
+        for (int k = 1; k < SG; ++k) m = fmaxf(m, sm[k][rj]);
+        const float base = m == -INFINITY ? 0.f : m;
+        l = 0.f;
+        o = zero4();
+#pragma unroll
+        for (int k = 0; k < SG; ++k) {
+            const float a = __builtin_amdgcn_exp2f(sm[k][rj] - base);
+            l += sl[k][rj] * a;
+            o += *reinterpret_cast<const f32x4 *>(&so[k][rj][4 * lane]) * a;
+        }
+    }
+    if (row >= rows) return;
+    const int64_t at = out_row(p, s, head, row0 + row);
+    const float r = l == 0.f ? 0.f : 1.f / l;
+    IoTraits<IO>::store4(static_cast<IO *>(p.out) + at * DV + 4 * lane, make_float4(o[0] * r, o[1] * r, o[2] * r, o[3] * r));
+    if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+template <typename IO>
+hipError_t rows(const AttnParams &p, dim3 grid, hipStream_t s) {
+    const dim3 block(256);
+    if (p.dk == 128 && p.dv == 128) hipLaunchKernelGGL((attn_rows_kernel<IO, 128, 128>), grid, block, 0, s, p);
+    if (p.dk == 128 && p.dv == 64) hipLaunchKernelGGL((attn_rows_kernel<IO, 128, 64>), grid, block, 0, s, p);
+    if (p.dk == 64 && p.dv == 128) hipLaunchKernelGGL((attn_rows_kernel<IO, 64, 128>), grid, block, 0, s, p);
+    if (p.dk == 64 && p.dv == 64) hipLaunchKernelGGL((attn_rows_kernel<IO, 64, 64>), grid, block, 0, s, p);
+    return hipGetLastError();
+}
+
+template <typename IO, int RJ>
+hipError_t join(const AttnParams &p, int M, int64_t tiles, hipStream_t s) {
+    const dim3 grid((unsigned)(tiles * p.Hk * ((M + RJ - 1) / RJ))), block(256);
+    if (p.dv == 128)
+        hipLaunchKernelGGL((attn_join_kernel<IO, 128, RJ>), grid, block, 0, s, p, M);
+    else
+        hipLaunchKernelGGL((attn_join_kernel<IO, 64, RJ>), grid, block, 0, s, p, M);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// c_min: two blocks, 256 cells, below which joining costs more than it gains
+AttnTile attn_rows_tile(bool) { return {kM, kKB, 2, 4}; }
+
+hipError_t launch_attn_rows(bool bf16, const AttnParams &p, int64_t blocks, hipStream_t stream) {
+    if (blocks <= 0) return hipSuccess;
+    return bf16 ? rows<uint16_t>(p, dim3((unsigned)blocks), stream) : rows<float>(p, dim3((unsigned)blocks), stream);
+}
+
+hipError_t launch_attn_join(bool bf16, const AttnParams &p, int M, int64_t tiles, hipStream_t stream) {
+    if (tiles <= 0) return hipSuccess;
+    return bf16 ? join<uint16_t, 1>(p, M, tiles, stream) : join<float, 1>(p, M, tiles, stream);
+}
+
+}  // namespace paged
+}  // namespace kda

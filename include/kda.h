@@ -516,6 +516,130 @@ kda_status_t kda_norm_gate_bwd(int64_t rows, int32_t d, int32_t io_dtype, float 
 /* Workspace bytes kda_norm_gate_bwd needs (0 also for arguments it refuses). */
 size_t kda_norm_gate_bwd_workspace(int64_t rows, int32_t d, int32_t io_dtype);
 
+/* Rotary positions of queries and keys (kda_rope). */
+typedef struct {
+    int32_t batch;        /* B sequences of seq_len tokens (a packed batch: 1) */
+    int32_t seq_len;
+    int32_t num_heads_q;  /* >= 1 */
+    int32_t num_heads_k;  /* >= 0; 0: q only, k is not looked at */
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t io_dtype;     /* kda_dtype_t of q, k and the results */
+    int32_t rot_dim;      /* leading channels of a head that turn: a multiple of 16 up to head_dim; the rest is copied */
+    int32_t interleaved;  /* 0: channels i and i + rot_dim / 2 are a pair; 1: channels 2 i and 2 i + 1 */
+    int32_t inverse;      /* 1: turned back, which is the gradient of turning */
+    float amplitude;      /* multiplies the turned channels (1, or what kda_rope_frequencies says) */
+    int64_t stride_q;     /* elements from one token to the next (0: dense), multiples of 16 bytes; the heads of */
+    int64_t stride_k;     /* a token are dense */
+    int64_t stride_q_out;
+    int64_t stride_k_out;
+} kda_rope_problem_t;
+
+/*
+ * kda_rope -- rotary positions.  Pair i of a head at position p becomes, with t = p inv_freq[i] (64 bits),
+ *
+ *     (x1, x2) -> amplitude (x1 cos t - x2 sin t, x1 sin t + x2 cos t)       inverse: t -> -t
+ *
+ *  q, q_out  [tokens, Hq, d], k, k_out [tokens, Hk, d]  io dtype; an output may be its input (same stride), and
+ *            overlaps nothing else
+ *  positions int32 [tokens], any value; NULL: a token's index in its sequence
+ *  inv_freq  fp32 [rot_dim / 2] device
+ * fp32 arithmetic, rounded once.  Errors as for kda_chunk_fwd.
+ */
+kda_status_t kda_rope(const kda_rope_problem_t *problem, const void *q, const void *k, const int32_t *positions,
+                      const float *inv_freq, void *q_out, void *k_out, void *stream);
+
+typedef enum {
+    KDA_ROPE_PLAIN = 0,  /* f_i = base^(-2 i / rot_dim) */
+    KDA_ROPE_LINEAR = 1, /* f_i / factor: positions squeezed */
+    KDA_ROPE_BASE = 2,   /* base factor^(rot_dim / (rot_dim - 2)) in place of base: the slowest pair squeezed by factor */
+    KDA_ROPE_PARTS = 3   /* pairs with fewer than `slow` turns in original_len positions squeezed by factor, those with more
+                            than `fast` kept, a ramp in between; amplitude 0.1 ln(factor) + 1 */
+} kda_rope_scaling_t;
+
+/* Frequencies for kda_rope, on the host: rot_dim / 2 values, computed in 64 bits and rounded once, and the amplitude
+ * that goes with them.  factor >= 1, base > 1; original_len, slow < fast only for KDA_ROPE_PARTS. */
+kda_status_t kda_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor, int64_t original_len,
+                                  double slow, double fast, float *inv_freq_host, float *amplitude_host);
+
+/* Shape of the calls on a paged key-value cache (kda_paged_*).  Query head h reads key-value head
+ * h / (num_heads_q / num_heads_kv).  The cache is two pools of num_pages pages, each of page_size cells of
+ * num_heads_kv keys or values; sequence n's cell p is cell p % page_size of page block_table[n][p / page_size]. */
+typedef struct {
+    int32_t batch;         /* B sequences of seq_len new tokens; must be 1 with cu_seqlens */
+    int32_t seq_len;       /* new tokens per sequence, or all of them with cu_seqlens */
+    int32_t num_seqs;      /* with cu_seqlens: its sequences; else ignored */
+    int32_t num_heads_q;   /* Hq, a multiple of Hkv */
+    int32_t num_heads_kv;  /* Hkv >= 1 */
+    int32_t head_dim_k;    /* 64 or 128 */
+    int32_t head_dim_v;    /* 64 or 128 */
+    int32_t io_dtype;      /* kda_dtype_t of q, k, v, out and the pages */
+    int32_t page_size;     /* cells of a page: a power of two, at least 16 */
+    int32_t max_pages;     /* entries of a sequence in block_table; max_pages * page_size < 2^31 */
+    int64_t num_pages;     /* pages in the pools (below 2^31) */
+    int64_t stride_table;  /* entries from one sequence to the next in block_table (0: max_pages) */
+    int64_t stride_q, stride_k, stride_v;                     /* as in kda_gdn_problem_t */
+    int64_t k_page_stride, k_head_stride, k_cell_stride;      /* elements, multiples of 16 bytes; all three 0: */
+    int64_t v_page_stride, v_head_stride, v_cell_stride;      /* dense [num_pages, Hkv, page_size, d] */
+} kda_paged_problem_t;
+
+/* Rotation of keys (and queries) on their way into the cache. */
+typedef struct {
+    int32_t rot_dim, interleaved;  /* as in kda_rope_problem_t, of head_dim_k */
+    float amplitude;
+    const float *inv_freq;
+    const int32_t *positions;      /* int32 [tokens], or NULL: the token's cell */
+} kda_rope_t;
+
+/*
+ * kda_paged_append -- new tokens' keys and values into the cache.  The i-th of a sequence's `new` tokens goes to cell
+ * kv_lens[n] - new + i.
+ *
+ *  k [tokens, Hkv, d_k], v [tokens, Hkv, d_v]   io dtype, strides as in the problem
+ *  q, q_out      [tokens, Hq, d_k] or NULL: queries turned like the keys in the same launch (needs rope); q_out dense,
+ *                or q itself in its own stride
+ *  rope          NULL: keys are stored as they are
+ *  block_table   int32 [num_seqs, max_pages]
+ *  kv_lens       int32 [num_seqs]: cells of each sequence with the new tokens, so that the same array goes to
+ *                kda_paged_attn
+ *  cu_seqlens, cu_seqlens_host   as for kda_gdn_chunk_fwd
+ *  k_pages, v_pages   the pools; they may be slices of one tensor that holds a page's keys next to its values
+ * A token whose cell would be negative is padding: nothing is read or written for it.  One whose page is not in
+ * [0, num_pages), or behind max_pages, is not stored (its query is turned).  Two tokens must not share a cell.
+ * Errors as for kda_chunk_fwd; nothing is allocated.
+ */
+kda_status_t kda_paged_append(const kda_paged_problem_t *problem, const void *k, const void *v, const void *q,
+                              const kda_rope_t *rope, const int32_t *block_table, const int32_t *kv_lens,
+                              const int32_t *cu_seqlens, const int32_t *cu_seqlens_host, void *k_pages, void *v_pages,
+                              void *q_out, void *stream);
+
+/*
+ * kda_paged_attn -- softmax attention of each sequence's new tokens, one or many, over its cells (the full-attention
+ * layers of a hybrid; "3:1 KDA and MLA hybrid" section).  The i-th of `new` tokens sits at t = kv_lens[n] - new + i:
+ *
+ *     o = sum_j p_j v_j,   p = softmax_j(scale q . k_j)   over the cells max(0, t - window + 1) <= j <= t
+ *
+ *  q     [tokens, Hq, d_k]   io dtype, stride as in the problem
+ *  k_pages, v_pages, block_table, kv_lens, cu_seqlens, cu_seqlens_host   as for kda_paged_append, which comes first
+ *  window        0: all cells up to the token's own
+ *  out   [tokens, Hq, d_v]   io dtype, dense
+ *  lse   [tokens, Hq] fp32 or NULL: ln sum_j exp(scale q . k_j), to join with attention over other cells
+ *  workspace     kda_paged_attn_workspace() bytes (may be 0), 256-byte aligned, not initialised: the parts of long rows
+ *                of cells that several workgroups share
+ * A row without cells (t < 0) is 0, its lse -inf.  Cells whose page is not in [0, num_pages) do not exist, nor do those
+ * behind max_pages.  What masked cells and cells behind kv_lens hold does not matter, NaN included; rows of out and
+ * lse that no sequence owns are left as they are.
+ * Statistics and sums are fp32; bf16 io: weights are rounded to bf16 for their product with the values.  The
+ * results repeat bit for bit.  Calls that overlap in time need a workspace each.  Errors as for kda_chunk_bwd.
+ */
+kda_status_t kda_paged_attn(const kda_paged_problem_t *problem, const void *q, const void *k_pages, const void *v_pages,
+                            const int32_t *block_table, const int32_t *kv_lens, const int32_t *cu_seqlens,
+                            const int32_t *cu_seqlens_host, float scale, int32_t window, void *out, float *lse,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes kda_paged_attn needs for the problem on the current device, as a plain batch and, where batch is 1 and
+ * num_seqs > 0, also as a packed one, whatever the lengths; *bytes = 0 on error. */
+kda_status_t kda_paged_attn_workspace(const kda_paged_problem_t *problem, size_t *bytes);
+
 /* Static description of a status code. */
 const char *kda_status_string(kda_status_t status);
 
