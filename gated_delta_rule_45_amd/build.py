@@ -17,7 +17,7 @@ SOURCES = ["kda_api.cpp", "kda_recurrent.hip", "kda_chunk_bf16.hip", "kda_chunk_
            "kda_split_f32.hip", "kda_epilogue.hip", "kda_prologue.hip", "kda_bwd_bf16.hip", "kda_bwd_f32.hip",
            "kda_dplr.hip", "kda_noalloc.hip", "kda_gdn_api.cpp", "kda_gdn_bf16.hip", "kda_gdn_f32.hip",
            "kda_gdn_grad_bf16.hip", "kda_gdn_grad_f32.hip", "kda_gdn_decode.hip", "kda_gdn_convert.hip", "kda_gdn_segments.hip",
-           "kda_epilogue_bwd.hip", "kda_paged_api.cpp", "kda_rope.hip", "kda_paged_append.hip", "kda_paged_attn.hip"]
+           "kda_epilogue_bwd.hip", "kda_paged_api.cpp", "kda_rope.hip", "kda_paged_append.hip", "kda_paged_attn.hip", "kda_paged_attn_tile.hip"]
 ARCH = "gfx950"
 # Packed fp32 VALU ops are disabled for every device pass.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

@@ -71,6 +71,7 @@ struct AttnParams {
     float *part;               // per (split, head): M rows of d_v sums, M maxima, M sums of weights
 };
 constexpr int kDesc = 8;
+constexpr int kFewRows = 16;  // one tile of the kernel for few rows
 
 // Shape of a kernel's tiles.
 struct AttnTile {
@@ -78,6 +79,8 @@ struct AttnTile {
 };
 AttnTile attn_rows_tile(bool bf16);
 hipError_t launch_attn_rows(bool bf16, const AttnParams &p, int64_t blocks, hipStream_t stream);
+AttnTile attn_tile_tile();
+hipError_t launch_attn_tile(const AttnParams &p, int64_t blocks, hipStream_t stream);  // bf16
 // joins the splits of at most `tiles` tiles of M rows per head
 hipError_t launch_attn_join(bool bf16, const AttnParams &p, int M, int64_t tiles, hipStream_t stream);
 

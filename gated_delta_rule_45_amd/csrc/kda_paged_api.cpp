@@ -115,6 +115,8 @@ kda_status_t pool_strides(const char *name, const kda_paged_problem_t *p, int64_
         if (out[i] > (1LL << 58) / size[i]) return set_error(KDA_ERR_UNSUPPORTED, "%s: pool too large", name);
         inner = out[i] * (size[i] - 1) + inner;
     }
+    if (size[2] > 1 && out[2] > 1 << 26)  // 16 cells are reached by a 32-bit offset in bytes
+        return set_error(KDA_ERR_UNSUPPORTED, "%s: cells %lld elements apart", name, (long long)out[2]);
     for (int i = 0; i < 3; ++i)
         if (size[i] <= 1) out[i] = 0;
     return KDA_OK;
@@ -225,8 +227,9 @@ kda_status_t plan_launch(const kda_paged_problem_t *p, const Shape &s, bool pack
         tiles = s.num_seqs * count(p->seq_len);
     } else if (cu_host) {
         for (int32_t i = 0; i < s.num_seqs; ++i) tiles += count(cu_host[i + 1] - cu_host[i]);
-    } else if (s.tokens * s.G >= l.rows_lo) {
-        tiles = s.tokens * s.G / M + std::min<int64_t>(s.num_seqs, s.tokens);
+    } else {
+        const int64_t rows = s.tokens * s.G;
+        tiles = rows / M + std::min<int64_t>(s.num_seqs, rows / std::max<int64_t>(l.rows_lo, s.G));
     }
     int64_t most = (cells + KB - 1) / KB;  // blocks of a tile, at most
     if (window > 0) most = std::min(most, ((int64_t)window + (M - 1) / s.G + 1 + KB - 1) / KB + 1);
@@ -253,21 +256,32 @@ kda_status_t plan_launch(const kda_paged_problem_t *p, const Shape &s, bool pack
 }
 
 struct AttnPlan {
-    Launch part[1];
+    Launch part[2];
+    bool tile[2] = {false, false};
     int n = 0;
     size_t bytes = 0;
 };
 
+// Sequences of at most 16 rows go to the kernel for few rows, longer ones of bf16 calls to the one that stages cells in LDS
+// for 256 rows.  A packed batch may hold both, and what its offsets do not rule out on the host is launched, but for a
+// batch with no more tokens than sequences: the step of one token each that it looks like needs no second launch, and
+// longer sequences among empty ones come out the same from the first.
 kda_status_t plan_attn(const kda_paged_problem_t *p, const Shape &s, bool packed, const int32_t *cu_host, int32_t window, int cus,
                        AttnPlan &a) {
     a = AttnPlan{};
-    Launch l;
-    l.t = kda::paged::attn_rows_tile(p->io_dtype == KDA_BF16);
-    a.part[a.n++] = l;
-    for (int i = 0; i < a.n; ++i) {
-        const kda_status_t st = plan_launch(p, s, packed, cu_host, window, cus, a.part[i]);
+    const bool bf16 = p->io_dtype == KDA_BF16;
+    const bool both = bf16 && (!packed || cu_host || s.tokens > s.num_seqs);
+    for (int tile = 0; tile < (both ? 2 : 1); ++tile) {
+        Launch l;
+        l.t = tile ? kda::paged::attn_tile_tile() : kda::paged::attn_rows_tile(bf16);
+        if (tile) l.rows_lo = kda::paged::kFewRows + 1;
+        if (both && !tile) l.rows_hi = kda::paged::kFewRows;
+        const kda_status_t st = plan_launch(p, s, packed, cu_host, window, cus, l);
         if (st != KDA_OK) return st;
-        a.bytes += a.part[i].desc + a.part[i].part;
+        if (l.blocks == 0) continue;
+        a.bytes += l.desc + l.part;
+        a.tile[a.n] = tile;
+        a.part[a.n++] = l;
     }
     return KDA_OK;
 }
@@ -511,14 +525,14 @@ kda_status_t kda_paged_attn(const kda_paged_problem_t *p, const void *q, const v
             r.slots = (int32_t)l.slots;
             r.desc = l.desc ? reinterpret_cast<int32_t *>(ws) : nullptr;
             r.part = reinterpret_cast<float *>(ws + l.desc);
-            if (l.blocks == 0) continue;
-            st = done(kda::paged::launch_attn_rows(bf16, r, l.blocks, hs), "kda_paged_attn launch");
+            st = done(a.tile[i] ? kda::paged::launch_attn_tile(r, l.blocks, hs) : kda::paged::launch_attn_rows(bf16, r, l.blocks, hs),
+                      "kda_paged_attn launch");
             if (st == KDA_OK && l.tiles > 0)
                 st = done(kda::paged::launch_attn_join(bf16, r, l.t.M, l.tiles, hs), "kda_paged_attn join launch");
             if (st != KDA_OK) return st;
             ws += l.desc + l.part;
         }
-        return KDA_OK;
+        return done(hipSuccess, "");
     } catch (...) {
         return set_error(KDA_ERR_HIP, "unexpected exception in argument checks");
     }

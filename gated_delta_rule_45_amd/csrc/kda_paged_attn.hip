@@ -19,7 +19,7 @@ namespace kda {
 namespace paged {
 namespace {
 
-constexpr int kM = 16, kKB = 128;
+constexpr int kM = kFewRows, kKB = 128;
 
 __device__ __forceinline__ float max_groups(float x) {  // over the lanes that differ in g
     auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(AttnParams p) {
         } sum;
     } lds;
     Work w;
-    if (!find_work(p, kM, kKB, w, lds.plan)) return;
+    if (!find_work<256>(p, kM, kKB, w, lds.plan)) return;
     const Cache &c = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4,
               col = lane & 15;
@@ -290,69 +290,75 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(AttnParams p) {
     put_row<IO, DV, kM>(p, w, out, c16, y, top, sum);
 }
 
-// Joins the splits of a tile.  Bound: the latency of reading them, so a workgroup takes few rows, a row's splits go
-// to 256 / (RJ * DV / 4) groups of threads side by side, and there is a workgroup for every RJ rows.
-template <typename IO, int DV, int RJ>
+// Joins the splits of a tile.  Bound: the latency of reading them, so a row's splits go to 256 / (RJ * DV / 4) groups of threads
+// side by side, RJ rows at a time.  There is a workgroup for every RB rows of the most tiles there can be: one row where a
+// tile has 16; 32 of 256, since mostly no tile is split and what the workgroups cost is their number (131,072 of them 40 us).
+template <typename IO, int DV, int RJ, int RB>
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p, int M) {
     constexpr int LPR = DV / 4, SG = 256 / (RJ * LPR);
-    static_assert(SG >= 1);
-    const int per = (M + RJ - 1) / RJ;
+    static_assert(SG >= 1 && RB % RJ == 0);
+    const int per = M / RB;
     const int64_t tile = blockIdx.x / (unsigned)per;
     const int chunk = blockIdx.x % (unsigned)per;
     if (tile >= (int64_t)p.desc[0] * p.Hk) return;
     const int32_t *d = p.desc + kDesc * (1 + tile);
     const int n = d[0], head = d[1], row0 = d[2], rows = d[3], splits = d[4];
     const int tid = threadIdx.x, lane = tid % LPR, sg = tid / LPR % SG, rj = tid / (LPR * SG);
-    const int row = chunk * RJ + rj;
     // (what no workgroup has written, as offsets that overlap leave it, is no row either)
     if (n < 0 || n >= p.c.num_seqs || head < 0 || head >= p.Hk || row0 < 0 || rows > M || splits < 2 || d[5] < 0 ||
-        d[5] > p.slots - splits || chunk * RJ >= rows)
+        d[5] > p.slots - splits || chunk * RB >= rows)
         return;
     const Seq s = sequence(p.c, n);
     if (row0 > s.len * p.G - rows) return;
     const int64_t stride = (int64_t)p.Hk * M * (DV + 2);
     const float *part = p.part + ((int64_t)d[5] * p.Hk + head) * M * (DV + 2);
     __shared__ float so[SG][RJ][DV + 4], sm[SG][RJ], sl[SG][RJ];
-    float m = -INFINITY, l = 0.f;
-    f32x4 o = zero4();
-    if (row < rows) {
+#pragma unroll 1
+    for (int row = chunk * RB + rj; row - rj < min(chunk * RB + RB, rows); row += RJ) {
+        float m = -INFINITY, l = 0.f;
+        f32x4 o = zero4();
+        if (row < rows) {
 #pragma unroll 4
-        for (int i = sg; i < splits; i += SG) {
-            const float *q = part + i * stride;
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(q + row * DV + 4 * lane);
-            const float ms = q[M * DV + row], ls = q[M * DV + M + row];
-            const float m1 = fmaxf(m, ms), base = m1 == -INFINITY ? 0.f : m1;
-            const float a = __builtin_amdgcn_exp2f(m - base), b = __builtin_amdgcn_exp2f(ms - base);
-            m = m1;
-            l = l * a + ls * b;
-            o = o * a + v * b;
+            for (int i = sg; i < splits; i += SG) {
+                const float *q = part + i * stride;
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(q + row * DV + 4 * lane);
+                const float ms = q[M * DV + row], ls = q[M * DV + M + row];
+                const float m1 = fmaxf(m, ms), base = m1 == -INFINITY ? 0.f : m1;
+                const float a = __builtin_amdgcn_exp2f(m - base), b = __builtin_amdgcn_exp2f(ms - base);
+                m = m1;
+                l = l * a + ls * b;
+                o = o * a + v * b;
+            }
+        }
+        if constexpr (SG > 1) {
+            if (row - rj > chunk * RB) __syncthreads();  // the last rows' have been read
+            *reinterpret_cast<f32x4 *>(&so[sg][rj][4 * lane]) = o;
+            if (lane == 0) {
+                sm[sg][rj] = m;
+                sl[sg][rj] = l;
+            }
+            __syncthreads();
+            if (sg == 0) {
+#pragma unroll
+                for (int k = 1; k < SG; ++k) m = fmaxf(m, sm[k][rj]);
+                const float base = m == -INFINITY ? 0.f : m;
+                l = 0.f;
+                o = zero4();
+#pragma unroll
+                for (int k = 0; k < SG; ++k) {
+                    const float a = __builtin_amdgcn_exp2f(sm[k][rj] - base);
+                    l += sl[k][rj] * a;
+                    o += *reinterpret_cast<const f32x4 *>(&so[k][rj][4 * lane]) * a;
+                }
+            }
+        }
+        if (row < rows && sg == 0) {
+            const int64_t at = out_row(p, s, head, row0 + row);
+            const float r = l == 0.f ? 0.f : 1.f / l;
+            IoTraits<IO>::store4(static_cast<IO *>(p.out) + at * DV + 4 * lane, make_float4(o[0] * r, o[1] * r, o[2] * r, o[3] * r));
+            if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
         }
     }
-    if constexpr (SG > 1) {
-        *reinterpret_cast<f32x4 *>(&so[sg][rj][4 * lane]) = o;
-        if (lane == 0) {
-            sm[sg][rj] = m;
-            sl[sg][rj] = l;
-        }
-        __syncthreads();
-        if (sg > 0) return;
-#pragma unroll
-        for (int k = 1; k < SG; ++k) m = fmaxf(m, sm[k][rj]);
-        const float base = m == -INFINITY ? 0.f : m;
-        l = 0.f;
-        o = zero4();
-#pragma unroll
-        for (int k = 0; k < SG; ++k) {
-            const float a = __builtin_amdgcn_exp2f(sm[k][rj] - base);
-            l += sl[k][rj] * a;
-            o += *reinterpret_cast<const f32x4 *>(&so[k][rj][4 * lane]) * a;
-        }
-    }
-    if (row >= rows) return;
-    const int64_t at = out_row(p, s, head, row0 + row);
-    const float r = l == 0.f ? 0.f : 1.f / l;
-    IoTraits<IO>::store4(static_cast<IO *>(p.out) + at * DV + 4 * lane, make_float4(o[0] * r, o[1] * r, o[2] * r, o[3] * r));
-    if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <typename IO>
@@ -365,13 +371,13 @@ hipError_t rows(const AttnParams &p, dim3 grid, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <typename IO, int RJ>
+template <typename IO, int RJ, int RB>
 hipError_t join(const AttnParams &p, int M, int64_t tiles, hipStream_t s) {
-    const dim3 grid((unsigned)(tiles * p.Hk * ((M + RJ - 1) / RJ))), block(256);
+    const dim3 grid((unsigned)(tiles * p.Hk * (M / RB))), block(256);
     if (p.dv == 128)
-        hipLaunchKernelGGL((attn_join_kernel<IO, 128, RJ>), grid, block, 0, s, p, M);
+        hipLaunchKernelGGL((attn_join_kernel<IO, 128, RJ, RB>), grid, block, 0, s, p, M);
     else
-        hipLaunchKernelGGL((attn_join_kernel<IO, 64, RJ>), grid, block, 0, s, p, M);
+        hipLaunchKernelGGL((attn_join_kernel<IO, 64, RJ, RB>), grid, block, 0, s, p, M);
     return hipGetLastError();
 }
 
@@ -387,7 +393,8 @@ hipError_t launch_attn_rows(bool bf16, const AttnParams &p, int64_t blocks, hipS
 
 hipError_t launch_attn_join(bool bf16, const AttnParams &p, int M, int64_t tiles, hipStream_t stream) {
     if (tiles <= 0) return hipSuccess;
-    return bf16 ? join<uint16_t, 1>(p, M, tiles, stream) : join<float, 1>(p, M, tiles, stream);
+    if (M > kM) return join<uint16_t, 8, 32>(p, M, tiles, stream);
+    return bf16 ? join<uint16_t, 1, 1>(p, M, tiles, stream) : join<float, 1, 1>(p, M, tiles, stream);
 }
 
 }  // namespace paged

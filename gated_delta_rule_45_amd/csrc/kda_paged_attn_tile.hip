@@ -1,0 +1,354 @@
+// Attention of many rows over a paged cache (chunks and whole prompts, bf16): tiles of 256 rows.
+//
+// Bound: the matrix units.  Eight waves own 32 rows each and share 64-cell blocks of keys and values in LDS; with
+// 2 (d_k + d_v) flops per row and cell a block costs 2,048 cycles of a CU's matrix units, and about as many of its vector
+// units for the softmax (an exponential is a quarter-rate instruction), so the two have to run side by side: the waves
+// 0-3 and 4-7, one of each on every SIMD, take turns, half an iteration apart: while one group multiplies (O += P V of
+// block t, then S = K Q^T of block t + 1), the other works out the weights of its block and starts the loads of later
+// ones.  A barrier ends each half.  Keys are staged three blocks ahead of their use, values two, in rings of four buffers.
+//
+// Layouts (lane = 32 h + r).  S^T = K Q^T and O^T = V^T P^T as in the kernel for few rows, here as 32 x 32 tiles: a
+// lane holds the scores of row r for cells 8 a + 4 h + b of each 32, which are the contraction slots of the next product as they
+// are.  V^T comes from LDS through the transposing read (4 cells of one column per lane).  Direct global-to-LDS loads
+// place lane l's 16 bytes at 16 l, so rows are scattered over the banks by which bytes a lane fetches: 16-byte
+// pieces of keys move by row mod 8, 32-byte pieces of values (what 16 lanes read of a row) by row mod 4.
+#include "kda_paged_work.h"
+
+namespace kda {
+namespace paged {
+namespace {
+
+constexpr int kM = 256, kKB = 64, kNT = 512, kRing = 4;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
+
+// what lanes read in place of cells that do not exist or that no row of the tile sees
+__device__ const u32x4 kZeros[1] = {};
+
+// Position of 16-byte piece c of row r in LDS, and back (both ways are the same exchange).
+template <int D>
+__device__ __forceinline__ int k_place(int r, int c) { return c ^ (r & 7); }
+template <int D>
+__device__ __forceinline__ int v_place(int r, int c) { return c ^ ((D == 128 ? r & 3 : (r >> 1) & 1) << 2); }
+
+// load_lds16 whose end is left to wait_vmcnt and a barrier: the compiler, which cannot tell the buffers of a ring apart, would
+// wait for the builtin's loads before every LDS read.  (M0 holds the destination and must be set a cycle before.)
+__device__ __forceinline__ unsigned lds_address(const void *p) {
+    return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
+}
+__device__ __forceinline__ void load_lds16_async(const void *base, unsigned offset, void *lds) {  // base: the wave's, offset: a lane's
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0" ::"s"(base), "v"(offset), "s"(lds_address(lds))
+                 : "memory");
+}
+__device__ __forceinline__ void load_lds16_async(const void *src, void *lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_address(lds)) : "memory");
+}
+
+template <int DK, int DV>
+struct Lds {
+    uint16_t k[kRing][kKB * DK], v[kRing][kKB * DV];
+    unsigned missing[kRing];  // a byte per 16 cells: page does not exist
+    PlanLds plan;
+};
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
+    constexpr int KS = DK / 16, DB = DV / 32;                    // steps of a score, column blocks of the output
+    constexpr int KC = DK / 8, VC = DV / 8;                      // 16-byte pieces of a row
+    constexpr int KI = kKB * KC / kNT, VI = kKB * VC / kNT;      // loads of a wave per block
+    constexpr int KR = 64 / KC, VR = 64 / VC;                    // rows of a load
+    __shared__ Lds<DK, DV> lds;
+    Work w;
+    if (!find_work<kNT>(p, kM, kKB, w, lds.plan)) return;
+    const Cache &c = p.c;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 31, h = lane >> 5;
+
+    // this wave's rows
+    const int wrow = min(wave * 32, w.rows - 1), wlast = min(wave * 32 + 31, w.rows - 1), row = w.row0 + min(wave * 32 + r, w.rows - 1);
+    const bool active = wave * 32 < w.rows;
+    const int pos = w.pos(row, p.G), from = w.first(pos, p.window), last = min(pos, w.cells - 1);
+    const int pos0 = w.pos(w.row0 + wrow, p.G), pos1 = w.pos(w.row0 + wlast, p.G);
+    const int see_lo = w.first(pos0, p.window), see_hi = active ? min(pos1 + 1, w.cells) : 0;   // some row
+    const int all_lo = w.first(pos1, p.window), all_hi = min(pos0 + 1, w.cells);                // every row
+    u32x4 q[KS];
+    {
+        const uint16_t *x = static_cast<const uint16_t *>(p.q) + (w.seq.t0 + row / p.G) * p.ldq + (w.head * p.G + row % p.G) * DK;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            q[i] = *reinterpret_cast<const u32x4 *>(x + 16 * i + 8 * h);
+            if (p.flip) q[i] ^= 0x80008000u;
+        }
+    }
+
+    // ---- staging: load i of a wave covers rows KR (wave + 8 i) .. of the block
+    const char *kp = reinterpret_cast<const char *>(static_cast<const uint16_t *>(c.k) + w.head * c.k_head);
+    const char *vp = reinterpret_cast<const char *>(static_cast<const uint16_t *>(c.v) + w.head * c.v_head);
+    const __attribute__((address_space(4))) int32_t *table =
+        (const __attribute__((address_space(4))) int32_t *)(c.table + w.n * c.table_ld);
+    const int mask = (1 << c.page_shift) - 1;
+    const int nt = w.b1 - w.b0;
+    // A wave loads rows 8 wave .. 8 wave + 7 of every block, of keys and of values: one page.  ek, ev: table entries of
+    // the next blocks' loads, read an iteration ahead.
+    const int row8 = 8 * wave;
+    int ek = -1, ev = -1;
+    auto look = [&](int t) { return table[min((w.b0 + t) * kKB + row8, w.hi - 1) >> c.page_shift]; };
+    unsigned k_off[KI], v_off[VI];  // bytes of a lane's piece from the wave's first cell
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+        const int rr = KR * i + lane / KC;
+        k_off[i] = (unsigned)(rr * c.k_cell) * 2 + 16 * k_place<DK>(row8 + rr, lane % KC);
+    }
+#pragma unroll
+    for (int i = 0; i < VI; ++i) {
+        const int rr = VR * i + lane / VC;
+        v_off[i] = (unsigned)(rr * c.v_cell) * 2 + 16 * v_place<DV>(row8 + rr, lane % VC);
+    }
+    // Loads of a wave's rows from page e; cells that are not there or out of sight are zeros.  Returns whether the page exists.
+    auto fetch = [&](auto &off, const char *pool, int64_t page, int64_t cell_ld, int e, int cell0, uint16_t *to, int rows_per_load,
+                     int elems_per_load) {
+        constexpr int N = sizeof(off) / sizeof(off[0]);
+        const bool exists = (unsigned)e < (unsigned)c.num_pages;
+        const char *base = pool + ((int64_t)e * page + (int64_t)(cell0 & mask) * cell_ld) * 2;
+        if (exists && cell0 >= w.lo && cell0 + 8 <= w.hi) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) load_lds16_async(base, off[i], to + i * elems_per_load);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int cell = cell0 + rows_per_load * i + lane / (64 / rows_per_load);
+                load_lds16_async(exists && cell >= w.lo && cell < w.hi ? base + off[i] : reinterpret_cast<const char *>(kZeros),
+                                 to + i * elems_per_load);
+            }
+        }
+        return exists;
+    };
+    auto stage_k = [&](int t) {
+        const bool exists = fetch(k_off, kp, c.k_page, c.k_cell, ek, (w.b0 + t) * kKB + row8, &lds.k[t % kRing][row8 * DK], KR, KR * DK);
+        if (lane == 0) reinterpret_cast<uint8_t *>(&lds.missing[t % kRing])[wave / 2] = !exists;
+    };
+    auto stage_v = [&](int t) { fetch(v_off, vp, c.v_page, c.v_cell, ev, (w.b0 + t) * kKB + row8, &lds.v[t % kRing][row8 * DV], VR, VR * DV); };
+
+    f32x16 s[2], o[DB];
+#pragma unroll
+    for (int i = 0; i < DB; ++i) o[i] = f32x16(0.f);
+    u32x4 pw[4];
+    float m = -INFINITY, l = 0.f;
+
+    auto seen = [&](int t) {
+        const int c0 = (w.b0 + t) * kKB;
+        return c0 < see_hi && c0 + kKB > see_lo;
+    };
+    auto scores = [&](int t) {  // S^T of block t
+        const uint16_t *k = lds.k[t % kRing];
+        s[0] = f32x16(0.f);
+        s[1] = f32x16(0.f);
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int rr = 32 * b + r;
+                const u32x4 x = *reinterpret_cast<const u32x4 *>(k + rr * DK + 8 * k_place<DK>(rr, 2 * i + h));
+                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, q[i]), s[b],
+                                                               0, 0, 0);
+            }
+    };
+    auto value = [&](const uint16_t *v, int step, int db) {  // V^T: 32 columns, 16 cells
+        u32x4 x;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int rr = 16 * step + 8 * y + 4 * h + (lane & 15) / 4, piece = 4 * db + ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+            const uint16_t *at = v + rr * DV + 8 * v_place<DV>(rr, piece) + 4 * (lane & 1);
+            const u32x2 z = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                          (__attribute__((address_space(3))) s16x4 *)at));
+            x[2 * y] = z[0];
+            x[2 * y + 1] = z[1];
+        }
+        return x;
+    };
+    auto add = [&](int t) {  // O^T += V^T P^T of block t
+        const uint16_t *v = lds.v[t % kRing];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int b = 0; b < DB; ++b)
+                o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, value(v, i, b)),
+                                                               __builtin_bit_cast(bf16x8, pw[i]), o[b], 0, 0, 0);
+    };
+    auto edge = [&](int t, unsigned missing) {
+        const int c0 = (w.b0 + t) * kKB;
+        return c0 < all_lo || c0 + kKB > all_hi || missing != 0;
+    };
+    auto odd = [&](int t) {
+        const uint16_t *v = lds.v[t % kRing];
+        bool bad = false;
+        for (int i = 0; i < kKB * DV / 8 / 64; ++i) {
+            const u32x4 x = reinterpret_cast<const u32x4 *>(v)[i * 64 + lane];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) bad |= (x[y] & 0x7f80u) == 0x7f80u || (x[y] & 0x7f800000u) == 0x7f800000u;
+        }
+        return __any(bad);
+    };
+    auto settle = [&]() {
+        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+v"(s[0]), "+v"(s[1]));
+#pragma unroll
+        for (int i = 0; i < DB; ++i) asm volatile("" : "+v"(o[i]));
+    };
+    auto weights = [&](int t, unsigned missing) {
+        if (edge(t, missing)) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int y = 0; y < 16; ++y) {
+                    const int k = 32 * b + 8 * (y >> 2) + 4 * h + (y & 3), cell = (w.b0 + t) * kKB + k;
+                    if (cell > last || cell < from || (missing >> (8 * (2 * b + (y >> 3))) & 0xff)) s[b][y] = -INFINITY;
+                }
+        }
+        float top = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+        for (int y = 1; y < 16; ++y) top = fmaxf(fmaxf(top, s[0][y]), s[1][y]);
+        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+        top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])) * p.scale;
+        // the maximum is let run ahead by up to 2^8 before the sums are rescaled
+        if (__any(top > m + 8.f)) {
+            const float m1 = fmaxf(m, top), f = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m1);
+            m = m1;
+            l *= f;
+#pragma unroll
+            for (int b = 0; b < DB; ++b) o[b] *= f;
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float e[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                e[y] = __builtin_amdgcn_exp2f(fmaf(s[i >> 1][8 * (i & 1) + y], p.scale, -base));
+                l += e[y];
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) pw[i][y] = pack_bf16x2(e[2 * y], e[2 * y + 1]);
+        }
+    };
+    // this wave's LDS accesses are done, its loads from memory may be on their way (a fence would wait for those too)
+    auto barrier = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+    for (int t = 0; t < 3 && t < nt; ++t) {
+        ev = ek = look(t);
+        stage_k(t);
+        if (t < 2) stage_v(t);
+    }
+    // ev: of block 2, ek: of block 3
+    if (nt > 3) ek = look(3);
+    wait_vmcnt<0>();
+    barrier();
+    const bool second = wave >= 4;
+    if (second) barrier();
+    if (nt > 0 && seen(0)) scores(0);
+    settle();
+    barrier();
+    unsigned odd_blocks[2] = {0, 0};
+    int odd_base[2] = {0, 0};
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+        const bool now = seen(t);
+        const unsigned missing = __builtin_amdgcn_readfirstlane(lds.missing[t % kRing]);
+        if (t + 3 < nt) stage_k(t + 3);
+        if (t + 2 < nt) stage_v(t + 2);
+        ev = ek;
+        if (t + 4 < nt) ek = look(t + 4);
+        if (now) weights(t, missing);
+        barrier();
+        bool whole = now;
+        const int c0 = (w.b0 + t) * kKB;
+        if (now && (c0 < all_lo || c0 + kKB > all_hi) && odd(t)) {
+            // (at most two blocks at either end of a window, which spans 32 tokens at most)
+            const int side = c0 + kKB > all_hi;
+            if (!odd_blocks[side]) odd_base[side] = t;
+            odd_blocks[side] |= 1u << (t - odd_base[side]);
+            whole = false;
+        }
+        if (whole) add(t);
+        if (t + 1 < nt && seen(t + 1)) scores(t + 1);
+        settle();
+        // the loads that the previous half iteration started may go on; all others are there for everyone behind the barrier
+        if (t + 3 < nt)
+            wait_vmcnt<KI + VI>();
+        else
+            wait_vmcnt<0>();
+        barrier();
+    }
+    if (!second) barrier();
+
+    // Blocks with infinities or NaN in cells that some rows see and others do not: a weight of 0 does not hide them, so each row
+    // adds only the cells that it sees, from memory.
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+        if (!(odd_blocks[i >> 5] >> (i & 31) & 1)) continue;
+        const int c0 = (w.b0 + odd_base[i >> 5] + (i & 31)) * kKB;
+        const uint16_t *x = static_cast<const uint16_t *>(p.q) + (w.seq.t0 + row / p.G) * p.ldq + (w.head * p.G + row % p.G) * DK;
+#pragma unroll 1
+        for (int k = 0; k < kKB; ++k) {
+            const int cell = c0 + k, e = cell < w.hi ? table[cell >> c.page_shift] : -1;
+            if (e < 0 || e >= c.num_pages || cell > last || cell < from) continue;
+            const uint16_t *kr = reinterpret_cast<const uint16_t *>(kp) + e * c.k_page + (cell & mask) * c.k_cell;
+            const uint16_t *vr = reinterpret_cast<const uint16_t *>(vp) + e * c.v_page + (cell & mask) * c.v_cell;
+            float z = 0.f;
+#pragma unroll 1
+            for (int j = 0; j < DK; ++j) z = fmaf(bf16_to_f32(x[j]), bf16_to_f32(kr[j]), z);
+            const float weight = __builtin_amdgcn_exp2f(fmaf(p.flip ? -z : z, p.scale, -m));
+#pragma unroll
+            for (int b = 0; b < DB; ++b)
+#pragma unroll
+                for (int y = 0; y < 16; ++y)
+                    o[b][y] = fmaf(weight, bf16_to_f32(vr[32 * b + 8 * (y >> 2) + 4 * h + (y & 3)]), o[b][y]);
+        }
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (wave * 32 + r >= w.rows) return;
+    if (w.splits > 1) {
+        float *part = p.part + w.slot * (int64_t)(kM * (DV + 2));
+        const int at = wave * 32 + r;
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+                *reinterpret_cast<f32x4 *>(part + at * DV + 32 * b + 8 * a + 4 * h) =
+                    f32x4{o[b][4 * a], o[b][4 * a + 1], o[b][4 * a + 2], o[b][4 * a + 3]};
+        if (h == 0) {
+            part[kM * DV + at] = m;
+            part[kM * DV + kM + at] = l;
+        }
+        return;
+    }
+    const int64_t at = out_row(p, w.seq, w.head, row);
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    uint16_t *y = static_cast<uint16_t *>(p.out) + at * DV + 4 * h;
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+            IoTraits<uint16_t>::store4(y + 32 * b + 8 * a, make_float4(o[b][4 * a] * f, o[b][4 * a + 1] * f, o[b][4 * a + 2] * f,
+                                                                       o[b][4 * a + 3] * f));
+    if (p.lse && h == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+}  // namespace
+
+// c_min: eight blocks, 512 cells: a part's sums (256 rows of d_v fp32) are then small beside its keys and values' work
+AttnTile attn_tile_tile() { return {kM, kKB, 8, 2}; }
+
+hipError_t launch_attn_tile(const AttnParams &p, int64_t blocks, hipStream_t s) {
+    if (blocks <= 0) return hipSuccess;
+    const dim3 grid((unsigned)blocks), block(kNT);
+    if (p.dk == 128 && p.dv == 128) hipLaunchKernelGGL((attn_tile_kernel<128, 128>), grid, block, 0, s, p);
+    if (p.dk == 128 && p.dv == 64) hipLaunchKernelGGL((attn_tile_kernel<128, 64>), grid, block, 0, s, p);
+    if (p.dk == 64 && p.dv == 128) hipLaunchKernelGGL((attn_tile_kernel<64, 128>), grid, block, 0, s, p);
+    if (p.dk == 64 && p.dv == 64) hipLaunchKernelGGL((attn_tile_kernel<64, 64>), grid, block, 0, s, p);
+    return hipGetLastError();
+}
+
+}  // namespace paged
+}  // namespace kda

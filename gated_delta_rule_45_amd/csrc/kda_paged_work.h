@@ -4,7 +4,7 @@
 // works out the plan for itself: the blocks of all tiles are summed, cut into parts of c = max(c_min, sum / target)
 // blocks (so that about `target` workgroups have equal parts whatever the lengths are), and a prefix sum over the
 // sequences finds the part that the workgroup's number stands for.  That costs two passes over the lengths, one load
-// each for up to 256 sequences, and needs no launch of its own.  The head is the number's fastest part: workgroups go round robin to the 8 XCDs,
+// each for as many sequences as threads, and needs no launch of its own.  The head is the number's fastest part: workgroups go round robin to the 8 XCDs,
 // so that with 8 heads the tiles of a head read its cells through one L2.
 #pragma once
 
@@ -62,13 +62,15 @@ __device__ __forceinline__ T wave_sum(T x) {
     return x;
 }
 
+constexpr int kPlanWaves = 8;  // at most
 struct PlanLds {
-    long long total[4];
-    int sums[4][3];
+    long long total[kPlanWaves];
+    int sums[kPlanWaves][3];
     int found[6];  // sequence, part within it, splits, first slot, first split tile, split tiles in all
 };
 
-// The workgroup's part; false: none.  256 threads, all of them call.
+// The workgroup's part; false: none.  NT threads, all of them call.
+template <int NT>
 __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Work &w, PlanLds &lds) {
     const Cache &c = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -84,7 +86,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Wo
         if (w.n >= c.num_seqs) return false;
     } else {
         long long total = 0;
-        for (int n = tid; n < c.num_seqs; n += 256) {
+        for (int n = tid; n < c.num_seqs; n += NT) {
             const Seq s = sequence(c, n);
             const int rows = s.len * p.G;
             if (rows >= p.rows_lo && rows <= p.rows_hi)
@@ -94,10 +96,13 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Wo
         if (lane == 0) lds.total[wave] = total;
         if (tid == 0) lds.found[0] = -1;
         __syncthreads();
-        total = (lds.total[0] + lds.total[1] + lds.total[2] + lds.total[3]) * p.Hk;
+        total = 0;
+#pragma unroll
+        for (int k = 0; k < NT / 64; ++k) total += lds.total[k];
+        total *= p.Hk;
         const int cut = (int)max((long long)p.c_min, (total + p.target - 1) / p.target);
         int parts = 0, slots = 0, stiles = 0;  // of the sequences so far
-        for (int n0 = 0; n0 < c.num_seqs; n0 += 256) {
+        for (int n0 = 0; n0 < c.num_seqs; n0 += NT) {
             const int n = n0 + tid;
             int v[3] = {0, 0, 0}, cuts = 1, tiles = 0;
             if (n < c.num_seqs) {
@@ -124,7 +129,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Wo
             }
             __syncthreads();
             int before[3] = {parts, slots, stiles};
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < NT / 64; ++k) {
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
                     if (k < wave) before[i] += lds.sums[k][i];

@@ -2,7 +2,7 @@
 
 A VALU instruction (or v_accvgpr_read / write, a memory instruction) that reads or overwrites the
 destination registers of an MFMA must come a number of wait states after it (8 after a 16x16x32
-bf16 product, 10 after a 16x16x4 f32 one: the counts the compiler itself leaves inside a basic
+bf16 product, 12 after a 32x32x16 one, 10 after a 16x16x4 f32 one: the counts the compiler itself leaves inside a basic
 block).  The compiler inserts them inside a block, but it has been seen to leave none where the read
 sits in another block reached through a join (wrong values, no fault).  This module
 walks every path of the control-flow graph from each MFMA, counting wait states (one per issued
@@ -26,11 +26,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 # Wait states an MFMA result needs before another instruction reads or overwrites it: the counts the
 # compiler itself leaves inside a basic block for the shapes used here (the 16x16x32 bf16 product is
-# a 4-pass instruction on gfx950, the 16x16x4 f32 one an 8-pass one); unknown shapes get the 16-pass
+# a 4-pass instruction on gfx950, the 32x32x16 and the 16x16x4 f32 ones 8-pass ones); unknown shapes get the 16-pass
 # count.
 def required_wait_states(op: str) -> int:
     if re.search(r"16x16x32_(bf16|f16)", op):
         return 8
+    if re.search(r"32x32x16_(bf16|f16)", op):
+        return 12
     if "16x16x4" in op:
         return 10
     return 18
