@@ -49,6 +49,18 @@ struct AppendParams {
 int64_t append_items(int64_t tokens, int32_t heads_q, int32_t heads_kv, int32_t dk, int32_t dv);
 hipError_t launch_append(bool bf16, const AppendParams &p, hipStream_t stream);
 
+// Quotients by a number that the host knows, n in 0 .. 2^31 - 1: n mul >> (31 + shift) with 2^shift >= d and
+// mul = ceil(2^(31 + shift) / d), exact as n (mul d - 2^(31 + shift)) < 2^(31 + shift).
+struct Div {
+    uint32_t mul = 0, shift = 0;
+    Div() = default;
+    explicit Div(uint32_t d) {
+        while ((1u << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << (31 + shift)) + d - 1) / d);
+    }
+    __host__ __device__ int by(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> (31 + shift)); }
+};
+
 // Attention.  A tile is M consecutive (token, head of the group) rows of one sequence and key-value head; its
 // cells are cut into blocks of KB, and rows of many blocks into splits that workgroups of their own take.
 struct AttnParams {
@@ -58,6 +70,7 @@ struct AttnParams {
     float *lse;
     int64_t ldq;
     int32_t Hq, Hk, G, dk, dv;
+    Div by_G, by_Hk;
     int32_t window;            // 0: none
     float scale;               // |scale| log2(e)
     int32_t flip;              // scale < 0: q enters negated

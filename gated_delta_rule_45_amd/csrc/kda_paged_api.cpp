@@ -115,8 +115,9 @@ kda_status_t pool_strides(const char *name, const kda_paged_problem_t *p, int64_
         if (out[i] > (1LL << 58) / size[i]) return set_error(KDA_ERR_UNSUPPORTED, "%s: pool too large", name);
         inner = out[i] * (size[i] - 1) + inner;
     }
-    if (size[2] > 1 && out[2] > 1 << 26)  // 16 cells are reached by a 32-bit offset in bytes
-        return set_error(KDA_ERR_UNSUPPORTED, "%s: cells %lld elements apart", name, (long long)out[2]);
+    if (out[2] * size[2] > 1LL << 30)  // the kernels reach a head's cells of a page by a 32-bit offset
+        return set_error(KDA_ERR_UNSUPPORTED, "%s: %lld cells, %lld elements apart: a head's cells of a page must lie within 2^30 elements",
+                         name, (long long)size[2], (long long)out[2]);
     for (int i = 0; i < 3; ++i)
         if (size[i] <= 1) out[i] = 0;
     return KDA_OK;
@@ -505,6 +506,8 @@ kda_status_t kda_paged_attn(const kda_paged_problem_t *p, const void *q, const v
         r.Hq = p->num_heads_q;
         r.Hk = p->num_heads_kv;
         r.G = s.G;
+        r.by_G = kda::paged::Div(s.G);
+        r.by_Hk = kda::paged::Div(p->num_heads_kv);
         r.dk = p->head_dim_k;
         r.dv = p->head_dim_v;
         r.window = window;

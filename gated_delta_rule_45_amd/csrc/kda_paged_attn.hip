@@ -167,11 +167,12 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(AttnParams p) {
 
     Ops<IO, DK, DV> x;
     const int row = w.row0 + min(col, w.rows - 1);  // this lane's row
-    x.load_q(static_cast<const IO *>(p.q) + (w.seq.t0 + row / p.G) * p.ldq + (w.head * p.G + row % p.G) * DK, g, col < w.rows,
+    const int token = p.by_G.by(row);
+    x.load_q(static_cast<const IO *>(p.q) + (w.seq.t0 + token) * p.ldq + (w.head * p.G + (row - token * p.G)) * DK, g, col < w.rows,
              p.flip);
-    const int pos = w.pos(row, p.G), from = w.first(pos, p.window);
+    const int pos = w.pos(row, p.by_G), from = w.first(pos, p.window);
     // cells that every row of the tile sees
-    const int all_lo = w.first(w.pos(w.row0 + w.rows - 1, p.G), p.window), all_hi = min(w.pos(w.row0, p.G) + 1, w.cells);
+    const int all_lo = w.first(w.pos(w.row0 + w.rows - 1, p.by_G), p.window), all_hi = min(w.pos(w.row0, p.by_G) + 1, w.cells);
     const bool ragged = all_lo != w.lo || all_hi != w.hi;  // rows see different cells
     const IO *kp = static_cast<const IO *>(c.k) + w.head * c.k_head, *vp = static_cast<const IO *>(c.v) + w.head * c.v_head;
     const int mask = (1 << c.page_shift) - 1;

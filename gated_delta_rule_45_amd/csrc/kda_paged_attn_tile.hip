@@ -11,14 +11,15 @@
 // lane holds the scores of row r for cells 8 a + 4 h + b of each 32, which are the contraction slots of the next product as they
 // are.  V^T comes from LDS through the transposing read (4 cells of one column per lane).  Direct global-to-LDS loads
 // place lane l's 16 bytes at 16 l, so rows are scattered over the banks by which bytes a lane fetches: 16-byte
-// pieces of keys move by row mod 8, 32-byte pieces of values (what 16 lanes read of a row) by row mod 4.
+// pieces of keys move by row mod 16 (by half of that where two rows make 256 bytes), 32-byte pieces of values, what 16
+// lanes read of a row, by row mod 4: neither then meets a bank twice in the 256 bytes that LDS gives in a cycle.
 #include "kda_paged_work.h"
 
 namespace kda {
 namespace paged {
 namespace {
 
-constexpr int kM = 256, kKB = 64, kNT = 512, kRing = 4;
+constexpr int kM = 256, kKB = 64, kNT = 512, kRing = 4, kAhead = 10;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
@@ -28,21 +29,22 @@ __device__ const u32x4 kZeros[1] = {};
 
 // Position of 16-byte piece c of row r in LDS, and back (both ways are the same exchange).
 template <int D>
-__device__ __forceinline__ int k_place(int r, int c) { return c ^ (r & 7); }
+__device__ __forceinline__ int k_place(int r, int c) { return c ^ (D == 128 ? r & 15 : (r >> 1) & 7); }
 template <int D>
 __device__ __forceinline__ int v_place(int r, int c) { return c ^ ((D == 128 ? r & 3 : (r >> 1) & 1) << 2); }
 
 // load_lds16 whose end is left to wait_vmcnt and a barrier: the compiler, which cannot tell the buffers of a ring apart, would
-// wait for the builtin's loads before every LDS read.  (M0 holds the destination and must be set a cycle before.)
+// wait for the builtin's loads before every LDS read.  `to`: the wave's address in LDS, for M0, which must be set a cycle
+// before.  Nothing here tells the compiler that LDS is written, so that it may move LDS reads of other buffers past it: the
+// barriers, which are volatile like this, keep it in its half iteration.
 __device__ __forceinline__ unsigned lds_address(const void *p) {
     return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(const __attribute__((address_space(3))) void *)p);
 }
-__device__ __forceinline__ void load_lds16_async(const void *base, unsigned offset, void *lds) {  // base: the wave's, offset: a lane's
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0" ::"s"(base), "v"(offset), "s"(lds_address(lds))
-                 : "memory");
+__device__ __forceinline__ void load_lds16_async(const void *base, unsigned offset, unsigned to) {  // base: the wave's, offset: a lane's
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0" ::"s"(base), "v"(offset), "s"(to));
 }
-__device__ __forceinline__ void load_lds16_async(const void *src, void *lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(lds_address(lds)) : "memory");
+__device__ __forceinline__ void load_lds16_async(const void *src, unsigned to) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(to));
 }
 
 template <int DK, int DV>
@@ -68,19 +70,12 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
     // this wave's rows
     const int wrow = min(wave * 32, w.rows - 1), wlast = min(wave * 32 + 31, w.rows - 1), row = w.row0 + min(wave * 32 + r, w.rows - 1);
     const bool active = wave * 32 < w.rows;
-    const int pos = w.pos(row, p.G), from = w.first(pos, p.window), last = min(pos, w.cells - 1);
-    const int pos0 = w.pos(w.row0 + wrow, p.G), pos1 = w.pos(w.row0 + wlast, p.G);
+    const int pos = w.pos(row, p.by_G), from = w.first(pos, p.window), last = min(pos, w.cells - 1);
+    const int pos0 = w.pos(w.row0 + wrow, p.by_G), pos1 = w.pos(w.row0 + wlast, p.by_G);
     const int see_lo = w.first(pos0, p.window), see_hi = active ? min(pos1 + 1, w.cells) : 0;   // some row
     const int all_lo = w.first(pos1, p.window), all_hi = min(pos0 + 1, w.cells);                // every row
-    u32x4 q[KS];
-    {
-        const uint16_t *x = static_cast<const uint16_t *>(p.q) + (w.seq.t0 + row / p.G) * p.ldq + (w.head * p.G + row % p.G) * DK;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            q[i] = *reinterpret_cast<const u32x4 *>(x + 16 * i + 8 * h);
-            if (p.flip) q[i] ^= 0x80008000u;
-        }
-    }
+    const int token = p.by_G.by(row);
+    const uint16_t *x = static_cast<const uint16_t *>(p.q) + (w.seq.t0 + token) * p.ldq + (w.head * p.G + (row - token * p.G)) * DK;
 
     // ---- staging: load i of a wave covers rows KR (wave + 8 i) .. of the block
     const char *kp = reinterpret_cast<const char *>(static_cast<const uint16_t *>(c.k) + w.head * c.k_head);
@@ -105,41 +100,42 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         const int rr = VR * i + lane / VC;
         v_off[i] = (unsigned)(rr * c.v_cell) * 2 + 16 * v_place<DV>(row8 + rr, lane % VC);
     }
-    // Loads of a wave's rows from page e; cells that are not there or out of sight are zeros.  Returns whether the page exists.
-    auto fetch = [&](auto &off, const char *pool, int64_t page, int64_t cell_ld, int e, int cell0, uint16_t *to, int rows_per_load,
-                     int elems_per_load) {
+    // Blocks t_in .. t_in + n_in - 1 of this part lie within what the tile's rows see.
+    const int t_in = (w.lo + kKB - 1) / kKB - w.b0;
+    const unsigned n_in = max(w.hi / kKB - w.b0 - t_in, 0);
+    const unsigned k_lds = lds_address(&lds.k[0][row8 * DK]), v_lds = lds_address(&lds.v[0][row8 * DV]);
+    // Loads of a wave's rows of block t from page e; cells that are not there or out of sight are zeros.
+    auto fetch = [&](auto &off, const char *pool, int64_t page, int64_t cell_ld, int e, int t, unsigned to, int rows_per_load) {
         constexpr int N = sizeof(off) / sizeof(off[0]);
+        const int cell0 = (w.b0 + t) * kKB + row8;
         const bool exists = (unsigned)e < (unsigned)c.num_pages;
-        const char *base = pool + ((int64_t)e * page + (int64_t)(cell0 & mask) * cell_ld) * 2;
-        if (exists && cell0 >= w.lo && cell0 + 8 <= w.hi) {
+        const char *base = pool + ((int64_t)e * page + (uint64_t)((unsigned)(cell0 & mask) * (unsigned)cell_ld)) * 2;
+        if (exists && (unsigned)(t - t_in) < n_in) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) load_lds16_async(base, off[i], to + i * elems_per_load);
+            for (int i = 0; i < N; ++i) load_lds16_async(base, off[i], to + 1024 * i);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int cell = cell0 + rows_per_load * i + lane / (64 / rows_per_load);
                 load_lds16_async(exists && cell >= w.lo && cell < w.hi ? base + off[i] : reinterpret_cast<const char *>(kZeros),
-                                 to + i * elems_per_load);
+                                 to + 1024 * i);
             }
         }
         return exists;
     };
     auto stage_k = [&](int t) {
-        const bool exists = fetch(k_off, kp, c.k_page, c.k_cell, ek, (w.b0 + t) * kKB + row8, &lds.k[t % kRing][row8 * DK], KR, KR * DK);
+        const bool exists = fetch(k_off, kp, c.k_page, c.k_cell, ek, t, k_lds + t % kRing * (kKB * DK * 2), KR);
         if (lane == 0) reinterpret_cast<uint8_t *>(&lds.missing[t % kRing])[wave / 2] = !exists;
     };
-    auto stage_v = [&](int t) { fetch(v_off, vp, c.v_page, c.v_cell, ev, (w.b0 + t) * kKB + row8, &lds.v[t % kRing][row8 * DV], VR, VR * DV); };
+    auto stage_v = [&](int t) { fetch(v_off, vp, c.v_page, c.v_cell, ev, t, v_lds + t % kRing * (kKB * DV * 2), VR); };
 
+    u32x4 q[KS];
     f32x16 s[2], o[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i) o[i] = f32x16(0.f);
     u32x4 pw[4];
     float m = -INFINITY, l = 0.f;
 
-    auto seen = [&](int t) {
-        const int c0 = (w.b0 + t) * kKB;
-        return c0 < see_hi && c0 + kKB > see_lo;
-    };
     auto scores = [&](int t) {  // S^T of block t
         const uint16_t *k = lds.k[t % kRing];
         s[0] = f32x16(0.f);
@@ -191,11 +187,11 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         return __any(bad);
     };
     auto settle = [&]() {
-        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+v"(s[0]), "+v"(s[1]));
+        asm volatile("s_nop 7\n\ts_nop 3" : "+v"(s[0]), "+v"(s[1]));
 #pragma unroll
         for (int i = 0; i < DB; ++i) asm volatile("" : "+v"(o[i]));
     };
-    auto weights = [&](int t, unsigned missing) {
+    auto weights = [&](int t, unsigned missing, auto &&loads) {
         if (edge(t, missing)) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -219,59 +215,102 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
             for (int b = 0; b < DB; ++b) o[b] *= f;
         }
         const float base = m == -INFINITY ? 0.f : m;
+        float sum[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            if (i < 2) loads(i);
             float e[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
                 e[y] = __builtin_amdgcn_exp2f(fmaf(s[i >> 1][8 * (i & 1) + y], p.scale, -base));
-                l += e[y];
+                sum[y & 3] = i == 0 && y < 4 ? e[y] : sum[y & 3] + e[y];
             }
 #pragma unroll
             for (int y = 0; y < 4; ++y) pw[i][y] = pack_bf16x2(e[2 * y], e[2 * y + 1]);
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
     // this wave's LDS accesses are done, its loads from memory may be on their way (a fence would wait for those too)
     auto barrier = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
-    for (int t = 0; t < 3 && t < nt; ++t) {
-        ev = ek = look(t);
-        stage_k(t);
-        if (t < 2) stage_v(t);
+    if (nt > 0) {
+        const int e0 = look(0), e1 = look(1), e2 = look(2);
+        ek = e0, stage_k(0);
+        ev = e0, stage_v(0);
+        if (nt > 1) {
+            ek = e1, stage_k(1);
+            ev = e1, stage_v(1);
+        }
+        if (nt > 2) ek = e2, stage_k(2);
+        ev = e2;  // of block 2, ek: of block 3
+        ek = look(3);
     }
-    // ev: of block 2, ek: of block 3
-    if (nt > 3) ek = look(3);
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+        q[i] = *reinterpret_cast<const u32x4 *>(x + 16 * i + 8 * h);
+        if (p.flip) q[i] ^= 0x80008000u;
+    }
     wait_vmcnt<0>();
     barrier();
     const bool second = wave >= 4;
     if (second) barrier();
-    if (nt > 0 && seen(0)) scores(0);
+    unsigned gone = lds.missing[0];
+    if (nt > 0) scores(0);
     settle();
     barrier();
     unsigned odd_blocks[2] = {0, 0};
     int odd_base[2] = {0, 0};
+    // (A wave none of whose rows sees a block goes through it all the same, with weights of 0: it has to wait for the others anyway.)
 #pragma unroll 1
     for (int t = 0; t < nt; ++t) {
-        const bool now = seen(t);
-        const unsigned missing = __builtin_amdgcn_readfirstlane(lds.missing[t % kRing]);
-        if (t + 3 < nt) stage_k(t + 3);
-        if (t + 2 < nt) stage_v(t + 2);
-        ev = ek;
-        if (t + 4 < nt) ek = look(t + 4);
-        if (now) weights(t, missing);
+        const unsigned missing = __builtin_amdgcn_readfirstlane(gone);
+        gone = lds.missing[(t + 1) % kRing];
+        // (loads take a while to leave the wave: between the weights)
+        weights(t, missing, [&](int i) {
+            if (i == 0) {
+                if (t + 3 < nt) stage_k(t + 3);
+            } else {
+                if (t + 2 < nt) stage_v(t + 2);
+                ev = ek;
+                if (t + 4 < nt) ek = look(t + 4);
+            }
+        });
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(pw[i]));  // worked out here, not between the products
+        asm volatile("" : "+v"(l));
         barrier();
-        bool whole = now;
         const int c0 = (w.b0 + t) * kKB;
-        if (now && (c0 < all_lo || c0 + kKB > all_hi) && odd(t)) {
-            // (at most two blocks at either end of a window, which spans 32 tokens at most)
-            const int side = c0 + kKB > all_hi;
-            if (!odd_blocks[side]) odd_base[side] = t;
-            odd_blocks[side] |= 1u << (t - odd_base[side]);
-            whole = false;
+        bool apart = false;
+        if ((c0 < all_lo || c0 + kKB > all_hi) && odd(t)) {
+            apart = true;
+            if (c0 < see_hi && c0 + kKB > see_lo) {  // (at most two blocks at either end of a window: 32 rows are 32 tokens at most)
+                const int side = c0 + kKB > all_hi;
+                if (!odd_blocks[side]) odd_base[side] = t;
+                odd_blocks[side] |= 1u << (t - odd_base[side]);
+            }
         }
-        if (whole) add(t);
-        if (t + 1 < nt && seen(t + 1)) scores(t + 1);
+        if (__builtin_expect(!apart, 1)) {
+            // both products in one run, each operand read from LDS kAhead reads before its product (behind the last block the
+            // scores are of whatever lies in the ring and are not looked at)
+            __builtin_amdgcn_s_setprio(1);
+            add(t);
+            scores(t + 1);
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int i = 0; i < 4 * DB; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * KS; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+        } else {
+            scores(t + 1);
+        }
         settle();
+        __builtin_amdgcn_s_setprio(0);
         // the loads that the previous half iteration started may go on; all others are there for everyone behind the barrier
         if (t + 3 < nt)
             wait_vmcnt<KI + VI>();
@@ -287,7 +326,6 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
     for (int i = 0; i < 64; ++i) {
         if (!(odd_blocks[i >> 5] >> (i & 31) & 1)) continue;
         const int c0 = (w.b0 + odd_base[i >> 5] + (i & 31)) * kKB;
-        const uint16_t *x = static_cast<const uint16_t *>(p.q) + (w.seq.t0 + row / p.G) * p.ldq + (w.head * p.G + row % p.G) * DK;
 #pragma unroll 1
         for (int k = 0; k < kKB; ++k) {
             const int cell = c0 + k, e = cell < w.hi ? table[cell >> c.page_shift] : -1;

@@ -40,7 +40,7 @@ struct Work {
     int64_t slot;             // where its sums go, if splits > 1
     int cells, lo, hi;        // cells that exist; those that some row of the tile sees
     int b0, b1;               // blocks of KB cells of this part
-    __device__ __forceinline__ int pos(int row, int G) const { return seq.kv - seq.len + row / G; }
+    __device__ __forceinline__ int pos(int row, const Div &by_G) const { return seq.kv - seq.len + by_G.by(row); }
     // (a position of -len .. 2^31 - 1: no overflow)
     __device__ __forceinline__ int first(int pos, int window) const {
         return window > 0 && pos >= window ? pos - window + 1 : 0;
@@ -51,20 +51,29 @@ struct Work {
 __device__ __forceinline__ int blocks_bound(const AttnParams &p, const Seq &s, int M, int KB, int cells) {
     const int all = (min(s.kv, cells) + KB - 1) / KB;
     if (p.window <= 0) return all;
-    const int64_t seen = (int64_t)p.window + (M - 1) / p.G + 1;  // by all tokens of a tile, from some cell of a block
+    const int64_t seen = (int64_t)p.window + p.by_G.by(M - 1) + 1;  // by all tokens of a tile, from some cell of a block
     return (int)min((int64_t)all, (seen + KB - 1) / KB + 1);
 }
 
-template <typename T>
-__device__ __forceinline__ T wave_sum(T x) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
+// Inclusive prefix sum over a wave: rows of 16 lanes, then each row's last lane to the next rows.
+__device__ __forceinline__ int wave_scan(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
     return x;
+}
+// ceil(a / b) of non-negative numbers; most sums fit 32 bits, whose division is a tenth of the other's
+__device__ __forceinline__ long long ceil_div(long long a, int b) {
+    a += b - 1;
+    return a >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
 
 constexpr int kPlanWaves = 8;  // at most
 struct PlanLds {
-    long long total[kPlanWaves];
+    unsigned long long total;
     int sums[kPlanWaves][3];
     int found[6];  // sequence, part within it, splits, first slot, first split tile, split tiles in all
 };
@@ -74,8 +83,8 @@ template <int NT>
 __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Work &w, PlanLds &lds) {
     const Cache &c = p.c;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int part = blockIdx.x / (unsigned)p.Hk;
-    w.head = blockIdx.x % (unsigned)p.Hk;
+    const int part = p.by_Hk.by(blockIdx.x);
+    w.head = blockIdx.x - part * p.Hk;
     w.cells = c.num_pages > 0 ? c.max_pages << c.page_shift : 0;
     int at, splits, slot0 = 0, tile0 = 0;  // part of its sequence
     if (p.c_min == 0) {
@@ -85,46 +94,44 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Wo
         splits = 1;
         if (w.n >= c.num_seqs) return false;
     } else {
-        long long total = 0;
-        for (int n = tid; n < c.num_seqs; n += NT) {
-            const Seq s = sequence(c, n);
-            const int rows = s.len * p.G;
-            if (rows >= p.rows_lo && rows <= p.rows_hi)
-                total += (long long)((rows + M - 1) / M) * blocks_bound(p, s, M, KB, w.cells);
-        }
-        total = wave_sum(total);
-        if (lane == 0) lds.total[wave] = total;
-        if (tid == 0) lds.found[0] = -1;
-        __syncthreads();
-        total = 0;
-#pragma unroll
-        for (int k = 0; k < NT / 64; ++k) total += lds.total[k];
-        total *= p.Hk;
-        const int cut = (int)max((long long)p.c_min, (total + p.target - 1) / p.target);
-        int parts = 0, slots = 0, stiles = 0;  // of the sequences so far
-        for (int n0 = 0; n0 < c.num_seqs; n0 += NT) {
-            const int n = n0 + tid;
-            int v[3] = {0, 0, 0}, cuts = 1, tiles = 0;
+        struct Share {
+            int rows = 0, blocks = 0;  // of a sequence, rows 0: none of this launch
+        };
+        auto share = [&](int n) {
+            Share x;
             if (n < c.num_seqs) {
                 const Seq s = sequence(c, n);
                 const int rows = s.len * p.G;
                 if (rows >= p.rows_lo && rows <= p.rows_hi) {
-                    tiles = (rows + M - 1) / M;
-                    cuts = max(1, (blocks_bound(p, s, M, KB, w.cells) + cut - 1) / cut);
-                    v[0] = tiles * cuts;
-                    v[1] = cuts > 1 ? v[0] : 0;
-                    v[2] = cuts > 1 ? tiles : 0;
+                    x.rows = rows;
+                    x.blocks = blocks_bound(p, s, M, KB, w.cells);
                 }
             }
+            return x;
+        };
+        if (tid == 0) {
+            lds.total = 0;
+            lds.found[0] = -1;
+        }
+        const Share mine0 = share(tid);
+        unsigned long long cost = (unsigned long long)((mine0.rows + M - 1) / M) * mine0.blocks;
+        for (int n = tid + NT; n < c.num_seqs; n += NT) {
+            const Share x = share(n);
+            cost += (unsigned long long)((x.rows + M - 1) / M) * x.blocks;
+        }
+        __syncthreads();
+        if (cost) atomicAdd(&lds.total, cost);
+        __syncthreads();
+        const int cut = (int)max((long long)p.c_min, ceil_div((long long)lds.total * p.Hk, p.target));
+        int parts = 0, slots = 0, stiles = 0;  // of the sequences so far
+        for (int n0 = 0; n0 < c.num_seqs; n0 += NT) {
+            const Share x = n0 == 0 ? mine0 : share(n0 + tid);
+            const int tiles = (x.rows + M - 1) / M, cuts = x.blocks > cut ? (int)((unsigned)(x.blocks + cut - 1) / (unsigned)cut) : 1;
+            const int v[3] = {tiles * cuts, cuts > 1 ? tiles * cuts : 0, cuts > 1 ? tiles : 0};
             int sum[3];
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-                sum[i] = v[i];
-#pragma unroll
-                for (int m = 1; m < 64; m <<= 1) {
-                    const int y = __shfl_up(sum[i], m, 64);
-                    if (lane >= m) sum[i] += y;
-                }
+                sum[i] = wave_scan(v[i]);
                 if (lane == 63) lds.sums[wave][i] = sum[i];
             }
             __syncthreads();
@@ -139,7 +146,7 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Wo
             }
             const int mine = part - (before[0] + sum[0] - v[0]);
             if (mine >= 0 && mine < v[0]) {
-                lds.found[0] = n;
+                lds.found[0] = n0 + tid;
                 lds.found[1] = mine;
                 lds.found[2] = cuts;
                 lds.found[3] = before[1] + sum[1] - v[1];
@@ -162,12 +169,12 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Wo
     const int rows = w.seq.len * p.G;
     if (rows < p.rows_lo || rows > p.rows_hi) return false;
     // the last tiles see the most cells: first
-    const int tiles = (rows + M - 1) / M, x = at / splits;
-    w.split = at % splits;
+    const int tiles = (rows + M - 1) / M, x = splits > 1 ? at / splits : at;
+    w.split = at - x * splits;
     w.row0 = (tiles - 1 - x) * M;
     w.rows = min(M, rows - w.row0);
-    w.hi = min(w.pos(w.row0 + w.rows - 1, p.G) + 1, w.cells);
-    w.lo = w.first(w.pos(w.row0, p.G), p.window);
+    w.hi = min(w.pos(w.row0 + w.rows - 1, p.by_G) + 1, w.cells);
+    w.lo = w.first(w.pos(w.row0, p.by_G), p.window);
     const int first = w.lo / KB, nb = w.hi > w.lo ? (w.hi + KB - 1) / KB - first : 0;
     w.splits = 1;
     if (splits > 1) {
@@ -196,7 +203,8 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Wo
 
 // Row r of a sequence: its token and head, as an offset in rows of the output.
 __device__ __forceinline__ int64_t out_row(const AttnParams &p, const Seq &s, int head, int row) {
-    return (s.t0 + row / p.G) * p.Hq + head * p.G + row % p.G;
+    const int t = p.by_G.by(row);
+    return (s.t0 + t) * p.Hq + head * p.G + (row - t * p.G);
 }
 
 // What a workgroup found for its rows, 16 threads a row (thread tid: row tid / 16, columns VW (tid % 16) ..): the
