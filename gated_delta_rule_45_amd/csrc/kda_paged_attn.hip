@@ -53,12 +53,13 @@ struct Ops<uint16_t, DK, DV> {
             if (flip) q[i] ^= 0x80008000u;
         }
     }
-    __device__ __forceinline__ void load_k(int s, const uint16_t *row, int g) {
+    // (base: the wave's, offset: a lane's, in 32 bits)
+    __device__ __forceinline__ void load_k(int s, const char *base, unsigned offset) {
 #pragma unroll
-        for (int i = 0; i < KK; ++i) k[s][i] = *reinterpret_cast<const u32x4 *>(row + 32 * i + 8 * g);
+        for (int i = 0; i < KK; ++i) k[s][i] = *reinterpret_cast<const u32x4 *>(base + offset + 64 * i);
     }
-    __device__ __forceinline__ void load_v(int j, const uint16_t *row, int c) {
-        v[j] = *reinterpret_cast<const Row *>(row + VW * c);
+    __device__ __forceinline__ void load_v(int j, const char *base, unsigned offset) {
+        v[j] = *reinterpret_cast<const Row *>(base + offset);
     }
     __device__ __forceinline__ void clear_v(int j) { v[j] = Row(0u); }
     __device__ __forceinline__ bool odd_v(int j) const {  // infinities or NaN among them
@@ -101,13 +102,13 @@ struct Ops<float, DK, DV> {
             if (flip) q[i] = -q[i];
         }
     }
-    __device__ __forceinline__ void load_k(int s, const float *row, int g) {
+    __device__ __forceinline__ void load_k(int s, const char *base, unsigned offset) {
 #pragma unroll
-        for (int i = 0; i < KK; ++i) k[s][i] = *reinterpret_cast<const f32x4 *>(row + 16 * i + 4 * g);
+        for (int i = 0; i < KK; ++i) k[s][i] = *reinterpret_cast<const f32x4 *>(base + offset + 64 * i);
     }
-    __device__ __forceinline__ void load_v(int j, const float *row, int c) {
+    __device__ __forceinline__ void load_v(int j, const char *base, unsigned offset) {
 #pragma unroll
-        for (int i = 0; i < VW / 4; ++i) v[j][i] = *reinterpret_cast<const f32x4 *>(row + VW * c + 4 * i);
+        for (int i = 0; i < VW / 4; ++i) v[j][i] = *reinterpret_cast<const f32x4 *>(base + offset + 16 * i);
     }
     __device__ __forceinline__ void clear_v(int j) {
 #pragma unroll
@@ -151,7 +152,7 @@ struct Pages {
 };
 
 template <typename IO, int DK, int DV>
-__global__ void __launch_bounds__(256) attn_rows_kernel(AttnParams p) {
+__global__ void __launch_bounds__(256, sizeof(IO) == 2 ? 3 : DK + DV == 256 ? 1 : 2) attn_rows_kernel(AttnParams p) {
     constexpr int VW = DV / 16, PAD = DV + 4;
     __shared__ union {
         PlanLds plan;
@@ -168,27 +169,31 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(AttnParams p) {
     Ops<IO, DK, DV> x;
     const int row = w.row0 + min(col, w.rows - 1);  // this lane's row
     const int token = p.by_G.by(row);
-    x.load_q(static_cast<const IO *>(p.q) + (w.seq.t0 + token) * p.ldq + (w.head * p.G + (row - token * p.G)) * DK, g, col < w.rows,
-             p.flip);
+    const IO *q = static_cast<const IO *>(p.q) + (w.seq.t0 + token) * p.ldq + (w.head * p.G + (row - token * p.G)) * DK;
+    x.load_q(q, g, col < w.rows, p.flip);
     const int pos = w.pos(row, p.by_G), from = w.first(pos, p.window);
     // cells that every row of the tile sees
     const int all_lo = w.first(w.pos(w.row0 + w.rows - 1, p.by_G), p.window), all_hi = min(w.pos(w.row0, p.by_G) + 1, w.cells);
     const bool ragged = all_lo != w.lo || all_hi != w.hi;  // rows see different cells
-    const IO *kp = static_cast<const IO *>(c.k) + w.head * c.k_head, *vp = static_cast<const IO *>(c.v) + w.head * c.v_head;
+    const char *kp = reinterpret_cast<const char *>(static_cast<const IO *>(c.k) + w.head * c.k_head);
+    const char *vp = reinterpret_cast<const char *>(static_cast<const IO *>(c.v) + w.head * c.v_head);
+    const unsigned k_cell = (unsigned)c.k_cell * sizeof(IO), v_cell = (unsigned)c.v_cell * sizeof(IO);  // bytes
+    const unsigned k_off = col * k_cell + 16 * g, v_off = 4 * g * v_cell + VW * sizeof(IO) * col;        // a lane's
     const int mask = (1 << c.page_shift) - 1;
 
     f32x4 o[VW];
 #pragma unroll
     for (int i = 0; i < VW; ++i) o[i] = zero4();
     float m = -INFINITY, l = 0.f;
+    OddBlocks odd_blocks;
 
     Pages pages;
     auto load_k = [&](int i, int b) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int page = pages.get(2 * i + s), cell = b * kKB + 32 * wave + 16 * s;
-            const int64_t at = page < 0 ? 0 : page * c.k_page + (cell & mask) * c.k_cell;
-            x.load_k(s, kp + at + col * c.k_cell, g);
+            const char *at = page < 0 ? kp : kp + page * c.k_page * (int64_t)sizeof(IO) + (uint64_t)((unsigned)(cell & mask) * k_cell);
+            x.load_k(s, at, k_off);
         }
     };
     pages.refill(c, w.n, w.b0, wave, lane, w.hi, w.b1);
@@ -200,9 +205,10 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(AttnParams p) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int page = s ? page1 : page0;
-            const int64_t at = page < 0 ? 0 : page * c.v_page + ((cell0 + 16 * s) & mask) * c.v_cell;
+            const char *at =
+                page < 0 ? vp : vp + page * c.v_page * (int64_t)sizeof(IO) + (uint64_t)((unsigned)((cell0 + 16 * s) & mask) * v_cell);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x.load_v(4 * s + j, vp + at + (4 * g + j) * c.v_cell, col);
+            for (int j = 0; j < 4; ++j) x.load_v(4 * s + j, at, v_off + j * v_cell);
         }
         f32x4 s0 = x.scores(0), s1 = x.scores(1);
         mfma_settle(s0, s1);
@@ -239,26 +245,36 @@ __global__ void __launch_bounds__(256) attn_rows_kernel(AttnParams p) {
             l += e[j];
         }
         if (__builtin_expect(edge && __any(odd), 0)) {
-            // infinities or NaN in cells that some rows see and others do not: a weight of 0 does not hide them, so
-            // each row adds only the cells that it sees
-#pragma unroll 1
-            for (int k = 0; k < 32; ++k) {
-                const int j = (k >> 4) * 4 + (k & 3), cell = cell0 + k, page = k < 16 ? page0 : page1;
-                float mine = e[0];
-#pragma unroll
-                for (int y = 1; y < 8; ++y) mine = j == y ? e[y] : mine;
-                const float weight = __shfl(mine, ((k & 15) >> 2) * 16 + col, 64);
-                if (page < 0 || cell > pos || cell < from || cell >= w.cells) continue;
-                const IO *v = vp + page * c.v_page + (cell & mask) * c.v_cell;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int y = 0; y < VW; ++y) o[y][r] = fmaf(weight, IoTraits<IO>::load1(v + VW * (4 * g + r) + y), o[y][r]);
-            }
+            const int side = cell0 + 32 > all_hi;  // (at most two blocks at either end of a window: 16 rows are 16 tokens at most)
+            odd_blocks.add(side, b);
         } else {
             x.add(o, e);
         }
         settle(o);
+    }
+
+    // Blocks with infinities or NaN in cells that some rows see and others do not: a weight of 0 does not hide them, so each row
+    // adds only the cells that it sees, from memory.
+#pragma unroll 1
+    for (int i = 0; i < OddBlocks::kMost; ++i) {
+        const int odd_block = odd_blocks.get(i);
+        if (odd_block < 0) continue;
+        const int cell0 = odd_block * kKB + 32 * wave;
+#pragma unroll 1
+        for (int cell = cell0; cell < cell0 + 32; ++cell) {
+            const int page = cell < w.hi ? c.table[w.n * c.table_ld + (cell >> c.page_shift)] : -1;
+            if (page < 0 || page >= c.num_pages || cell > pos || cell < from) continue;
+            const IO *kr = reinterpret_cast<const IO *>(kp) + page * c.k_page + (cell & mask) * c.k_cell;
+            const IO *vr = reinterpret_cast<const IO *>(vp) + page * c.v_page + (cell & mask) * c.v_cell;
+            float z = 0.f;
+#pragma unroll 1
+            for (int j = 0; j < DK; ++j) z = fmaf(IoTraits<IO>::load1(q + j), IoTraits<IO>::load1(kr + j), z);
+            const float weight = __builtin_amdgcn_exp2f(fmaf(p.flip ? -z : z, p.scale, -m));
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int y = 0; y < VW; ++y) o[y][r] = fmaf(weight, IoTraits<IO>::load1(vr + VW * (4 * g + r) + y), o[y][r]);
+        }
     }
 
     l += __shfl_xor(l, 16, 64);
@@ -385,7 +401,7 @@ hipError_t join(const AttnParams &p, int M, int64_t tiles, hipStream_t s) {
 }  // namespace
 
 // c_min: two blocks, 256 cells, below which joining costs more than it gains
-AttnTile attn_rows_tile(bool) { return {kM, kKB, 2, 4}; }
+AttnTile attn_rows_tile(bool) { return {kM, kKB, 2, 3}; }
 
 hipError_t launch_attn_rows(bool bf16, const AttnParams &p, int64_t blocks, hipStream_t stream) {
     if (blocks <= 0) return hipSuccess;

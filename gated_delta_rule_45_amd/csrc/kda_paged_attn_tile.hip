@@ -24,9 +24,6 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
 
-// what lanes read in place of cells that do not exist or that no row of the tile sees
-__device__ const u32x4 kZeros[1] = {};
-
 // Position of 16-byte piece c of row r in LDS, and back (both ways are the same exchange).
 template <int D>
 __device__ __forceinline__ int k_place(int r, int c) { return c ^ (D == 128 ? r & 15 : (r >> 1) & 7); }
@@ -42,9 +39,6 @@ __device__ __forceinline__ unsigned lds_address(const void *p) {
 }
 __device__ __forceinline__ void load_lds16_async(const void *base, unsigned offset, unsigned to) {  // base: the wave's, offset: a lane's
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %0" ::"s"(base), "v"(offset), "s"(to));
-}
-__device__ __forceinline__ void load_lds16_async(const void *src, unsigned to) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "s"(to));
 }
 
 template <int DK, int DV>
@@ -87,8 +81,8 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
     // A wave loads rows 8 wave .. 8 wave + 7 of every block, of keys and of values: one page.  ek, ev: table entries of
     // the next blocks' loads, read an iteration ahead.
     const int row8 = 8 * wave;
-    int ek = -1, ev = -1;
-    auto look = [&](int t) { return table[min((w.b0 + t) * kKB + row8, w.hi - 1) >> c.page_shift]; };
+    int ek = -1, ev = -1, e1 = -1;  // of the next keys, the next values, the values before those
+    auto look = [&](int t) { return table[min((unsigned)(w.b0 + t) * kKB + row8, (unsigned)w.hi - 1) >> c.page_shift]; };
     unsigned k_off[KI], v_off[VI];  // bytes of a lane's piece from the wave's first cell
 #pragma unroll
     for (int i = 0; i < KI; ++i) {
@@ -100,34 +94,35 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         const int rr = VR * i + lane / VC;
         v_off[i] = (unsigned)(rr * c.v_cell) * 2 + 16 * v_place<DV>(row8 + rr, lane % VC);
     }
-    // Blocks t_in .. t_in + n_in - 1 of this part lie within what the tile's rows see.
-    const int t_in = (w.lo + kKB - 1) / kKB - w.b0;
-    const unsigned n_in = max(w.hi / kKB - w.b0 - t_in, 0);
     const unsigned k_lds = lds_address(&lds.k[0][row8 * DK]), v_lds = lds_address(&lds.v[0][row8 * DV]);
-    // Loads of a wave's rows of block t from page e; cells that are not there or out of sight are zeros.
-    auto fetch = [&](auto &off, const char *pool, int64_t page, int64_t cell_ld, int e, int t, unsigned to, int rows_per_load) {
+    const int64_t k_page = c.k_page * 2, v_page = c.v_page * 2;  // bytes
+    const unsigned k_cell = (unsigned)c.k_cell * 2, v_cell = (unsigned)c.v_cell * 2;
+    // Loads of a wave's rows of block t from page e.  No branch and no address of a lane's own: where the page does not exist they read
+    // page 0, behind the last cell what the last page holds there.  Scores of such cells are replaced; values are cleared.
+    auto fetch = [&](auto &off, const char *pool, int64_t page, unsigned cell_bytes, int e, int t, unsigned to) {
         constexpr int N = sizeof(off) / sizeof(off[0]);
-        const int cell0 = (w.b0 + t) * kKB + row8;
-        const bool exists = (unsigned)e < (unsigned)c.num_pages;
-        const char *base = pool + ((int64_t)e * page + (uint64_t)((unsigned)(cell0 & mask) * (unsigned)cell_ld)) * 2;
-        if (exists && (unsigned)(t - t_in) < n_in) {
+        const char *base = pool + (int64_t)((unsigned)e < (unsigned)c.num_pages ? e : 0) * page +
+                           (uint64_t)(((unsigned)((w.b0 + t) * kKB + row8) & mask) * cell_bytes);
 #pragma unroll
-            for (int i = 0; i < N; ++i) load_lds16_async(base, off[i], to + 1024 * i);
-        } else {
+        for (int i = 0; i < N; ++i) load_lds16_async(base, off[i], to + 1024 * i);
+    };
+    auto stage_k = [&](int t) { fetch(k_off, kp, k_page, k_cell, ek, t, k_lds + t % kRing * (kKB * DK * 2)); };
+    auto stage_v = [&](int t) { fetch(v_off, vp, v_page, v_cell, ev, t, v_lds + t % kRing * (kKB * DV * 2)); };
+    auto mark = [&](int t) {
+        if (lane == 0)
+            reinterpret_cast<uint8_t *>(&lds.missing[t % kRing])[wave / 2] = (unsigned)ek >= (unsigned)c.num_pages;
+    };
+    // Zeros over the values of this wave's cells of block t (page e) that are not there or out of every row's sight: a weight of 0
+    // would not hide what lies there.
+    auto clear = [&](int t, int e) {
+        const unsigned cell0 = (unsigned)(w.b0 + t) * kKB + row8;
+        if ((unsigned)e < (unsigned)c.num_pages && cell0 >= (unsigned)w.lo && cell0 + 8 <= (unsigned)w.hi) return;
+        const unsigned seen = (unsigned)e < (unsigned)c.num_pages ? w.hi - w.lo : 0;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int cell = cell0 + rows_per_load * i + lane / (64 / rows_per_load);
-                load_lds16_async(exists && cell >= w.lo && cell < w.hi ? base + off[i] : reinterpret_cast<const char *>(kZeros),
-                                 to + 1024 * i);
-            }
-        }
-        return exists;
+        for (int i = 0; i < VI; ++i)
+            if (cell0 + VR * i + lane / VC - w.lo >= seen)
+                *reinterpret_cast<u32x4 *>(&lds.v[t % kRing][row8 * DV + 512 * i + 8 * lane]) = u32x4{0, 0, 0, 0};
     };
-    auto stage_k = [&](int t) {
-        const bool exists = fetch(k_off, kp, c.k_page, c.k_cell, ek, t, k_lds + t % kRing * (kKB * DK * 2), KR);
-        if (lane == 0) reinterpret_cast<uint8_t *>(&lds.missing[t % kRing])[wave / 2] = !exists;
-    };
-    auto stage_v = [&](int t) { fetch(v_off, vp, c.v_page, c.v_cell, ev, t, v_lds + t % kRing * (kKB * DV * 2), VR); };
 
     u32x4 q[KS];
     f32x16 s[2], o[DB];
@@ -191,15 +186,22 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
 #pragma unroll
         for (int i = 0; i < DB; ++i) asm volatile("" : "+v"(o[i]));
     };
-    auto weights = [&](int t, unsigned missing, auto &&loads) {
+    auto weights = [&](int t, unsigned missing) {
         if (edge(t, missing)) {
+            const int c0 = (w.b0 + t) * kKB + 4 * h, to = last - c0, at = from - c0;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int y = 0; y < 16; ++y) {
-                    const int k = 32 * b + 8 * (y >> 2) + 4 * h + (y & 3), cell = (w.b0 + t) * kKB + k;
-                    if (cell > last || cell < from || (missing >> (8 * (2 * b + (y >> 3))) & 0xff)) s[b][y] = -INFINITY;
+                    const int k = 32 * b + 8 * (y >> 2) + (y & 3);
+                    const bool see = (k <= to) & (k >= at);
+                    s[b][y] = see ? s[b][y] : -INFINITY;
                 }
+            if (missing)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) s[b][y] = missing >> (8 * (2 * b + (y >> 3))) & 0xff ? -INFINITY : s[b][y];
         }
         float top = fmaxf(s[0][0], s[1][0]);
 #pragma unroll
@@ -218,7 +220,6 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         float sum[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (i < 2) loads(i);
             float e[8];
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
@@ -234,14 +235,15 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
     auto barrier = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
     if (nt > 0) {
-        const int e0 = look(0), e1 = look(1), e2 = look(2);
-        ek = e0, stage_k(0);
+        const int e0 = look(0), e2 = look(2);
+        e1 = look(1);
+        ek = e0, stage_k(0), mark(0);
         ev = e0, stage_v(0);
-        if (nt > 1) {
-            ek = e1, stage_k(1);
-            ev = e1, stage_v(1);
-        }
-        if (nt > 2) ek = e2, stage_k(2);
+        ek = e1, stage_k(1), mark(1);
+        ev = e1, stage_v(1);
+        ek = e2, stage_k(2), mark(2);
+        wait_vmcnt<0>();
+        clear(0, e0);
         ev = e2;  // of block 2, ek: of block 3
         ek = look(3);
     }
@@ -250,7 +252,6 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         q[i] = *reinterpret_cast<const u32x4 *>(x + 16 * i + 8 * h);
         if (p.flip) q[i] ^= 0x80008000u;
     }
-    wait_vmcnt<0>();
     barrier();
     const bool second = wave >= 4;
     if (second) barrier();
@@ -258,23 +259,16 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
     if (nt > 0) scores(0);
     settle();
     barrier();
-    unsigned odd_blocks[2] = {0, 0};
-    int odd_base[2] = {0, 0};
+    OddBlocks odd_blocks;
     // (A wave none of whose rows sees a block goes through it all the same, with weights of 0: it has to wait for the others anyway.)
 #pragma unroll 1
     for (int t = 0; t < nt; ++t) {
         const unsigned missing = __builtin_amdgcn_readfirstlane(gone);
         gone = lds.missing[(t + 1) % kRing];
-        // (loads take a while to leave the wave: between the weights)
-        weights(t, missing, [&](int i) {
-            if (i == 0) {
-                if (t + 3 < nt) stage_k(t + 3);
-            } else {
-                if (t + 2 < nt) stage_v(t + 2);
-                ev = ek;
-                if (t + 4 < nt) ek = look(t + 4);
-            }
-        });
+        stage_k(t + 3);
+        mark(t + 3);
+        stage_v(t + 2);
+        weights(t, missing);
 #pragma unroll
         for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(pw[i]));  // worked out here, not between the products
         asm volatile("" : "+v"(l));
@@ -284,9 +278,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         if ((c0 < all_lo || c0 + kKB > all_hi) && odd(t)) {
             apart = true;
             if (c0 < see_hi && c0 + kKB > see_lo) {  // (at most two blocks at either end of a window: 32 rows are 32 tokens at most)
-                const int side = c0 + kKB > all_hi;
-                if (!odd_blocks[side]) odd_base[side] = t;
-                odd_blocks[side] |= 1u << (t - odd_base[side]);
+                odd_blocks.add(c0 + kKB > all_hi, t);
             }
         }
         if (__builtin_expect(!apart, 1)) {
@@ -311,21 +303,24 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         }
         settle();
         __builtin_amdgcn_s_setprio(0);
-        // the loads that the previous half iteration started may go on; all others are there for everyone behind the barrier
-        if (t + 3 < nt)
-            wait_vmcnt<KI + VI>();
-        else
-            wait_vmcnt<0>();
+        // the loads that this half iteration started may go on; all others are there for everyone behind the barrier
+        wait_vmcnt<KI + VI>();
+        clear(t + 1, e1);
+        e1 = ev;
+        ev = ek;
+        ek = look(t + 4);
         barrier();
     }
+    wait_vmcnt<0>();
     if (!second) barrier();
 
     // Blocks with infinities or NaN in cells that some rows see and others do not: a weight of 0 does not hide them, so each row
     // adds only the cells that it sees, from memory.
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i) {
-        if (!(odd_blocks[i >> 5] >> (i & 31) & 1)) continue;
-        const int c0 = (w.b0 + odd_base[i >> 5] + (i & 31)) * kKB;
+    for (int i = 0; i < OddBlocks::kMost; ++i) {
+        const int odd_block = odd_blocks.get(i);
+        if (odd_block < 0) continue;
+        const int c0 = (w.b0 + odd_block) * kKB;
 #pragma unroll 1
         for (int k = 0; k < kKB; ++k) {
             const int cell = c0 + k, e = cell < w.hi ? table[cell >> c.page_shift] : -1;

@@ -201,6 +201,23 @@ __device__ __forceinline__ bool find_work(const AttnParams &p, int M, int KB, Wo
     return true;
 }
 
+// Blocks that a wave puts off: those at the start and at the end of what its rows see that hold infinities or NaN where some
+// rows see and others do not.  A wave's rows are 32 tokens at most, so each end is two blocks at most.
+struct OddBlocks {
+    static constexpr int kMost = 4;
+    int start0 = -1, start1 = -1, end0 = -1, end1 = -1;
+    __device__ __forceinline__ void add(bool end, int b) {
+        if (end) {
+            end1 = end0 < 0 ? end1 : b;
+            end0 = end0 < 0 ? b : end0;
+        } else {
+            start1 = start0 < 0 ? start1 : b;
+            start0 = start0 < 0 ? b : start0;
+        }
+    }
+    __device__ __forceinline__ int get(int i) const { return i == 0 ? start0 : i == 1 ? start1 : i == 2 ? end0 : end1; }
+};
+
 // Row r of a sequence: its token and head, as an offset in rows of the output.
 __device__ __forceinline__ int64_t out_row(const AttnParams &p, const Seq &s, int head, int row) {
     const int t = p.by_G.by(row);
