@@ -59,7 +59,7 @@ struct Ops<uint16_t, DK, DV> {
         for (int i = 0; i < KK; ++i) k[s][i] = *reinterpret_cast<const u32x4 *>(base + offset + 64 * i);
     }
     __device__ __forceinline__ void load_v(int j, const char *base, unsigned offset) {
-        v[j] = *reinterpret_cast<const Row *>(base + offset);
+        v[j] = __builtin_nontemporal_load(reinterpret_cast<const Row *>(base + offset));
     }
     __device__ __forceinline__ void clear_v(int j) { v[j] = Row(0u); }
     __device__ __forceinline__ bool odd_v(int j) const {  // infinities or NaN among them
@@ -401,7 +401,7 @@ hipError_t join(const AttnParams &p, int M, int64_t tiles, hipStream_t s) {
 }  // namespace
 
 // c_min: two blocks, 256 cells, below which joining costs more than it gains
-AttnTile attn_rows_tile(bool) { return {kM, kKB, 2, 3}; }
+AttnTile attn_rows_tile(bool) { return {kM, kKB, 2, 2}; }
 
 hipError_t launch_attn_rows(bool bf16, const AttnParams &p, int64_t blocks, hipStream_t stream) {
     if (blocks <= 0) return hipSuccess;
