@@ -149,9 +149,9 @@ kda_status_t check_shape(const kda_paged_problem_t *p, bool packed, Shape &s) {
     if (p->page_size < 1) return set_error(KDA_ERR_INVALID_ARGUMENT, "page_size %d < 1", p->page_size);
     if (p->page_size < 16 || (p->page_size & (p->page_size - 1)) != 0)
         return set_error(KDA_ERR_UNSUPPORTED, "page_size %d: supported are powers of two from 16 on", p->page_size);
-    if (p->max_pages < 0 || (int64_t)p->max_pages * p->page_size > 0x7fffffffLL)
-        return set_error(KDA_ERR_INVALID_ARGUMENT, "max_pages %d of %d cells: at most 2^31 - 1 cells a sequence", p->max_pages,
-                         p->page_size);
+    if (p->max_pages < 0) return set_error(KDA_ERR_INVALID_ARGUMENT, "max_pages %d < 0", p->max_pages);
+    if ((int64_t)p->max_pages * p->page_size > 1LL << 30)
+        return set_error(KDA_ERR_UNSUPPORTED, "max_pages %d of %d cells: at most 2^30 cells a sequence", p->max_pages, p->page_size);
     if (p->num_pages < 0 || p->num_pages > 0x7fffffffLL)
         return set_error(KDA_ERR_INVALID_ARGUMENT, "num_pages %lld out of range", (long long)p->num_pages);
     if (packed) {
@@ -513,7 +513,7 @@ kda_status_t kda_paged_attn(const kda_paged_problem_t *p, const void *q, const v
         r.window = window;
         // the kernels multiply by |scale|, never by 0: a masked score of -inf stays what it is (scores of finite inputs
         // times the least normal number are 0 beside any weight's rounding)
-        r.scale = std::max(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f);
+        r.scale = std::min(std::max(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f), 3.40282347e38f);
         r.flip = std::signbit(scale);
         const bool bf16 = p->io_dtype == KDA_BF16;
         hipStream_t hs = static_cast<hipStream_t>(stream);

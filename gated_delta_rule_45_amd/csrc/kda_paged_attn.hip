@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(256, sizeof(IO) == 2 ? 3 : DK + DV == 256 ? 1 
         if (i == 31) pages.refill(c, w.n, b + 1, wave, lane, w.hi, w.b1);
         if (b + 1 < w.b1) load_k(i + 1, b + 1);
         const bool edge = page0 < 0 || page1 < 0 || cell0 < all_lo || cell0 + 32 > all_hi;
+        const bool part = ragged && (cell0 < all_lo || cell0 + 32 > all_hi);  // some rows see what others do not
         bool odd = false;
         if (edge) {
 #pragma unroll
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(256, sizeof(IO) == 2 ? 3 : DK + DV == 256 ? 1 
                 const bool there = (j < 4 ? page0 : page1) >= 0 && cell < w.cells;
                 if (!there || cell > pos || cell < from) (j < 4 ? s0 : s1)[j & 3] = -INFINITY;
                 if (!there || cell >= w.hi || cell < w.lo) x.clear_v(j);
-                if (ragged) odd |= x.odd_v(j);
+                if (part) odd |= x.odd_v(j);
             }
         }
         float t = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])), fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(256, sizeof(IO) == 2 ? 3 : DK + DV == 256 ? 1 
             e[j] = __builtin_amdgcn_exp2f(fmaf(j < 4 ? s0[j & 3] : s1[j & 3], p.scale, -base));
             l += e[j];
         }
-        if (__builtin_expect(edge && __any(odd), 0)) {
+        if (__builtin_expect(part && __any(odd), 0)) {
             const int side = cell0 + 32 > all_hi;  // (at most two blocks at either end of a window: 16 rows are 16 tokens at most)
             odd_blocks.add(side, b);
         } else {

@@ -574,12 +574,13 @@ typedef struct {
     int32_t head_dim_v;    /* 64 or 128 */
     int32_t io_dtype;      /* kda_dtype_t of q, k, v, out and the pages */
     int32_t page_size;     /* cells of a page: a power of two, at least 16 */
-    int32_t max_pages;     /* entries of a sequence in block_table; max_pages * page_size < 2^31 */
+    int32_t max_pages;     /* entries of a sequence in block_table; at most 2^30 cells */
     int64_t num_pages;     /* pages in the pools (below 2^31) */
     int64_t stride_table;  /* entries from one sequence to the next in block_table (0: max_pages) */
     int64_t stride_q, stride_k, stride_v;                     /* as in kda_gdn_problem_t */
-    int64_t k_page_stride, k_head_stride, k_cell_stride;      /* elements, multiples of 16 bytes; all three 0: */
-    int64_t v_page_stride, v_head_stride, v_cell_stride;      /* dense [num_pages, Hkv, page_size, d] */
+    int64_t k_page_stride, k_head_stride, k_cell_stride;      /* elements, multiples of 16 bytes; all three 0: dense */
+    int64_t v_page_stride, v_head_stride, v_cell_stride;      /* [num_pages, Hkv, page_size, d].  No two cells share */
+                                                              /* memory; page_size * cell stride is at most 2^30 */
 } kda_paged_problem_t;
 
 /* Rotation of keys (and queries) on their way into the cache. */

@@ -371,6 +371,53 @@ def test_attention_split_over_the_cells(io, new, cells):
     c.check("window", window=1100)
 
 
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_attention_holes_beside_infinities(io, bad):
+    """Every other page missing and a cell of each page that is there infinite: all tokens see them."""
+    c = Case([5, 40], [700, 900], 2, 1, 64, 64, io, 16, seed=21)
+    c.table[:, ::2] = -1
+    for n in (0, 1):
+        for page in c.table[n].tolist():
+            if page >= 0:
+                c.vp[page, 0, 3, 7] = bad
+    out, lse = kda.paged_attention(*c.args(), return_lse=True)
+    want, wl, _ = ref.attention(*c.args())
+    ok = torch.isfinite(want)
+    assert not ok[..., 7].any() and torch.equal(torch.isfinite(out), ok)
+    close("finite", out[ok], want[ok], *tol(io, int(ok.sum())))
+    assert float((lse.double() - wl).abs().max()) <= 6e-5
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_attention_one_chunk_among_empty_sequences(io):
+    """No more tokens than sequences, all of them one sequence's; and offsets that decrease on the device."""
+    new = [0] * 60
+    new[17] = 41
+    cells = [5] * 60
+    cells[17] = 400
+    Case(new, cells, 4, 1, 64, 128, io, 16, seed=22).check("one chunk")
+    c = Case([30, 10, 20], [100, 50, 70], 4, 2, 64, 64, io, 16, seed=23)
+    c.cu = i32(0, 30, 25, 60)  # the second is empty, the third starts inside the first
+    out, lse = kda.paged_attention(*c.args(), return_lse=True)
+    torch.cuda.synchronize()
+    want, _, _ = ref.attention(*c.args())
+    close("first rows", out[:, :25], want[:, :25], *tol(io, 25 * 4 * 64))
+    close("last rows", out[:, 30:], want[:, 30:], *tol(io, 30 * 4 * 64))
+
+
+def test_attention_more_sequences_than_threads():
+    g = gen(24)
+    n = 1200
+    cells = torch.randint(0, 90, (n,), generator=g).tolist()
+    new = [int(c > 0) for c in cells]
+    cells[700], new[700] = 6000, 1
+    cells[30], new[30] = 3000, 33
+    c = Case(new, cells, 4, 2, 64, 64, BF, 32, seed=25)
+    c.check("1,200 sequences")
+    c.check("window", window=50)
+
+
 def test_attention_of_a_large_pool():
     """Cells behind 2^31 elements of the pool."""
     g = gen(11)

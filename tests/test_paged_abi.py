@@ -124,7 +124,7 @@ def room(p):
     (dict(batch=-1), INVALID), (dict(seq_len=-1), INVALID), (dict(num_heads_q=0), INVALID), (dict(num_heads_kv=0), INVALID),
     (dict(num_heads_q=3), INVALID), (dict(io_dtype=7), INVALID), (dict(head_dim_k=256), UNSUPPORTED), (dict(head_dim_v=80), UNSUPPORTED),
     (dict(page_size=0), INVALID), (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED), (dict(max_pages=-1), INVALID),
-    (dict(max_pages=1 << 27), INVALID), (dict(num_pages=-1), INVALID), (dict(num_pages=1 << 31), INVALID), (dict(stride_table=6), INVALID),
+    (dict(max_pages=(1 << 26) + 1), UNSUPPORTED), (dict(k_page_stride=1 << 40, k_head_stride=1 << 36, k_cell_stride=1 << 27), UNSUPPORTED), (dict(num_pages=-1), INVALID), (dict(num_pages=1 << 31), INVALID), (dict(stride_table=6), INVALID),
     (dict(stride_table=-9), INVALID), (dict(stride_q=100), INVALID), (dict(stride_q=260), INVALID), (dict(stride_k=64), INVALID),
     (dict(stride_v=252), INVALID), (dict(stride_v=1 << 59), UNSUPPORTED), (dict(batch=1 << 20, seq_len=1 << 12), UNSUPPORTED),
     (dict(k_page_stride=2048, k_head_stride=1024, k_cell_stride=32), INVALID),   # cells over each other
