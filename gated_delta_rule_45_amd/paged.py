@@ -124,7 +124,11 @@ def rope_bwd(d_q: torch.Tensor, d_k: Optional[torch.Tensor], inv_freq: torch.Ten
 
 
 def _pool(t, name: str, like: torch.Tensor):
-    """A pool's shape and strides."""
+    """A pool's shape and strides (the checks in one go first, as in _dense)."""
+    if isinstance(t, torch.Tensor) and t.dtype == like.dtype and t.get_device() == like.get_device() and t.dim() == 4:
+        s = t.stride()
+        if s[3] == 1 and s[0] > 0 and s[1] > 0 and s[2] > 0:
+            return t.shape, s
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.get_device() != like.get_device() or t.device.type != like.device.type:
@@ -138,7 +142,7 @@ def _pool(t, name: str, like: torch.Tensor):
         raise ValueError(f"{name}: the last axis must be dense (strides {s})")
     if any(a == 0 and b > 1 for a, b in zip(s, t.shape)):
         raise ValueError(f"{name}: cells share memory (strides {s})")
-    return t.shape, s[:3]
+    return t.shape, s
 
 
 def _paged(like, B, T, Hq, k_pages, v_pages, block_table, kv_lens, cu_seqlens, lq, lk, lv):
@@ -165,7 +169,7 @@ def _paged(like, B, T, Hq, k_pages, v_pages, block_table, kv_lens, cu_seqlens, l
             _want(block_table, "block_table", torch.int32, (n, most), like)
         lt = block_table.stride(0) if n > 1 else 0
     p = PagedProblem(B, T, n if cu_seqlens is not None else 0, Hq, Hk, dk, vshape[3], _io_code(like.dtype), cells, most, pages, lt,
-                     lq, lk, lv, *ks, *vs)
+                     lq, lk, lv, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
     return p, n
 
 
