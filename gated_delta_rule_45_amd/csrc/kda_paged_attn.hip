@@ -402,7 +402,7 @@ hipError_t join(const AttnParams &p, int M, int64_t tiles, hipStream_t s) {
 }  // namespace
 
 // c_min: two blocks, 256 cells, below which joining costs more than it gains
-AttnTile attn_rows_tile(bool) { return {kM, kKB, 2, 2}; }
+AttnTile attn_rows_tile(bool bf16) { return {kM, kKB, bf16 ? 2 : 1, 2}; }
 
 hipError_t launch_attn_rows(bool bf16, const AttnParams &p, int64_t blocks, hipStream_t stream) {
     if (blocks <= 0) return hipSuccess;
