@@ -6,6 +6,7 @@
 // A tile is 16 rows (tokens x heads that share a key head), the width of the matrix instruction.  Four waves take the
 // 32-cell quarters of each 128-cell block by themselves and are added at the end, so nothing is staged in LDS and
 // the loop has no barrier: with few rows each cell is used once per wave, and the kernel is bound by the cache's bytes.
+// fp32 calls with many rows are bound by the fp32 matrix instruction and by reading each cell once per 16 rows.
 //
 // Layouts (lane = 16 g + c).  S^T = K Q^T leaves lane (g, c) the scores of row c for cells 4 g + j of each 16: a lane holds
 // 8 cells of one row, the contraction slots of the next product (which may come in any order), so P feeds O^T = V^T P^T
@@ -13,6 +14,12 @@
 // the rescaling factor of a row belongs to the lane that holds the row's sums.  V^T needs 8 cells of one column in a
 // lane: a lane loads d_v / 16 columns of its 8 cells (a cell's row is one run over 16 lanes) and pairs them up with
 // byte permutes, one per two values.
+//
+// Measured (bf16, 32 query and 8 key heads of 128): 64 ragged contexts of up to 8,192 cells 202 us (5.4 TB/s of the cache), one
+// of 131,072 cells 97 us (5.6 TB/s), 96 sequences of 4 tokens, 16 query heads and a window of 1,024 cells 72 us
+// (5.6 TB/s); fp32, 4 x 1,024 tokens behind 4,096 cells, 16 heads: 1.8 ms (87 TFLOP/s of the 154 of a large product).
+// Values are loaded past the caches' usual order, as nothing reads them twice: 216 -> 200 us for the ragged batch;
+// keys, whose 128-byte lines are read by halves, gain nothing from it (204).
 #include "kda_paged_work.h"
 
 namespace kda {
@@ -78,15 +85,22 @@ struct Ops<uint16_t, DK, DV> {
         return a;
     }
     __device__ __forceinline__ void add(f32x4 (&o)[VW], const float (&p)[8]) const {
-        const u32x4 pp = {pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]), pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7])};
+        // p as two bf16 terms: one would add its rounding to the output's (2.3e-3 of the norm instead of 1.7e-3), and the
+        // second product costs nothing beside the cache's bytes (204.2 us either way for the ragged batch)
+        u32x4 hi, lo;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            hi[d] = pack_bf16x2(p[2 * d], p[2 * d + 1]);
+            lo[d] = pack_bf16x2(p[2 * d] - bf16_lo(hi[d]), p[2 * d + 1] - bf16_hi(hi[d]));
+        }
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
             u32x4 a;
 #pragma unroll
             for (int d = 0; d < 4; ++d)
                 a[d] = __builtin_amdgcn_perm(v[2 * d + 1][i / 2], v[2 * d][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
-            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, pp), o[i], 0,
-                                                           0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, hi), o[i], 0, 0, 0);
+            o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, lo), o[i], 0, 0, 0);
         }
     }
 };
@@ -308,8 +322,8 @@ __global__ void __launch_bounds__(256, sizeof(IO) == 2 ? 3 : DK + DV == 256 ? 1 
     put_row<IO, DV, kM>(p, w, out, c16, y, top, sum);
 }
 
-// Joins the splits of a tile.  Bound: the latency of reading them, so a row's splits go to 256 / (RJ * DV / 4) groups of threads
-// side by side, RJ rows at a time.  There is a workgroup for every RB rows of the most tiles there can be: one row where a
+// Joins the splits of a tile (4 us, of which the launch is most).  Bound: the latency of reading them, so a row's splits go to
+// 256 / (RJ * DV / 4) groups of threads side by side, RJ rows at a time.  There is a workgroup for every RB rows of the most tiles there can be: one row where a
 // tile has 16; 32 of 256, since mostly no tile is split and what the workgroups cost is their number (131,072 of them 40 us).
 template <typename IO, int DV, int RJ, int RB>
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p, int M) {
@@ -401,7 +415,11 @@ hipError_t join(const AttnParams &p, int M, int64_t tiles, hipStream_t s) {
 
 }  // namespace
 
-// c_min: two blocks, 256 cells, below which joining costs more than it gains
+// Parts: of at least two blocks of 128 cells in bf16 (a block takes a wave about 1 us, the join 4: with one block a part 512 to
+// 4,096 cells of one sequence take 10.0 to 10.3 us instead of 11.1 to 11.6, 256 cells 9.9 instead of 9.1) and one in fp32, whose
+// block takes twice as long (1,002 cells 16.0 -> 13.0 us); for two workgroups per CU: one leaves the ends of ragged batches to few (220
+// us instead of 205), three make more parts than the cache's bandwidth needs (131,072 cells: 94 us instead of 89, the
+// batch 200).  Three workgroups of the bf16 kernel fit a CU.
 AttnTile attn_rows_tile(bool bf16) { return {kM, kKB, bf16 ? 2 : 1, 2}; }
 
 hipError_t launch_attn_rows(bool bf16, const AttnParams &p, int64_t blocks, hipStream_t stream) {

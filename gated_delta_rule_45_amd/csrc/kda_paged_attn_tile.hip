@@ -1,11 +1,11 @@
 // Attention of many rows over a paged cache (chunks and whole prompts, bf16): tiles of 256 rows.
 //
-// Bound: the matrix units.  Eight waves own 32 rows each and share 64-cell blocks of keys and values in LDS; with
-// 2 (d_k + d_v) flops per row and cell a block costs 2,048 cycles of a CU's matrix units, and about as many of its vector
-// units for the softmax (an exponential is a quarter-rate instruction), so the two have to run side by side: the waves
-// 0-3 and 4-7, one of each on every SIMD, take turns, half an iteration apart: while one group multiplies (O += P V of
-// block t, then S = K Q^T of block t + 1), the other works out the weights of its block and starts the loads of later
-// ones.  A barrier ends each half.  Keys are staged three blocks ahead of their use, values two, in rings of four buffers.
+// Bound: the SIMDs' issue of matrix and vector instructions.  Eight waves own 32 rows each and share 64-cell blocks of
+// keys and values in LDS; with 2 (d_k + d_v) flops per row and cell a block costs 2,048 cycles of a CU's matrix units, and about as
+// many of its vector units for the softmax (an exponential is a quarter-rate instruction), so the two have to run side by
+// side: the waves 0-3 and 4-7, one of each on every SIMD, take turns, half an iteration apart: while one group multiplies
+// (O += P V of block t, then S = K Q^T of block t + 1), the other starts the loads of later blocks and works out the
+// weights of its own.  A barrier ends each half.  Keys are staged three blocks ahead of their use, values two, in rings of four buffers.
 //
 // Layouts (lane = 32 h + r).  S^T = K Q^T and O^T = V^T P^T as in the kernel for few rows, here as 32 x 32 tiles: a
 // lane holds the scores of row r for cells 8 a + 4 h + b of each 32, which are the contraction slots of the next product as they
@@ -13,6 +13,18 @@
 // place lane l's 16 bytes at 16 l, so rows are scattered over the banks by which bytes a lane fetches: 16-byte
 // pieces of keys move by row mod 16 (by half of that where two rows make 256 bytes), 32-byte pieces of values, what 16
 // lanes read of a row, by row mod 4: neither then meets a bank twice in the 256 bytes that LDS gives in a cycle.
+//
+// Weights are rounded to bf16 for their product (error of the output 2.1 to 2.4e-3 of its norm, 1.7e-3 of that its own
+// rounding): a second term, as in the kernel for few rows, would add half as many products again.
+//
+// Measured (32 query and 8 key heads of 128): 4 prompts of 4,096 tokens 565 us, 973 TFLOP/s (a large matrix product: 1,378; matrix
+// units busy 46 % of the time, waves waiting 25 %), 6 chunks of 1,024 tokens behind 16,384 cells 1.60 ms, 1,064 TFLOP/s;
+// d_k = d_v = 64: 780 TFLOP/s (the same softmax for half the products).  A half iteration takes 1,600 to 1,700 cycles of
+// the 1,024 that its products need.  What it took, on the prompts: products in one run with their LDS reads ten ahead and the
+// weights kept before them (678 -> 634 us; weights left to sink between the products: 738; six or fourteen reads ahead: 2 and
+// 1 % slower), a bank-free order of the keys (630 -> 615), one base address per load (with one per lane 655, else 600).  Loads
+// between the products cost more than they hide (610).  A workgroup's start (plan,
+// first blocks) is 10,000 of its 140,000 cycles: one fills a CU, so nothing covers it.
 #include "kda_paged_work.h"
 
 namespace kda {
@@ -370,7 +382,8 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
 
 }  // namespace
 
-// c_min: eight blocks, 512 cells: a part's sums (256 rows of d_v fp32) are then small beside its keys and values' work
+// Parts of at least eight blocks, 512 cells: a part's sums (256 rows of d_v fp32) are then small beside its work (1 x 1,024 tokens:
+// 40 us, of at least four blocks 52); for two workgroups per CU, although one fills it (one: attention of chunks 664 us instead of 650)
 AttnTile attn_tile_tile() { return {kM, kKB, 8, 2}; }
 
 hipError_t launch_attn_tile(const AttnParams &p, int64_t blocks, hipStream_t s) {

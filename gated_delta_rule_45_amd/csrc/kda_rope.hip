@@ -4,6 +4,9 @@
 // Bound: HBM, each value is read and written once.  A thread owns 8 pairs (16 channels) of a token and turns them in
 // HP heads, so that the angles (about 30 instructions a pair, some in 64 bits) are worked out once for them; the
 // threads of a wave lie along a head and then along the heads, whose loads are all issued first.
+//
+// bf16, 16,384 tokens: 16 + 8 heads of 128, slices of one projection, 42 us a call (4.8 TB/s; the kernel 34); 32 + 8 heads, half
+// of the channels copied, 64 us (5.3 TB/s).  A copy reaches 4.9.
 #include "kda_paged.h"
 #include "kda_rope.h"
 
