@@ -472,6 +472,42 @@ def test_attention_on_streams_and_in_graphs():
         assert torch.equal(out, eager) and torch.equal(lse, el), i
 
 
+def test_rope_and_append_on_streams_and_in_graphs():
+    g = gen(31)
+    k, v, q = rnd(g, 3, 2, 2, 64), rnd(g, 3, 2, 2, 64), rnd(g, 3, 2, 4, 64)
+    table, pages = ref.table_of([40, 18, 5], 16, 1, g, DEV)
+    wide = torch.full((3, 50), -1, dtype=I32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    k0, v0 = ref.pools(pages, 2, 16, 64, 64, BF, g, DEV)
+    freq, lens = kda.rope_frequencies(64, device=DEV)[0], i32(40, 18, 5)
+    torch.cuda.synchronize()
+
+    def call(kp, vp, s=None, tab=table):
+        y = kda.paged_append(k, v, kp, vp, tab, lens, q=q, inv_freq=freq, stream=s)
+        return y, kda.rope(y, None, freq, stream=s)[0]
+
+    kp, vp = k0.clone(), v0.clone()
+    want = call(kp, vp)
+    torch.cuda.synchronize()
+    for s, tab in ((torch.cuda.Stream(), table), (torch.cuda.Stream(), wide[:, :table.shape[1]])):
+        a, b = k0.clone(), v0.clone()
+        torch.cuda.synchronize()
+        got = call(a, b, s, tab)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(a, kp) and torch.equal(b, vp)
+    graph, s, a, b = torch.cuda.CUDAGraph(), torch.cuda.Stream(), k0.clone(), v0.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        got = call(a, b)
+    for i in range(3):
+        lens.sub_(1)
+        a.copy_(k0), b.copy_(v0), kp.copy_(k0), vp.copy_(v0)
+        graph.replay()
+        want = call(kp, vp)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(a, kp) and torch.equal(b, vp), i
+
+
 def test_a_serving_run():
     """Prompts in chunks, then token by token, through rope, cache and attention: as attention over the whole."""
     g, H, Hk, d, size = gen(15), 4, 2, 64, 16
