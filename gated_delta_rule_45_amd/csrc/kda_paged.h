@@ -84,7 +84,6 @@ struct AttnParams {
     float *part;               // per (split, head): M rows of d_v sums, M maxima, M sums of weights
 };
 constexpr int kDesc = 8;
-constexpr int kFewRows = 16;  // one tile of the kernel for few rows
 
 // Shape of a kernel's tiles.
 struct AttnTile {

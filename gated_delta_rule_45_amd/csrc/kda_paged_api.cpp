@@ -270,20 +270,26 @@ struct AttnPlan {
     size_t bytes = 0;
 };
 
-// Sequences of at most 16 rows go to the kernel for few rows, longer ones of bf16 calls to the one that stages cells in LDS
-// for 256 rows.  A packed batch may hold both, and what its offsets do not rule out on the host is launched, but for a
-// batch with no more tokens than sequences: the step of one token each that it looks like needs no second launch, and
-// longer sequences among empty ones come out the same from the first.
+// Sequences of few rows go to the kernel for few rows, longer ones of bf16 calls to the one that stages cells in LDS for 256 rows.
+// Few: 32, two tiles that read the cells from HBM once (2 sequences of 24 rows over 1,600 cells 25.0 -> 17.7 us, 64 of 32 over
+// 100 27.5 -> 16.3; 64 of 36 over 4,000 cells 297, and 315 as few); 64 in calls of few sequences and heads, where the
+// other kernel's longer start counts (1 of 64 rows over 30,000 cells, 8 key heads: 78 -> 57; 8 of them over 8,000: 90, 97 as few).
+// A packed batch may hold both, and what its offsets do not rule out on the host is launched, but for a batch with no more
+// tokens than sequences: the step of one token each that it looks like needs no second launch, and longer sequences among
+// empty ones come out the same from the first.
+int32_t few_rows(int64_t num_seqs, int64_t heads_kv) { return num_seqs * heads_kv <= 32 ? 64 : 32; }
+
 kda_status_t plan_attn(const kda_paged_problem_t *p, const Shape &s, bool packed, const int32_t *cu_host, int32_t window, int cus,
                        AttnPlan &a) {
     a = AttnPlan{};
     const bool bf16 = p->io_dtype == KDA_BF16;
+    const int32_t few = few_rows(s.num_seqs, p->num_heads_kv);
     const bool both = bf16 && (!packed || cu_host || s.tokens > s.num_seqs);
     for (int tile = 0; tile < (both ? 2 : 1); ++tile) {
         Launch l;
         l.t = tile ? kda::paged::attn_tile_tile() : kda::paged::attn_rows_tile(bf16);
-        if (tile) l.rows_lo = kda::paged::kFewRows + 1;
-        if (both && !tile) l.rows_hi = kda::paged::kFewRows;
+        if (tile) l.rows_lo = few + 1;
+        if (both && !tile) l.rows_hi = few;
         const kda_status_t st = plan_launch(p, s, packed, cu_host, window, cus, l);
         if (st != KDA_OK) return st;
         if (l.blocks == 0) continue;

@@ -3,7 +3,7 @@
 //
 // One pass over the cells with a running maximum m and sum l per row:  p_j = 2^(s_j - m),  o = sum p_j v_j / l.
 //
-// A tile is 16 rows (tokens x heads that share a key head), the width of the matrix instruction.  Four waves take the
+// A tile is 16 rows (tokens x heads that share a key head), the width of the matrix instruction; a sequence has one or a few.  Four waves take the
 // 32-cell quarters of each 128-cell block by themselves and are added at the end, so nothing is staged in LDS and
 // the loop has no barrier: with few rows each cell is used once per wave, and the kernel is bound by the cache's bytes.
 // fp32 calls with many rows are bound by the fp32 matrix instruction and by reading each cell once per 16 rows.
@@ -26,7 +26,7 @@ namespace kda {
 namespace paged {
 namespace {
 
-constexpr int kM = kFewRows, kKB = 128;
+constexpr int kM = 16, kKB = 128;
 
 __device__ __forceinline__ float max_groups(float x) {  // over the lanes that differ in g
     auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -210,11 +210,13 @@ __global__ void __launch_bounds__(256, sizeof(IO) == 2 ? 3 : DK + DV == 256 ? 1 
             x.load_k(s, at, k_off);
         }
     };
-    pages.refill(c, w.n, w.b0, wave, lane, w.hi, w.b1);
-    if (w.b0 < w.b1) load_k(0, w.b0);
+    // this wave's quarters of the first and the last block may be out of sight
+    const int b0 = w.b0 * kKB + 32 * wave + 32 > w.lo ? w.b0 : w.b0 + 1, b1 = (w.b1 - 1) * kKB + 32 * wave < w.hi ? w.b1 : w.b1 - 1;
+    pages.refill(c, w.n, b0, wave, lane, w.hi, b1);
+    if (b0 < b1) load_k(0, b0);
 #pragma unroll 1
-    for (int b = w.b0; b < w.b1; ++b) {
-        const int i = (b - w.b0) & 31, cell0 = b * kKB + 32 * wave;
+    for (int b = b0; b < b1; ++b) {
+        const int i = (b - b0) & 31, cell0 = b * kKB + 32 * wave;
         const int page0 = pages.get(2 * i), page1 = pages.get(2 * i + 1);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
@@ -227,8 +229,8 @@ __global__ void __launch_bounds__(256, sizeof(IO) == 2 ? 3 : DK + DV == 256 ? 1 
         f32x4 s0 = x.scores(0), s1 = x.scores(1);
         mfma_settle(s0, s1);
         // the next block's keys
-        if (i == 31) pages.refill(c, w.n, b + 1, wave, lane, w.hi, w.b1);
-        if (b + 1 < w.b1) load_k(i + 1, b + 1);
+        if (i == 31) pages.refill(c, w.n, b + 1, wave, lane, w.hi, b1);
+        if (b + 1 < b1) load_k(i + 1, b + 1);
         const bool edge = page0 < 0 || page1 < 0 || cell0 < all_lo || cell0 + 32 > all_hi;
         const bool part = ragged && (cell0 < all_lo || cell0 + 32 > all_hi);  // some rows see what others do not
         bool odd = false;
