@@ -90,7 +90,8 @@ struct AttnTile {
     int32_t M, KB, c_min, target_per_cu;
 };
 AttnTile attn_rows_tile(bool bf16);
-hipError_t launch_attn_rows(bool bf16, const AttnParams &p, int64_t blocks, hipStream_t stream);
+// many: fp32 calls of many rows over long contexts, see the host's choice
+hipError_t launch_attn_rows(bool bf16, bool many, const AttnParams &p, int64_t blocks, hipStream_t stream);
 AttnTile attn_tile_tile();
 hipError_t launch_attn_tile(const AttnParams &p, int64_t blocks, hipStream_t stream);  // bf16
 // joins the splits of at most `tiles` tiles of M rows per head

@@ -216,6 +216,7 @@ struct Launch {
     AttnTile t{};
     int32_t rows_lo = 1, rows_hi = 0x7fffffff, c_min = 0, target = 0;
     int64_t blocks = 0, tiles = 0, slots = 0;  // workgroups; split tiles and their splits per head
+    int64_t most = 0;                          // blocks of a tile, at most
     size_t desc = 0, part = 0;                 // bytes
 };
 
@@ -236,6 +237,7 @@ kda_status_t plan_launch(const kda_paged_problem_t *p, const Shape &s, bool pack
     }
     int64_t most = (cells + KB - 1) / KB;  // blocks of a tile, at most
     if (window > 0) most = std::min(most, ((int64_t)window + (M - 1) / s.G + 1 + KB - 1) / KB + 1);
+    l.most = most;
     const int64_t Hk = p->num_heads_kv, target = (int64_t)cus * l.t.target_per_cu;
     l.target = (int32_t)target;
     // No tile is worth splitting: it has few blocks; or they are not many and there are tiles enough; or the blocks that a
@@ -533,6 +535,10 @@ kda_status_t kda_paged_attn(const kda_paged_problem_t *p, const void *q, const v
         char *ws = static_cast<char *>(workspace);
         for (int i = 0; i < a.n; ++i) {
             const Launch &l = a.part[i];
+            // fp32 heads of 128: two workgroups of 237 registers on a CU suit single rows and short contexts, whose
+            // latency counts (3 x 229 tokens x 32 heads 59 -> 44 us, 59 x 8 tokens over 563 cells 66 -> 56); one of 270, which
+            // keeps more loads in flight, many rows over long ones (4 x 512 tokens over 4,608 cells 984 -> 794)
+            const bool many = s.tokens * s.G > 16LL * s.num_seqs && l.most > 4;
             r.rows_lo = l.rows_lo;
             r.rows_hi = l.rows_hi;
             r.c_min = l.c_min;
@@ -541,7 +547,7 @@ kda_status_t kda_paged_attn(const kda_paged_problem_t *p, const void *q, const v
             r.slots = (int32_t)l.slots;
             r.desc = l.desc ? reinterpret_cast<int32_t *>(ws) : nullptr;
             r.part = reinterpret_cast<float *>(ws + l.desc);
-            st = done(a.tile[i] ? kda::paged::launch_attn_tile(r, l.blocks, hs) : kda::paged::launch_attn_rows(bf16, r, l.blocks, hs),
+            st = done(a.tile[i] ? kda::paged::launch_attn_tile(r, l.blocks, hs) : kda::paged::launch_attn_rows(bf16, many, r, l.blocks, hs),
                       "kda_paged_attn launch");
             if (st == KDA_OK && l.tiles > 0)
                 st = done(kda::paged::launch_attn_join(bf16, r, l.t.M, l.tiles, hs), "kda_paged_attn join launch");

@@ -165,8 +165,9 @@ struct Pages {
     __device__ __forceinline__ int get(int i) const { return __builtin_amdgcn_readlane(entry, i & 63); }
 };
 
-template <typename IO, int DK, int DV>
-__global__ void __launch_bounds__(256, sizeof(IO) == 2 ? 3 : DK + DV == 256 ? 1 : 2) attn_rows_kernel(AttnParams p) {
+// WG: workgroups that share a CU.
+template <typename IO, int DK, int DV, int WG>
+__global__ void __launch_bounds__(256, WG) attn_rows_kernel(AttnParams p) {
     constexpr int VW = DV / 16, PAD = DV + 4;
     __shared__ union {
         PlanLds plan;
@@ -396,13 +397,13 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p, int M) {
     }
 }
 
-template <typename IO>
+template <typename IO, int WG, int WGL>
 hipError_t rows(const AttnParams &p, dim3 grid, hipStream_t s) {
     const dim3 block(256);
-    if (p.dk == 128 && p.dv == 128) hipLaunchKernelGGL((attn_rows_kernel<IO, 128, 128>), grid, block, 0, s, p);
-    if (p.dk == 128 && p.dv == 64) hipLaunchKernelGGL((attn_rows_kernel<IO, 128, 64>), grid, block, 0, s, p);
-    if (p.dk == 64 && p.dv == 128) hipLaunchKernelGGL((attn_rows_kernel<IO, 64, 128>), grid, block, 0, s, p);
-    if (p.dk == 64 && p.dv == 64) hipLaunchKernelGGL((attn_rows_kernel<IO, 64, 64>), grid, block, 0, s, p);
+    if (p.dk == 128 && p.dv == 128) hipLaunchKernelGGL((attn_rows_kernel<IO, 128, 128, WGL>), grid, block, 0, s, p);
+    if (p.dk == 128 && p.dv == 64) hipLaunchKernelGGL((attn_rows_kernel<IO, 128, 64, WG>), grid, block, 0, s, p);
+    if (p.dk == 64 && p.dv == 128) hipLaunchKernelGGL((attn_rows_kernel<IO, 64, 128, WG>), grid, block, 0, s, p);
+    if (p.dk == 64 && p.dv == 64) hipLaunchKernelGGL((attn_rows_kernel<IO, 64, 64, WG>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 
@@ -425,9 +426,11 @@ hipError_t join(const AttnParams &p, int M, int64_t tiles, hipStream_t s) {
 // batch 200).  Three workgroups of the bf16 kernel fit a CU.
 AttnTile attn_rows_tile(bool bf16) { return {kM, kKB, bf16 ? 2 : 1, 2}; }
 
-hipError_t launch_attn_rows(bool bf16, const AttnParams &p, int64_t blocks, hipStream_t stream) {
+hipError_t launch_attn_rows(bool bf16, bool many, const AttnParams &p, int64_t blocks, hipStream_t stream) {
     if (blocks <= 0) return hipSuccess;
-    return bf16 ? rows<uint16_t>(p, dim3((unsigned)blocks), stream) : rows<float>(p, dim3((unsigned)blocks), stream);
+    const dim3 grid((unsigned)blocks);
+    if (bf16) return rows<uint16_t, 3, 3>(p, grid, stream);
+    return many ? rows<float, 2, 1>(p, grid, stream) : rows<float, 2, 2>(p, grid, stream);
 }
 
 hipError_t launch_attn_join(bool bf16, const AttnParams &p, int M, int64_t tiles, hipStream_t stream) {
