@@ -279,14 +279,21 @@ struct AttnPlan {
 // A packed batch may hold both, and what its offsets do not rule out on the host is launched, but for a batch with no more
 // tokens than sequences: the step of one token each that it looks like needs no second launch, and longer sequences among
 // empty ones come out the same from the first.
-int32_t few_rows(int64_t num_seqs, int64_t heads_kv) { return num_seqs * heads_kv <= 32 ? 64 : 32; }
+// All rows are few in calls of little work, at most 12 M pairs of (row, key head) and cells that a table has room for: one round of
+// the kernel for few rows is then over before the other one's workgroups have started (1 x 128 tokens over 628 cells,
+// 32 / 8 heads: 33 -> 22 us; 3 ragged chunks of up to 700 over 300: 47 -> 21; 64 x 9 over 209: 36 -> 26; beyond,
+// 1 x 128 over 4,028: 40 both ways, 8 x 40 over 2,040: 40, 70 as few).
+int32_t few_rows(int64_t num_seqs, int64_t heads_kv, int64_t rows, int64_t cells) {
+    if (rows * heads_kv <= (12LL << 20) / std::max<int64_t>(cells, 1)) return 0x7fffffff;
+    return num_seqs * heads_kv <= 32 ? 64 : 32;
+}
 
 kda_status_t plan_attn(const kda_paged_problem_t *p, const Shape &s, bool packed, const int32_t *cu_host, int32_t window, int cus,
                        AttnPlan &a) {
     a = AttnPlan{};
     const bool bf16 = p->io_dtype == KDA_BF16;
-    const int32_t few = few_rows(s.num_seqs, p->num_heads_kv);
-    const bool both = bf16 && (!packed || cu_host || s.tokens > s.num_seqs);
+    const int32_t few = few_rows(s.num_seqs, p->num_heads_kv, s.tokens * s.G, p->num_pages > 0 ? (int64_t)p->max_pages * p->page_size : 0);
+    const bool both = bf16 && few < 0x7fffffff && (!packed || cu_host || s.tokens > s.num_seqs);
     for (int tile = 0; tile < (both ? 2 : 1); ++tile) {
         Launch l;
         l.t = tile ? kda::paged::attn_tile_tile() : kda::paged::attn_rows_tile(bf16);

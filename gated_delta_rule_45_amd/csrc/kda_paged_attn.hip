@@ -86,12 +86,14 @@ struct Ops<uint16_t, DK, DV> {
     }
     __device__ __forceinline__ void add(f32x4 (&o)[VW], const float (&p)[8]) const {
         // p as two bf16 terms: one would add its rounding to the output's (2.3e-3 of the norm instead of 1.7e-3), and the
-        // second product costs nothing beside the cache's bytes (204.2 us either way for the ragged batch)
+        // second product costs nothing beside the cache's bytes (204.2 us either way for the ragged batch).  The first is p cut
+        // off and the second not quite the rest, so that both are above 0 where p is: an infinite value stays infinite.
         u32x4 hi, lo;
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-            hi[d] = pack_bf16x2(p[2 * d], p[2 * d + 1]);
-            lo[d] = pack_bf16x2(p[2 * d] - bf16_lo(hi[d]), p[2 * d + 1] - bf16_hi(hi[d]));
+            hi[d] = __builtin_amdgcn_perm(__float_as_uint(p[2 * d + 1]), __float_as_uint(p[2 * d]), 0x07060302u);
+            lo[d] = pack_bf16x2(fmaf(p[2 * d], 0x1p-60f, p[2 * d] - bf16_lo(hi[d])),
+                                fmaf(p[2 * d + 1], 0x1p-60f, p[2 * d + 1] - bf16_hi(hi[d])));
         }
 #pragma unroll
         for (int i = 0; i < VW; ++i) {

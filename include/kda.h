@@ -630,7 +630,8 @@ kda_status_t kda_paged_append(const kda_paged_problem_t *problem, const void *k,
  * behind max_pages.  What masked cells and cells behind kv_lens hold does not matter, NaN included; rows of out and
  * lse that no sequence owns are left as they are.
  * Statistics and sums are fp32; bf16 io: weights enter their product with the values as two bf16 terms where a sequence has
- * at most 32 rows (new tokens x Hq / Hkv; 64 in calls of up to 32 sequences x key heads), rounded to one where it has more.
+ * at most 32 rows (new tokens x Hq / Hkv; 64 in calls of up to 32 sequences x key heads, any number in calls of little
+ * work), rounded to one where it has more.
  * The results repeat bit for bit; how rows are split goes by all lengths of the batch, so a sequence's last bits may differ
  * in another batch.  Calls that overlap in time need a workspace each.  Errors as for kda_chunk_bwd.
  */

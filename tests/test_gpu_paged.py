@@ -234,12 +234,19 @@ def test_append_of_slices_into_slices():
 
 # --------------------------------------------------------------------------------- attention --
 class Case:
-    def __init__(self, new, cells, Hq, Hk, dk, dv, io, size, seed=1, first=False, packed=None, q_scale=1.0):
+    """wide: a table with room for 2^20 cells a sequence, as a server keeps them: calls are then never of little work, and
+    sequences of more than 64 rows (bf16) go to the kernel for many."""
+
+    def __init__(self, new, cells, Hq, Hk, dk, dv, io, size, seed=1, first=False, packed=None, q_scale=1.0, wide=False):
         g = gen(seed)
         self.packed = len(set(new)) > 1 if packed is None else packed
         B, T, self.cu = batch(g, new, self.packed)
         self.q = rnd(g, B, T, Hq, dk, dtype=io) * q_scale
         self.table, pages = ref.table_of(cells, size, 2, g, DEV)
+        if wide:
+            room = torch.full((len(new), 2 ** 20 // size), -1, dtype=I32, device=DEV)
+            room[:, :self.table.shape[1]] = self.table
+            self.table = room
         self.kp, self.vp = ref.pools(pages, Hk, size, dk, dv, io, g, DEV, first)
         self.lens = i32(*cells)
 
@@ -262,61 +269,68 @@ class Case:
         return out, lse
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("io", [BF, F32])
 @pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
 @pytest.mark.parametrize("new,cells", [([1], [1]), ([1, 1], [17, 16]), ([1], [700]), ([5, 5, 5], [5, 130, 333]),
                                        ([33, 33], [33, 300]), ([150], [150])])
-def test_attention_lengths_and_head_sizes(io, dk, dv, new, cells):
-    Case(new, cells, 4, 2, dk, dv, io, 16, seed=dk + dv + len(new) + cells[-1]).check(f"{new} {cells} {dk}x{dv}")
+def test_attention_lengths_and_head_sizes(wide, io, dk, dv, new, cells):
+    Case(new, cells, 4, 2, dk, dv, io, 16, seed=dk + dv + len(new) + cells[-1], wide=wide).check(f"{new} {cells} {dk}x{dv}")
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("io", [BF, F32])
 @pytest.mark.parametrize("Hq,Hk", [(1, 1), (3, 3), (5, 1), (24, 3), (32, 1), (8, 8)])
 @pytest.mark.parametrize("new", [1, 3, 40])
-def test_attention_head_groups(io, Hq, Hk, new):
-    Case([new] * 2, [new + 90, new], Hq, Hk, 64, 64, io, 32, seed=Hq).check(f"{Hq}/{Hk} x{new}")
+def test_attention_head_groups(wide, io, Hq, Hk, new):
+    Case([new] * 2, [new + 90, new], Hq, Hk, 64, 64, io, 32, seed=Hq, wide=wide).check(f"{Hq}/{Hk} x{new}")
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("io", [BF, F32])
 @pytest.mark.parametrize("size,first", [(16, True), (64, False), (128, True), (1024, False)])
-def test_attention_page_sizes(io, size, first):
-    Case([1, 70, 0, 2, 9], [1030, 70, 40, 515, 129], 8, 2, 128, 128, io, size, seed=size, first=first).check(f"pages of {size}")
+def test_attention_page_sizes(wide, io, size, first):
+    Case([1, 70, 0, 2, 9], [1030, 70, 40, 515, 129], 8, 2, 128, 128, io, size, seed=size, first=first, wide=wide).check(f"pages of {size}")
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("io", [BF, F32])
 @pytest.mark.parametrize("window", [1, 2, 15, 128, 200, 5000, 2 ** 31 - 1])
-def test_attention_windows(io, window):
-    Case([1, 130, 6], [900, 300, 1300], 6, 2, 64, 128, io, 16, seed=window % 97).check(f"window {window}", window=window)
+def test_attention_windows(wide, io, window):
+    Case([1, 130, 6], [900, 300, 1300], 6, 2, 64, 128, io, 16, seed=window % 97, wide=wide).check(f"window {window}", window=window)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("io", [BF, F32])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0])
-def test_attention_scales(io, scale):
+def test_attention_scales(wide, io, scale):
     """Sharp rows too: scores of some 30."""
-    Case([1, 20, 40], [500, 20, 333], 4, 1, 64, 64, io, 16, seed=3).check(f"scale {scale}", scale=scale)
+    Case([1, 20, 40], [500, 20, 333], 4, 1, 64, 64, io, 16, seed=3, wide=wide).check(f"scale {scale}", scale=scale)
 
 
+@pytest.mark.parametrize("Hq,wide", [(4, False), (32, True)])
 @pytest.mark.parametrize("io", [BF, F32])
-def test_attention_rows_without_cells(io):
+def test_attention_rows_without_cells(io, Hq, wide):
     """Sequences with fewer cells than new tokens, without cells, without tokens; rows that no sequence owns."""
-    c = Case([4, 6, 0, 20, 1], [2, 0, 9, 11, 1], 4, 2, 64, 64, io, 16, seed=4)
+    c = Case([4, 6, 0, 20, 1], [2, 0, 9, 11, 1], Hq, 2, 64, 64, io, 16, seed=4, wide=wide)
     c.check("empty rows")
     c.lens = i32(2, -5, 9, 11, 1)
     c.check("negative length")
     c.cu = i32(0, 4, 10, 10, 25, 26)  # five rows fewer are owned
     c.lens = i32(2, 0, 9, 11, 1)
-    mark, ml = torch.full((1, 31, 4, 64), 7.0, dtype=io, device=DEV), torch.full((1, 31, 4), 7.0, device=DEV)
+    mark, ml = torch.full((1, 31, Hq, 64), 7.0, dtype=io, device=DEV), torch.full((1, 31, Hq), 7.0, device=DEV)
     out, lse = c.check("padded", out=mark, lse=ml)
     assert (out[:, 26:] == 7).all() and (lse[:, 26:] == 7).all()
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("io", [BF, F32])
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
-def test_attention_does_not_see_what_is_masked(io, bad):
+def test_attention_does_not_see_what_is_masked(wide, io, bad):
     """NaN and infinities in cells behind a sequence's end, in other pages, before the window, and in cells of the chunk that
     only later tokens see; those tokens get them."""
     new, cells = [1, 30, 7, 150], [77, 130, 90, 290]
-    c = Case(new, cells, 4, 2, 64, 128, io, 16, seed=6)
+    c = Case(new, cells, 4, 2, 64, 128, io, 16, seed=6, wide=wide)
     pages = c.kp.shape[0]
     used = torch.zeros(pages, 16, dtype=torch.bool)
     for n, m in enumerate(cells):
@@ -342,9 +356,10 @@ def test_attention_does_not_see_what_is_masked(io, bad):
     close("window", out[ok], want[ok], *tol(io, int(ok.sum())))
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("io", [BF, F32])
-def test_attention_pages_that_do_not_exist(io):
-    c = Case([1, 40, 3], [600, 200, 333], 4, 2, 64, 64, io, 32, seed=7)
+def test_attention_pages_that_do_not_exist(io, wide):
+    c = Case([1, 40, 3], [600, 200, 333], 4, 2, 64, 64, io, 32, seed=7, wide=wide)
     c.table[0, 3] = -1
     c.table[0, 9] = 2 ** 30
     c.table[1, 1] = c.kp.shape[0]
@@ -371,11 +386,12 @@ def test_attention_split_over_the_cells(io, new, cells):
     c.check("window", window=1100)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("io", [BF, F32])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
-def test_attention_holes_beside_infinities(io, bad):
+def test_attention_holes_beside_infinities(wide, io, bad):
     """Every other page missing and a cell of each page that is there infinite: all tokens see them."""
-    c = Case([5, 40], [700, 900], 2, 1, 64, 64, io, 16, seed=21)
+    c = Case([5, 40], [700, 900], 2, 1, 64, 64, io, 16, seed=21, wide=wide)
     c.table[:, ::2] = -1
     for n in (0, 1):
         for page in c.table[n].tolist():
@@ -384,20 +400,21 @@ def test_attention_holes_beside_infinities(io, bad):
     out, lse = kda.paged_attention(*c.args(), return_lse=True)
     want, wl, _ = ref.attention(*c.args())
     ok = torch.isfinite(want)
-    assert not ok[..., 7].any() and torch.equal(torch.isfinite(out), ok)
+    assert not ok[..., 7].any() and torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(torch.isinf(out), torch.isinf(want))
     close("finite", out[ok], want[ok], *tol(io, int(ok.sum())))
     assert float((lse.double() - wl).abs().max()) <= 6e-5
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("io", [BF, F32])
-def test_attention_one_chunk_among_empty_sequences(io):
+def test_attention_one_chunk_among_empty_sequences(wide, io):
     """No more tokens than sequences, all of them one sequence's; and offsets that decrease on the device."""
     new = [0] * 60
     new[17] = 41
     cells = [5] * 60
     cells[17] = 400
-    Case(new, cells, 4, 1, 64, 128, io, 16, seed=22).check("one chunk")
-    c = Case([30, 10, 20], [100, 50, 70], 4, 2, 64, 64, io, 16, seed=23)
+    Case(new, cells, 4, 1, 64, 128, io, 16, seed=22, wide=wide).check("one chunk")
+    c = Case([30, 10, 20], [100, 50, 70], 4, 2, 64, 64, io, 16, seed=23, wide=wide)
     c.cu = i32(0, 30, 25, 60)  # the second is empty, the third starts inside the first
     out, lse = kda.paged_attention(*c.args(), return_lse=True)
     torch.cuda.synchronize()
@@ -424,14 +441,14 @@ def test_attention_of_a_large_pool():
     pages, size = 2 ** 31 // (64 * 1024) + 5, 1024  # [pages, 1, 1024, 64] bf16: 4.3 GB
     kp = torch.zeros(pages, 1, size, 64, dtype=BF, device=DEV)
     vp = torch.zeros(pages, 1, size, 64, dtype=BF, device=DEV)
-    table, lens = i32(pages - 1, 0, pages - 3).view(1, 3), i32(2500)
+    table, lens = i32(pages - 1, 0, pages - 3, -1).view(1, 4), i32(2500)
     k, v, q = rnd(g, 1, 2500, 1, 64), rnd(g, 1, 2500, 1, 64), rnd(g, 1, 2500, 2, 64)
     kda.paged_append(k, v, kp, vp, table, lens)
     assert torch.equal(kp[pages - 1, 0], k[0, :1024, 0]) and torch.equal(vp[pages - 3, 0, :452], v[0, 2048:, 0])
     small = [x[[0, pages - 3, pages - 1]].contiguous() for x in (kp, vp)]
     for rows in (q, q[:, -1:].contiguous()):
         a = kda.paged_attention(rows, kp, vp, table, lens)
-        b = kda.paged_attention(rows, *small, i32(2, 0, 1).view(1, 3), lens)
+        b = kda.paged_attention(rows, *small, i32(2, 0, 1, -1).view(1, 4), lens)
         assert torch.equal(a, b)
 
 
