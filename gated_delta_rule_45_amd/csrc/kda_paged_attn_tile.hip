@@ -25,6 +25,8 @@
 // 1 % slower), a bank-free order of the keys (630 -> 615), one base address per load (with one per lane 655, else 600).  Loads
 // between the products cost more than they hide (610).  A workgroup's start (plan,
 // first blocks) is 10,000 of its 140,000 cycles: one fills a CU, so nothing covers it.
+#include <type_traits>
+
 #include "kda_paged_work.h"
 
 namespace kda {
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
     const int token = p.by_G.by(row);
     const uint16_t *x = static_cast<const uint16_t *>(p.q) + (w.seq.t0 + token) * p.ldq + (w.head * p.G + (row - token * p.G)) * DK;
 
-    // ---- staging: load i of a wave covers rows KR (wave + 8 i) .. of the block
+    // ---- staging
     const char *kp = reinterpret_cast<const char *>(static_cast<const uint16_t *>(c.k) + w.head * c.k_head);
     const char *vp = reinterpret_cast<const char *>(static_cast<const uint16_t *>(c.v) + w.head * c.v_head);
     const __attribute__((address_space(4))) int32_t *table =
@@ -243,6 +245,11 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
+    // at most N of this wave's loads are on their way; LDS is touched behind that, not before
+    auto landed = [&](auto n) {
+        wait_vmcnt<decltype(n)::value>();
+        asm volatile("" ::: "memory");
+    };
     // this wave's LDS accesses are done, its loads from memory may be on their way (a fence would wait for those too)
     auto barrier = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
@@ -254,7 +261,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         ek = e1, stage_k(1), mark(1);
         ev = e1, stage_v(1);
         ek = e2, stage_k(2), mark(2);
-        wait_vmcnt<0>();
+        landed(std::integral_constant<int, 0>());
         clear(0, e0);
         ev = e2;  // of block 2, ek: of block 3
         ek = look(3);
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
         settle();
         __builtin_amdgcn_s_setprio(0);
         // the loads that this half iteration started may go on; all others are there for everyone behind the barrier
-        wait_vmcnt<KI + VI>();
+        landed(std::integral_constant<int, KI + VI>());
         clear(t + 1, e1);
         e1 = ev;
         ev = ek;
