@@ -145,6 +145,11 @@ def _pool(t, name: str, like: torch.Tensor):
     return t.shape, s
 
 
+def _shared(block_table) -> bool:
+    """Sequences that share one row of the table (an expanded one)."""
+    return block_table.shape[0] > 1 and block_table.shape[1] > 0 and block_table.stride(0) == 0
+
+
 def _paged(like, B, T, Hq, k_pages, v_pages, block_table, kv_lens, cu_seqlens, lq, lk, lv):
     (pages, Hk, cells, dk), ks = _pool(k_pages, "k_pages", like)
     vshape, vs = _pool(v_pages, "v_pages", like)
@@ -167,7 +172,7 @@ def _paged(like, B, T, Hq, k_pages, v_pages, block_table, kv_lens, cu_seqlens, l
         if block_table.shape[0] != n or block_table.dtype != torch.int32 or block_table.device != like.device or \
                 (most > 1 and block_table.stride(1) != 1):
             _want(block_table, "block_table", torch.int32, (n, most), like)
-        lt = block_table.stride(0) if n > 1 else 0
+        lt = block_table.stride(0) if n > 1 else 0  # (0, sequences that share a row: the caller's to settle, as C reads it as dense)
     p = PagedProblem(B, T, n if cu_seqlens is not None else 0, Hq, Hk, dk, vshape[3], _io_code(like.dtype), cells, most, pages, lt,
                      lq, lk, lv, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
     return p, n
@@ -180,7 +185,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     """Store the new tokens' k [B, T, Hkv, d_k] and v [B, T, Hkv, d_v] in their sequences' pages (written in place).
     With inv_freq (and positions, interleaved, amplitude as for rope; positions None: the token's cell) the keys are
     turned on the way, and the queries q [B, T, Hq, d_k] with them, into q_out (allocated here when None; may be q).
-    A token whose page is not in the pool is not stored.  Returns q_out, or None without q."""
+    A token whose page is not in the pool is not stored.  Sequences that share a row of an expanded block_table are refused.
+    Returns q_out, or None without q."""
     shape, dt = k.shape, k.dtype
     if len(shape) != 4 or len(v.shape) != 4:
         raise ValueError("k and v must be [B, T, heads, d]")
@@ -201,6 +207,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     elif q_out is not None:
         raise ValueError("q_out is given without q")
     p, n = _paged(k, B, T, Hq, k_pages, v_pages, block_table, kv_lens, cu_seqlens, lq, lk, lv)
+    if _shared(block_table):
+        raise ValueError("block_table: sequences share a row, their tokens would share cells")
     if (p.num_heads_kv, p.head_dim_k, p.head_dim_v) != (Hk, dk, v.shape[3]):
         raise ValueError(f"k {tuple(shape)} and v {tuple(v.shape)} do not fit pages of {p.num_heads_kv} heads of "
                          f"{p.head_dim_k} and {p.head_dim_v}")
@@ -221,7 +229,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                     window: int = 0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                     return_lse: bool = False, cu_seqlens_host=None, workspace: Optional[torch.Tensor] = None, stream=None):
     """Attention of the new tokens q [B, T, Hq, d_k] over their sequences' pages, each token over the cells up to its own
-    (the last `window` of them, 0: all).  scale: None for d_k ** -0.5.  workspace: uint8, as long as
+    (the last `window` of them, 0: all).  scale: None for d_k ** -0.5.  block_table may be one row expanded to all sequences
+    (it is copied then).  workspace: uint8, as long as
     kda_paged_attn_workspace says (allocated here when None and needed).  Returns out [B, T, Hq, d_v]; with return_lse, or
     an lse to write, (out, lse [B, T, Hq] fp32: the logarithm of the summed weights, -inf for a row without cells)."""
     shape, dt = q.shape, q.dtype
@@ -234,6 +243,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         raise ValueError(f"q has heads of {dk}, the pages keys of {p.head_dim_k}")
     host, lib, want = _host_i32(cu_seqlens_host, n + 1, "cu_seqlens_host"), library(), (B, T, Hq, p.head_dim_v)
     with _Launch(q.device, stream) as handle:
+        if _shared(block_table):
+            block_table = block_table.contiguous()
         if out is None:
             out = q.new_empty(want)
         else:
