@@ -240,12 +240,14 @@ kda_status_t plan_launch(const kda_paged_problem_t *p, const Shape &s, bool pack
     l.most = most;
     const int64_t Hk = p->num_heads_kv, target = (int64_t)cus * l.t.target_per_cu;
     l.target = (int32_t)target;
-    // No tile is worth splitting: it has few blocks; or they are not many and there are tiles enough; or the blocks that a
-    // plain batch's own tokens fill make parts so long that the kernel would not cut any (without the plan, which costs
+    // No tile is worth splitting: it has few blocks; or they are not many and there are tiles enough; or the blocks of a plain
+    // batch's own tokens that its tiles see make parts so long that the kernel would not cut any (without the plan, which costs
     // each workgroup 2 us, and the join, 4 us a call: 4 x 4,096 x 32 heads 577 -> 565 us, 96 x 4 drafted tokens 79 -> 72).
+    // Each of the three holds for every window where it holds without one, and parts of fewer blocks take no more room: so
+    // the query, which has no window, counts enough for all of them.
     const bool counted = !packed || cu_host;
-    const int64_t own = packed ? 0 : tiles * ((std::min<int64_t>(p->seq_len, cells) + KB - 1) / KB);
-    if (most <= l.t.c_min || (counted && tiles * Hk >= target && most <= kFewBlocks) || (window == 0 && own * Hk >= most * target)) {
+    const int64_t own = packed ? 0 : tiles * std::min(most, (std::min<int64_t>(p->seq_len, cells) + KB - 1) / KB);
+    if (most <= l.t.c_min || (counted && tiles * Hk >= target && most <= kFewBlocks) || (!packed && own * Hk >= most * target)) {
         l.c_min = packed ? (int32_t)std::max<int64_t>(most, 1) : 0;
         l.blocks = tiles * Hk;
     } else {

@@ -1,5 +1,5 @@
-"""Calls of the paged cache that its users make beside the plain ones: tables that share a row.  Against the same calls
-on copies and the fp64 reference (paged_reference.py), with the tolerances of test_gpu_paged.py."""
+"""Calls of the paged cache that its users make beside the plain ones: tables that share a row, windows over prompts.  Against
+the same calls on copies and the fp64 reference (paged_reference.py), with the tolerances of test_gpu_paged.py."""
 import pytest
 import torch
 
@@ -25,3 +25,19 @@ def test_sequences_that_share_a_context(io, new):
     out = kda.paged_attention(*c.args(), stream=s)  # the copy is made on the call's stream
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("io,new,cells,Hq,Hk,window,wide", [
+    (BF, 2048, [2048, 2048], 32, 8, 1024, False),  # every tile a workgroup: no room is needed
+    (BF, 2048, [2048, 2040], 32, 8, 1024, True),
+    (F32, 2200, [2200], 4, 4, 2100, False),
+    (BF, 600, [4000], 8, 2, 1500, True),           # parts and their join
+    (F32, 100, [3000, 2900], 2, 1, 1500, True),
+])
+def test_plain_prompts_under_a_window(io, new, cells, Hq, Hk, window, wide):
+    """Without a workspace of the caller's: the binding asks for the room of the problem, which has no window."""
+    say(f"[window {window} over {new} of {cells}, {io}]")
+    c = Case([new] * len(cells), cells, Hq, Hk, 64, 128, io, 64, seed=42, packed=False, wide=wide)
+    out, lse = c.check("prompts", window=window)
+    again, l2 = kda.paged_attention(*c.args(), window=window, return_lse=True)
+    assert torch.equal(out, again) and torch.equal(lse, l2)

@@ -1,0 +1,73 @@
+"""The room that kda_paged_attn_workspace names is enough for every call on the problem.  The calls get addresses that are never
+read: without a GPU they end at the launch at the latest, and where there is one these tests do not run."""
+import ctypes
+import os
+import random
+
+import pytest
+
+import gated_delta_rule_45_amd as kda
+from gated_delta_rule_45_amd.paged import PagedProblem
+
+pytestmark = pytest.mark.skipif(os.path.exists("/dev/kfd"), reason="launches on made-up addresses: only without a GPU")
+
+at = lambda i: ctypes.c_void_p(0x100000000000 * (i + 1))  # noqa: E731  aligned, far apart
+
+
+def problem(batch, T, Hq, Hk, dk, dv, io, page, pages, num_seqs=0):
+    return PagedProblem(batch, T, num_seqs, Hq, Hk, dk, dv, io, page, pages, 1 << 14)
+
+
+def room(p):
+    n = ctypes.c_size_t(7)
+    assert kda.library().kda_paged_attn_workspace(ctypes.byref(p), ctypes.byref(n)) == kda.KDA_OK
+    return n.value
+
+
+def call(p, size, window=0, cu=False, host=None):
+    """Status and message of a call with so many bytes of workspace."""
+    lib = kda.library()
+    if host is not None:
+        host = (ctypes.c_int32 * len(host))(*host)
+    st = lib.kda_paged_attn(ctypes.byref(p), at(0), at(1), at(2), at(3), at(4), at(5) if cu else None, host, 1.0, window, at(6), None,
+                            at(7) if size else None, size, None)
+    return st, lib.kda_last_error().decode()
+
+
+def enough(p, **kw):
+    st, message = call(p, room(p), **kw)
+    assert st == kda.KDA_ERR_HIP, (message, [(n, getattr(p, n)) for n, _ in p._fields_], kw)
+
+
+@pytest.mark.parametrize("T,N,Hq,Hk,d,io,page,pages,window", [
+    (4096, 4, 32, 8, 128, kda.KDA_BF16, 64, 66, 1024), (8192, 1, 32, 8, 128, kda.KDA_BF16, 64, 130, 1024),
+    (16384, 1, 32, 8, 128, kda.KDA_BF16, 64, 258, 4096), (1024, 6, 32, 8, 128, kda.KDA_BF16, 64, 18, 1000),
+    (1024, 6, 32, 8, 128, kda.KDA_BF16, 64, 18, 1100), (4096, 4, 16, 4, 64, kda.KDA_F32, 64, 66, 2047),
+])
+def test_prompts_under_a_window(T, N, Hq, Hk, d, io, page, pages, window):
+    p = problem(N, T, Hq, Hk, d, d, io, page, pages)
+    for w in (0, 1, window - 1, window, 2 * window, 2 ** 31 - 1):
+        enough(p, window=w)
+
+
+def log(rng, a, b):
+    return int(round(a * (b / a) ** rng.random()))
+
+
+def draw(rng, packed):
+    hk = rng.choice([1, 2, 3, 4, 8, 16, 64, 300, 600])
+    tokens, n = log(rng, 1, 20000), log(rng, 1, 600)
+    shape = (1, tokens) if packed else (n, max(1, tokens // n))
+    return problem(*shape, hk * rng.choice([1, 2, 4, 5, 8]), hk, rng.choice([64, 128]), rng.choice([64, 128]),
+                   rng.choice([kda.KDA_BF16, kda.KDA_F32]), rng.choice([16, 64, 256]), log(rng, 1, 4000), n if packed else 0)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_any_window(packed):
+    rng, reached = random.Random(11 + packed), 0
+    for _ in range(6000):
+        p = draw(rng, packed)
+        cells = p.max_pages * p.page_size
+        enough(p, window=rng.choice([0, log(rng, 1, 2 * cells), log(rng, 1, 5000)]), cu=packed)
+        reached += room(p) > 0
+    assert reached > 1000
