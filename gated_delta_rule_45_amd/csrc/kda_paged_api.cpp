@@ -222,8 +222,9 @@ struct Launch {
 
 constexpr int64_t kFewBlocks = 16;
 
+// room: bytes of workspace that the launch may take; it cuts its tiles into fewer parts to stay within them.
 kda_status_t plan_launch(const kda_paged_problem_t *p, const Shape &s, bool packed, const int32_t *cu_host, int32_t window,
-                         int cus, Launch &l) {
+                         int cus, size_t room, Launch &l) {
     const int64_t M = l.t.M, KB = l.t.KB, cells = p->num_pages > 0 ? (int64_t)p->max_pages * p->page_size : 0;
     int64_t tiles = 0;  // of a head, at most
     auto count = [&](int64_t len) { return len * s.G >= l.rows_lo && len * s.G <= l.rows_hi ? (len * s.G + M - 1) / M : 0; };
@@ -238,8 +239,8 @@ kda_status_t plan_launch(const kda_paged_problem_t *p, const Shape &s, bool pack
     int64_t most = (cells + KB - 1) / KB;  // blocks of a tile, at most
     if (window > 0) most = std::min(most, ((int64_t)window + (M - 1) / s.G + 1 + KB - 1) / KB + 1);
     l.most = most;
-    const int64_t Hk = p->num_heads_kv, target = (int64_t)cus * l.t.target_per_cu;
-    l.target = (int32_t)target;
+    const int64_t Hk = p->num_heads_kv;
+    int64_t target = (int64_t)cus * l.t.target_per_cu;
     // No tile is worth splitting: it has few blocks; or they are not many and there are tiles enough; or the blocks of a plain
     // batch's own tokens that its tiles see make parts so long that the kernel would not cut any (without the plan, which costs
     // each workgroup 2 us, and the join, 4 us a call: 4 x 4,096 x 32 heads 577 -> 565 us, 96 x 4 drafted tokens 79 -> 72).
@@ -253,15 +254,25 @@ kda_status_t plan_launch(const kda_paged_problem_t *p, const Shape &s, bool pack
     } else {
         const int64_t each = (most + l.t.c_min - 1) / l.t.c_min;  // parts of a tile, at most
         l.c_min = l.t.c_min;
-        // parts are at least sum / target blocks long: all tiles have at most one part more than target / Hk together; a split
-        // tile has more than one part's blocks, hence at most twice as many parts as blocks / part
-        l.blocks = std::min(target / Hk + tiles, tiles * each) * Hk;
-        l.tiles = std::min(target / Hk, tiles);
-        l.slots = std::min(2 * target / Hk, tiles * each);
-        if (tiles == 0 || l.slots < 2) l.tiles = l.slots = 0;
-        l.desc = (size_t)((1 + l.tiles * Hk) * kda::paged::kDesc * 4 + 255) / 256 * 256;
-        l.part = (size_t)(l.slots * Hk * M * (p->head_dim_v + 2) * 4 + 255) / 256 * 256;
+        for (;; target /= 2) {
+            // parts are at least sum / target blocks long: all tiles have at most one part more than target / Hk together; a split
+            // tile has more than one part's blocks, hence at most twice as many parts as blocks / part
+            l.blocks = std::min(target / Hk + tiles, tiles * each) * Hk;
+            l.tiles = std::min(target / Hk, tiles);
+            l.slots = std::min(2 * target / Hk, tiles * each);
+            if (tiles == 0 || l.slots < 2) l.tiles = l.slots = 0;
+            l.desc = (size_t)((1 + l.tiles * Hk) * kda::paged::kDesc * 4 + 255) / 256 * 256;
+            l.part = (size_t)(l.slots * Hk * M * (p->head_dim_v + 2) * 4 + 255) / 256 * 256;
+            if (l.desc + l.part <= room || target <= 1) break;
+        }
+        if (l.desc + l.part > room) {  // none: tiles of up to `most` blocks are one part
+            l.c_min = (int32_t)std::max<int64_t>(most, 1);
+            l.blocks = tiles * Hk;
+            l.tiles = l.slots = 0;
+            l.desc = l.part = 0;
+        }
     }
+    l.target = (int32_t)target;
     if (l.blocks > kMostItems / 256 || l.tiles * Hk * M > kMostItems / 256)
         return set_error(KDA_ERR_UNSUPPORTED, "too many rows: %lld workgroups", (long long)l.blocks);
     return KDA_OK;
@@ -291,7 +302,7 @@ int32_t few_rows(int64_t num_seqs, int64_t heads_kv, int64_t rows, int64_t cells
 }
 
 kda_status_t plan_attn(const kda_paged_problem_t *p, const Shape &s, bool packed, const int32_t *cu_host, int32_t window, int cus,
-                       AttnPlan &a) {
+                       size_t room, AttnPlan &a) {
     a = AttnPlan{};
     const bool bf16 = p->io_dtype == KDA_BF16;
     const int32_t few = few_rows(s.num_seqs, p->num_heads_kv, s.tokens * s.G, p->num_pages > 0 ? (int64_t)p->max_pages * p->page_size : 0);
@@ -301,13 +312,33 @@ kda_status_t plan_attn(const kda_paged_problem_t *p, const Shape &s, bool packed
         l.t = tile ? kda::paged::attn_tile_tile() : kda::paged::attn_rows_tile(bf16);
         if (tile) l.rows_lo = few + 1;
         if (both && !tile) l.rows_hi = few;
-        const kda_status_t st = plan_launch(p, s, packed, cu_host, window, cus, l);
+        const kda_status_t st = plan_launch(p, s, packed, cu_host, window, cus, room, l);
         if (st != KDA_OK) return st;
         if (l.blocks == 0) continue;
-        a.bytes += l.desc + l.part;
+        a.bytes = std::max(a.bytes, l.desc + l.part);  // one after the other, in the same room
         a.tile[a.n] = tile;
         a.part[a.n++] = l;
     }
+    return KDA_OK;
+}
+
+// Room for the problem as a plain batch and, where it can be one, as a packed one, whatever lengths, window and host offsets.
+// Only offsets on the host can need more than the plans without a window and without them: in a batch of no more tokens than
+// sequences they may show rows for a second launch.  That one stays within this room (or the caller's, if it is larger), rather
+// than have every step of single tokens ask for eight times as much (64 sequences over 8,192 cells, 32 / 8 heads of 128: 17 MB,
+// 136 with it).
+kda_status_t room_of(const kda_paged_problem_t *p, int cus, size_t &room) {
+    size_t need = 0;
+    for (int packed = 0; packed < 2; ++packed) {
+        if (packed && (!p || p->batch != 1 || p->num_seqs <= 0)) break;
+        Shape s;
+        AttnPlan a;
+        kda_status_t st = check_shape(p, packed, s);
+        if (st == KDA_OK) st = plan_attn(p, s, packed, nullptr, 0, cus, SIZE_MAX, a);
+        if (st != KDA_OK) return st;
+        need = std::max(need, a.bytes);
+    }
+    room = need;
     return KDA_OK;
 }
 
@@ -468,17 +499,9 @@ kda_status_t kda_paged_attn_workspace(const kda_paged_problem_t *p, size_t *byte
     if (!bytes) return set_error(KDA_ERR_INVALID_ARGUMENT, "bytes is NULL");
     *bytes = 0;
     try {
-        const int cus = current_cus();
         size_t need = 0;
-        for (int packed = 0; packed < 2; ++packed) {
-            if (packed && (!p || p->batch != 1 || p->num_seqs <= 0)) break;
-            Shape s;
-            AttnPlan a;
-            kda_status_t st = check_shape(p, packed, s);
-            if (st == KDA_OK) st = plan_attn(p, s, packed, nullptr, 0, cus, a);
-            if (st != KDA_OK) return st;
-            need = std::max(need, a.bytes);
-        }
+        const kda_status_t st = room_of(p, current_cus(), need);
+        if (st != KDA_OK) return st;
         *bytes = need;
         return done(hipSuccess, "");
     } catch (...) {
@@ -511,8 +534,11 @@ kda_status_t kda_paged_attn(const kda_paged_problem_t *p, const void *q, const v
         st = check_runs(args);
         if (st == KDA_OK) st = check_offsets(p->seq_len, s.num_seqs, cu_seqlens, cu_seqlens_host);
         if (st != KDA_OK) return st;
-        AttnPlan a;  // asks for the device's CUs
-        st = plan_attn(p, s, cu_seqlens != nullptr, cu_seqlens_host, window, current_cus(), a);
+        AttnPlan a;
+        const int cus = current_cus();
+        size_t room = SIZE_MAX;  // (kept where the query refuses the problem: exact offsets may name fewer workgroups than it counts)
+        if (cu_seqlens_host && room_of(p, cus, room) == KDA_OK) room = std::max(room, workspace_bytes);
+        st = plan_attn(p, s, cu_seqlens != nullptr, cu_seqlens_host, window, cus, room, a);
         if (st != KDA_OK) return st;
         args[8].run = (int64_t)a.bytes;
         st = check_runs(args);
@@ -541,7 +567,7 @@ kda_status_t kda_paged_attn(const kda_paged_problem_t *p, const void *q, const v
         r.flip = std::signbit(scale);
         const bool bf16 = p->io_dtype == KDA_BF16;
         hipStream_t hs = static_cast<hipStream_t>(stream);
-        char *ws = static_cast<char *>(workspace);
+        char *const ws = static_cast<char *>(workspace);
         for (int i = 0; i < a.n; ++i) {
             const Launch &l = a.part[i];
             // fp32 heads of 128: two workgroups of 237 registers on a CU suit single rows and short contexts, whose
@@ -561,7 +587,6 @@ kda_status_t kda_paged_attn(const kda_paged_problem_t *p, const void *q, const v
             if (st == KDA_OK && l.tiles > 0)
                 st = done(kda::paged::launch_attn_join(bf16, r, l.t.M, l.tiles, hs), "kda_paged_attn join launch");
             if (st != KDA_OK) return st;
-            ws += l.desc + l.part;
         }
         return done(hipSuccess, "");
     } catch (...) {

@@ -641,7 +641,9 @@ kda_status_t kda_paged_attn(const kda_paged_problem_t *problem, const void *q, c
                             void *workspace, size_t workspace_bytes, void *stream);
 
 /* Workspace bytes kda_paged_attn needs for the problem on the current device, as a plain batch and, where batch is 1 and
- * num_seqs > 0, also as a packed one, whatever the lengths; *bytes = 0 on error. */
+ * num_seqs > 0, also as a packed one, whatever the lengths, the window and cu_seqlens_host; *bytes = 0 on error.  (In a batch
+ * of no more tokens than sequences that cu_seqlens_host shows to hold long ones, their rows are cut into as many parts as this
+ * room, or the call's if it is larger, has place for.) */
 kda_status_t kda_paged_attn_workspace(const kda_paged_problem_t *problem, size_t *bytes);
 
 /* Static description of a status code. */

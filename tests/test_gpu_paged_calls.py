@@ -1,5 +1,6 @@
-"""Calls of the paged cache that its users make beside the plain ones: tables that share a row, windows over prompts.  Against
-the same calls on copies and the fp64 reference (paged_reference.py), with the tolerances of test_gpu_paged.py."""
+"""Calls of the paged cache that its users make beside the plain ones: tables that share a row, windows over prompts, offsets
+known on the host.  Against the same calls on copies and the fp64 reference (paged_reference.py), with the tolerances of
+test_gpu_paged.py."""
 import pytest
 import torch
 
@@ -41,3 +42,31 @@ def test_plain_prompts_under_a_window(io, new, cells, Hq, Hk, window, wide):
     out, lse = c.check("prompts", window=window)
     again, l2 = kda.paged_attention(*c.args(), window=window, return_lse=True)
     assert torch.equal(out, again) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("new,cells,Hq,Hk", [
+    ([1] * 10 + [90] + [0] * 117, [(i * 331) % 4000 for i in range(10)] + [4000] + [0] * 117, 32, 8),
+    ([24] + [1] * 30 + [0] * 30, [2000] + [(i * 577) % 1900 for i in range(30)] + [0] * 30, 32, 8),
+    ([0] * 300 + [300], [0] * 300 + [5000], 4, 1),
+    ([64] * 2 + [0] * 126, [3000, 2000] + [0] * 126, 48, 48),  # not as many parts as without a limit to their room
+])
+@pytest.mark.parametrize("window", [0, 700])
+def test_long_sequences_among_single_tokens_by_host_offsets(new, cells, Hq, Hk, window):
+    """No more tokens than sequences: one launch, and two that share their room where the host's offsets show long sequences."""
+    say(f"[{sum(new)} tokens in {len(new)} sequences, {Hq}/{Hk} heads, window {window}]")
+    c = Case(new, cells, Hq, Hk, 64, 128, BF, 64, seed=43, packed=True)
+    host = c.cu.cpu()
+    c.check("without", window=window)
+    out, lse = c.check("with", window=window, cu_seqlens_host=host)
+    again, l2 = kda.paged_attention(*c.args(), window=window, return_lse=True, cu_seqlens_host=host)
+    assert torch.equal(out, again) and torch.equal(lse, l2)
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    a, b = torch.empty_like(out), torch.empty_like(lse)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        kda.paged_attention(*c.args(), window=window, out=a, lse=b, cu_seqlens_host=host)
+    for i in range(3):
+        a.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, out) and torch.equal(b, lse), i

@@ -71,3 +71,33 @@ def test_any_window(packed):
         enough(p, window=rng.choice([0, log(rng, 1, 2 * cells), log(rng, 1, 5000)]), cu=packed)
         reached += room(p) > 0
     assert reached > 1000
+
+
+def offsets(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+@pytest.mark.parametrize("pages", [4, 16, 64, 128, 512, 2048])
+@pytest.mark.parametrize("lens", [[24] + [1] * 30 + [0] * 30, [1] * 10 + [90] + [0] * 117, [0] * 500 + [500], [64] * 8 + [0] * 504])
+def test_long_sequences_among_empty_ones_by_host_offsets(lens, pages):
+    """No more tokens than sequences: without host offsets one launch, with them two."""
+    for hq, hk in ((32, 8), (4, 1), (96, 96)):
+        p = problem(1, sum(lens), hq, hk, 128, 128, kda.KDA_BF16, 64, pages, len(lens))
+        for window in (0, 700):
+            enough(p, cu=True, host=offsets(lens), window=window)
+            enough(p, cu=True, window=window)
+
+
+def test_any_host_offsets():
+    rng, few = random.Random(13), 0
+    for _ in range(6000):
+        p = draw(rng, True)
+        cut = sorted(rng.randint(0, p.seq_len) for _ in range(p.num_seqs - 1))
+        if rng.random() < 0.5:  # some sequences hold all tokens
+            cut = sorted(rng.choice(cut[:3] or [0]) for _ in cut)
+        enough(p, cu=True, host=[0, *cut, p.seq_len], window=rng.choice([0, 0, log(rng, 1, 5000)]))
+        few += p.seq_len <= p.num_seqs and p.io_dtype == kda.KDA_BF16
+    assert few > 500
