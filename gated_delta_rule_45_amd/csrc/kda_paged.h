@@ -87,7 +87,7 @@ constexpr int kDesc = 8;
 
 // Shape of a kernel's tiles.
 struct AttnTile {
-    int32_t M, KB, c_min, target_per_cu;
+    int32_t M, KB, c_min, target_per_cu, threads;
 };
 AttnTile attn_rows_tile(bool bf16);
 // many: fp32 calls of many rows over long contexts, see the host's choice

@@ -273,7 +273,7 @@ kda_status_t plan_launch(const kda_paged_problem_t *p, const Shape &s, bool pack
         }
     }
     l.target = (int32_t)target;
-    if (l.blocks > kMostItems / 256 || l.tiles * Hk * M > kMostItems / 256)
+    if (l.blocks > kMostItems / l.t.threads || l.tiles * Hk * M > kMostItems / 256)
         return set_error(KDA_ERR_UNSUPPORTED, "too many rows: %lld workgroups", (long long)l.blocks);
     return KDA_OK;
 }

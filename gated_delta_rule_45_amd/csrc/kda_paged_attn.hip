@@ -426,7 +426,7 @@ hipError_t join(const AttnParams &p, int M, int64_t tiles, hipStream_t s) {
 // block takes twice as long (1,002 cells 16.0 -> 13.0 us); for two workgroups per CU: one leaves the ends of ragged batches to few (220
 // us instead of 205), three make more parts than the cache's bandwidth needs (131,072 cells: 94 us instead of 89, the
 // batch 200).  Three workgroups of the bf16 kernel fit a CU.
-AttnTile attn_rows_tile(bool bf16) { return {kM, kKB, bf16 ? 2 : 1, 2}; }
+AttnTile attn_rows_tile(bool bf16) { return {kM, kKB, bf16 ? 2 : 1, 2, 256}; }
 
 hipError_t launch_attn_rows(bool bf16, bool many, const AttnParams &p, int64_t blocks, hipStream_t stream) {
     if (blocks <= 0) return hipSuccess;

@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kNT, 1) attn_tile_kernel(AttnParams p) {
 
 // Parts of at least eight blocks, 512 cells: a part's sums (256 rows of d_v fp32) are then small beside its work (1 x 1,024 tokens:
 // 40 us, of at least four blocks 52); for two workgroups per CU, although one fills it (one: attention of chunks 664 us instead of 650)
-AttnTile attn_tile_tile() { return {kM, kKB, 8, 2}; }
+AttnTile attn_tile_tile() { return {kM, kKB, 8, 2, kNT}; }
 
 hipError_t launch_attn_tile(const AttnParams &p, int64_t blocks, hipStream_t s) {
     if (blocks <= 0) return hipSuccess;

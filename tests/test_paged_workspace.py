@@ -101,3 +101,18 @@ def test_any_host_offsets():
         enough(p, cu=True, host=[0, *cut, p.seq_len], window=rng.choice([0, 0, log(rng, 1, 5000)]))
         few += p.seq_len <= p.num_seqs and p.io_dtype == kda.KDA_BF16
     assert few > 500
+
+
+@pytest.mark.parametrize("io,T,Hk,most", [(kda.KDA_BF16, 33, 8, (2 ** 32 - 1) // 512 // 8),  # tiles of 256 rows, 512 threads
+                                          (kda.KDA_F32, 16, 8, (2 ** 32 - 1) // 256 // 8)])  # of 16 rows, 256 threads
+def test_more_workgroups_than_a_launch_has(io, T, Hk, most):
+    """A tile a sequence and head; the work-items of a launch are at most 2^32 - 1."""
+    enough(problem(most, T, Hk, Hk, 64, 64, io, 64, 64))
+    for n in (most + 1, most + most // 2):
+        p, size = problem(n, T, Hk, Hk, 64, 64, io, 64, 64), ctypes.c_size_t(7)
+        if n * T * Hk >= 2 ** 31:
+            continue
+        assert kda.library().kda_paged_attn_workspace(ctypes.byref(p), ctypes.byref(size)) == kda.KDA_ERR_UNSUPPORTED
+        assert size.value == 0
+        st, message = call(p, 1 << 40)
+        assert st == kda.KDA_ERR_UNSUPPORTED and "workgroups" in message
