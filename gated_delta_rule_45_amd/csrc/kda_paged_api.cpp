@@ -24,7 +24,8 @@ struct Runs {
     int64_t run, step, n;
     size_t align;
     bool needed, written;
-    int twin = -1;  // index of the argument that may be the same runs
+    int twin = -1;   // index of the argument that may be the same runs
+    int apart = -1;  // of one that they are compared with elsewhere
     uintptr_t begin() const { return reinterpret_cast<uintptr_t>(p); }
     uintptr_t end() const { return begin() + (uintptr_t)((n - 1) * step + run); }
     bool empty() const { return !p || n <= 0 || run <= 0; }
@@ -49,7 +50,7 @@ kda_status_t check_runs(const Runs (&a)[N]) {
     for (int i = 0; i < N; ++i) {
         if (!a[i].written || a[i].empty()) continue;
         for (int j = 0; j < N; ++j) {
-            if (j == i || a[j].empty()) continue;
+            if (j == i || a[j].empty() || a[i].apart == j || a[j].apart == i) continue;
             if ((a[i].twin == j || a[j].twin == i) && a[i].p == a[j].p && (a[i].step == a[j].step || a[i].n <= 1)) continue;
             if (meet(a[i], a[j])) return set_error(KDA_ERR_INVALID_ARGUMENT, "%s aliases %s", a[i].name, a[j].name);
         }
@@ -134,6 +135,37 @@ Runs pool_runs(const char *name, const void *x, const kda_paged_problem_t *p, co
     return {name, x, run, step, p->num_pages, 16, true, written};
 }
 
+// Whether a cell of one pool may share a byte with one of the other, which starts `apart` bytes behind it.  Strides nest
+// (pool_strides), so from the widest axis in, cells can only meet for one or two differences of their indexes.  Those are
+// followed while the pools have the axis and its stride in common, as slices of one tensor do; behind that a pool's
+// remaining axes count as one run.
+struct Pool {
+    int64_t stride[3], run;  // bytes; stride 0: an axis of one entry, or one that has been followed
+};
+bool pools_meet(const int64_t (&size)[3], const Pool &a, const Pool &b, int64_t apart) {
+    int64_t reach[2];  // bytes from the first to the last
+    int widest[2];
+    for (int x = 0; x < 2; ++x) {
+        const Pool &p = x ? b : a;
+        reach[x] = p.run;
+        widest[x] = 0;
+        for (int i = 0; i < 3; ++i) {
+            reach[x] += p.stride[i] * (size[i] - 1);
+            if (p.stride[i] > p.stride[widest[x]]) widest[x] = i;
+        }
+    }
+    if (apart >= reach[0] || apart <= -reach[1]) return false;
+    const int i = widest[0];
+    const int64_t step = a.stride[i];
+    if (step == 0 || i != widest[1] || b.stride[i] != step) return true;
+    Pool c = a, d = b;
+    c.stride[i] = d.stride[i] = 0;
+    int64_t more = apart / step;  // indexes that the first is ahead of the second
+    if (apart % step < 0) --more;
+    for (int64_t n = more; n <= more + 1; ++n)
+        if (n < size[i] && -n < size[i] && pools_meet(size, c, d, apart - n * step)) return true;
+    return false;
+}
 kda_status_t check_shape(const kda_paged_problem_t *p, bool packed, Shape &s) {
     if (!p) return set_error(KDA_ERR_INVALID_ARGUMENT, "problem is NULL");
     if (p->batch < 0 || p->seq_len < 0 || p->num_heads_q < 1 || p->num_heads_kv < 1)
@@ -180,6 +212,20 @@ kda_status_t check_shape(const kda_paged_problem_t *p, bool packed, Shape &s) {
     if (st == KDA_OK) st = pool_strides("k_pages", p, s.io, p->head_dim_k, kg, s.kp);
     if (st == KDA_OK) st = pool_strides("v_pages", p, s.io, p->head_dim_v, vg, s.vp);
     return st;
+}
+
+// Keys and values, both to be written, in memory of their own.
+kda_status_t check_pools(const kda_paged_problem_t *p, const Shape &s, const void *k, const void *v) {
+    if (p->num_pages == 0) return KDA_OK;
+    const int64_t size[3] = {p->num_pages, p->num_heads_kv, p->page_size};
+    Pool a{{}, p->head_dim_k * s.io}, b{{}, p->head_dim_v * s.io};
+    for (int i = 0; i < 3; ++i) {
+        a.stride[i] = s.kp[i] * s.io;
+        b.stride[i] = s.vp[i] * s.io;
+    }
+    if (pools_meet(size, a, b, (int64_t)(reinterpret_cast<uintptr_t>(v) - reinterpret_cast<uintptr_t>(k))))
+        return set_error(KDA_ERR_INVALID_ARGUMENT, "k_pages aliases v_pages");
+    return KDA_OK;
 }
 
 Runs table_runs(const kda_paged_problem_t *p, const Shape &s, const int32_t *t) {
@@ -456,7 +502,7 @@ kda_status_t kda_paged_append(const kda_paged_problem_t *p, const void *k, const
             return set_error(KDA_ERR_UNSUPPORTED, "too many rows: %lld tokens", (long long)s.tokens);
         const bool turned = rope && rope->rot_dim > 0;
         const int64_t ldqo = q_out && q_out == q ? s.ldq : s.q_row;
-        const Runs args[] = {
+        Runs args[] = {
             {"k", k, s.k_row * s.io, s.ldk * s.io, s.tokens, 16, true, false},
             {"v", v, s.v_row * s.io, s.ldv * s.io, s.tokens, 16, true, false},
             {"q", q, s.q_row * s.io, s.ldq * s.io, s.tokens, 16, false, false},
@@ -469,7 +515,9 @@ kda_status_t kda_paged_append(const kda_paged_problem_t *p, const void *k, const
             pool_runs("k_pages", k_pages, p, s.kp, p->head_dim_k, s.io, true),
             pool_runs("v_pages", v_pages, p, s.vp, p->head_dim_v, s.io, true),
         };
+        args[9].apart = 10;
         st = check_runs(args);
+        if (st == KDA_OK) st = check_pools(p, s, k_pages, v_pages);
         if (st == KDA_OK) st = check_offsets(p->seq_len, s.num_seqs, cu_seqlens, cu_seqlens_host);
         if (st != KDA_OK) return st;
         if (s.num_seqs == 0 || s.tokens == 0) return done(hipSuccess, "");

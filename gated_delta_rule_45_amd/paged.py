@@ -6,8 +6,8 @@ for the kda_rope* and kda_paged_* entry points of libkda.so.
     paged_attention softmax attention of the new tokens, one or many per sequence, over those pages
 
 Query head h of Hq reads key-value head h // (Hq // Hkv).  Pages: [num_pages, Hkv, page_size, d], a view of any order
-in memory whose last axis is dense (pages that hold cells first: pages.transpose(1, 2)), page_size a power of two from
-16 on.  block_table: int32 [N, max_pages]; cell p of sequence n is cell p % page_size of page block_table[n, p //
+in memory whose last axis is dense (pages that hold cells first: pages.transpose(1, 2); keys and values may be slices of one
+tensor), page_size a power of two from 16 on.  block_table: int32 [N, max_pages]; cell p of sequence n is cell p % page_size of page block_table[n, p //
 page_size].  kv_lens: int32 [N], the cells of each sequence WITH its new tokens, for both calls: the i-th of `new`
 tokens is cell kv_lens[n] - new + i.  A plain batch is q, k, v [N, T, heads, d], T new tokens each; a packed one
 [1, tokens, heads, d] with cu_seqlens int32 [N + 1].  q, k and v may be slices of one projection's output.

@@ -603,7 +603,8 @@ typedef struct {
  *  kv_lens       int32 [num_seqs]: cells of each sequence with the new tokens, so that the same array goes to
  *                kda_paged_attn
  *  cu_seqlens, cu_seqlens_host   as for kda_gdn_chunk_fwd
- *  k_pages, v_pages   the pools; they may be slices of one tensor that holds a page's keys next to its values
+ *  k_pages, v_pages   the pools; they may be slices of one tensor that holds keys next to values by pages, heads or cells
+ *                (with one stride for the axes from there out)
  * A token whose cell would be negative is padding: nothing is read or written for it.  One whose page is not in
  * [0, num_pages), or behind max_pages, is not stored (its query is turned).  Two tokens must not share a cell.
  * Errors as for kda_chunk_fwd; nothing is allocated.

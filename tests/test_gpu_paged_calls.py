@@ -1,11 +1,11 @@
 """Calls of the paged cache that its users make beside the plain ones: tables that share a row, windows over prompts, offsets
-known on the host.  Against the same calls on copies and the fp64 reference (paged_reference.py), with the tolerances of
-test_gpu_paged.py."""
+known on the host, keys beside values in a page.  Against the same calls on copies and the fp64 reference
+(paged_reference.py), with the tolerances of test_gpu_paged.py."""
 import pytest
 import torch
 
 import gated_delta_rule_45_amd as kda
-from test_gpu_paged import BF, F32, Case, say
+from test_gpu_paged import BF, DEV, F32, Case, gen, rnd, say
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +70,39 @@ def test_long_sequences_among_single_tokens_by_host_offsets(new, cells, Hq, Hk, 
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(a, out) and torch.equal(b, lse), i
+
+
+def beside(layout, pages, heads, size, dk, dv, io):
+    """Keys and values [pages, heads, size, d] as slices of one tensor."""
+    if layout == "cell":      # a head's key, then its value
+        x = torch.zeros(pages, heads, size, dk + dv, dtype=io, device=DEV)
+        return x[..., :dk], x[..., dk:]
+    if layout == "cells first":
+        x = torch.zeros(pages, size, heads, dk + dv, dtype=io, device=DEV).transpose(1, 2)
+        return x[..., :dk], x[..., dk:]
+    if layout == "heads":     # all keys of a cell, then all values
+        x = torch.zeros(pages, size, heads * (dk + dv), dtype=io, device=DEV)
+        return (t.unflatten(-1, (heads, -1)).transpose(1, 2) for t in (x[..., :heads * dk], x[..., heads * dk:]))
+    x = torch.zeros(pages, heads, size * (dk + dv), dtype=io, device=DEV)  # all keys of a head in a page, then its values
+    return (t.unflatten(-1, (size, -1)) for t in (x[..., :size * dk], x[..., size * dk:]))
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("layout", ["cell", "cells first", "heads", "head"])
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 128)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_keys_beside_values_in_a_page(io, layout, dk, dv, wide):
+    """Appended to and read where keys and values are slices of one tensor, as in pools of their own."""
+    say(f"[{layout}, {dk}x{dv}, {io}]")
+    c = Case([70, 1, 3], [300, 41, 90], 4, 2, dk, dv, io, 32, seed=44, wide=wide)
+    g = gen(45)
+    k, v = rnd(g, 1, 74, 2, dk, dtype=io), rnd(g, 1, 74, 2, dv, dtype=io)
+    kp, vp = beside(layout, c.kp.shape[0], 2, 32, dk, dv, io)
+    kp.copy_(c.kp), vp.copy_(c.vp)
+    for pools in ((kp, vp), (c.kp, c.vp)):
+        kda.paged_append(k, v, *pools, c.table, c.lens, c.cu)
+    assert torch.equal(kp, c.kp) and torch.equal(vp, c.vp)
+    want = kda.paged_attention(*c.args())
+    c.kp, c.vp = kp, vp
+    out, _ = c.check(layout)
+    assert torch.equal(out, want)
