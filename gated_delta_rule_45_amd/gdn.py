@@ -46,6 +46,13 @@ def declare(lib: ctypes.CDLL) -> None:
         f.restype = ctypes.c_int
 
 
+def _current_handle(index: int) -> int:
+    """The current stream's handle on a device: alone, where this torch has a function for that, since a Stream object around
+    it costs 1.7 us, a good part of a small call."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 class _Launch:
     """The device and the stream of a call: what is allocated inside belongs to that stream, and the
     launch happens with that device current."""
@@ -57,8 +64,7 @@ class _Launch:
             raise ValueError(f"stream is on {stream.device}, expected {device}")
         self.other = None
         if stream is None:
-            # (the handle alone: a Stream object around it would cost 1.7 us, a good part of a small call)
-            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+            self.handle = _current_handle(device.index)
         else:
             self.handle = stream.cuda_stream
             if stream != torch.cuda.current_stream(device):
