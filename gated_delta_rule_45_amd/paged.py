@@ -178,6 +178,11 @@ def _paged(like, B, T, Hq, k_pages, v_pages, block_table, kv_lens, cu_seqlens, l
     return p, n
 
 
+def _in_place(out, x: torch.Tensor) -> bool:
+    return out is x or (isinstance(out, torch.Tensor) and out.data_ptr() == x.data_ptr() and out.dtype == x.dtype
+                        and out.shape == x.shape and out.stride() == x.stride() and out.get_device() == x.get_device())
+
+
 def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
                  kv_lens: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, *, q: Optional[torch.Tensor] = None,
                  inv_freq: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, interleaved: bool = False,
@@ -216,8 +221,10 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     with _Launch(k.device, stream) as handle:
         if q is not None and q_out is None:
             q_out = q.new_empty(q.shape)
-        elif q is not None and q_out is not q:
+        elif q is not None and not _in_place(q_out, q):
             _want(q_out, "q_out", dt, q.shape, k)
+            if q_out.data_ptr() == q.data_ptr() and not q.is_contiguous():  # (C would take it for q in place)
+                raise ValueError("q_out starts where q does, but its tokens lie elsewhere")
         _check(library().kda_paged_append(ctypes.byref(p), _ptr(k), _ptr(v), _ptr(q), ctypes.byref(turn) if turn else None,
                                           _ptr(block_table), _ptr(kv_lens), _ptr(cu_seqlens), _ptr(host), _ptr(k_pages),
                                           _ptr(v_pages), _ptr(q_out), handle))

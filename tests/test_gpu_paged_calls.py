@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import gated_delta_rule_45_amd as kda
-from test_gpu_paged import BF, DEV, F32, Case, gen, rnd, say
+from test_gpu_paged import BF, DEV, F32, Case, gen, i32, rnd, say
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,17 @@ def test_keys_beside_values_in_a_page(io, layout, dk, dv, wide):
     c.kp, c.vp = kp, vp
     out, _ = c.check(layout)
     assert torch.equal(out, want)
+
+
+def test_queries_in_place_by_a_second_view():
+    """q_out as another view of q's tokens, which lie apart."""
+    g = gen(46)
+    wide = rnd(g, 3, 2, 6 * 64)
+    q, k, v = (x.unflatten(-1, (-1, 64)) for x in wide.split([256, 64, 64], -1))
+    rest = wide[..., 256:].clone()
+    kp, vp = rnd(g, 9, 1, 16, 64), rnd(g, 9, 1, 16, 64)
+    table, lens, freq = i32(3, 1, 8, 2, 5, 4).view(3, 2), i32(21, 5, 2), kda.rope_frequencies(64, device=DEV)[0]
+    want = kda.paged_append(k, v, kp, vp, table, lens, q=q, inv_freq=freq)
+    view = wide[..., :256].unflatten(-1, (4, 64))
+    assert kda.paged_append(k, v, kp, vp, table, lens, q=q, inv_freq=freq, q_out=view) is view
+    assert torch.equal(q, want) and torch.equal(wide[..., 256:], rest)
