@@ -244,6 +244,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     if len(shape) != 4:
         raise ValueError("q must be [B, T, heads, d]")
     B, T, Hq, dk = shape
+    if not 0 <= window < 1 << 31:  # (ctypes would cut it to 32 bits)
+        raise ValueError(f"window {window} is not in 0 .. 2^31 - 1")
     lq = 0 if q.is_contiguous() else _rows(q, "q", dt, shape, q.device)
     p, n = _paged(q, B, T, Hq, k_pages, v_pages, block_table, kv_lens, cu_seqlens, lq, 0, 0)
     if p.head_dim_k != dk:
