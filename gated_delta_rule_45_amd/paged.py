@@ -64,10 +64,11 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "non
                      original_len: int = 0, slow: float = 1.0, fast: float = 32.0, device=None):
     """Frequencies (fp32 [rot_dim / 2]) and the amplitude that goes with them.  scaling: "none"; "linear" (positions
     squeezed by factor); "base" (a larger base, the slowest pair squeezed by factor); "parts" (pairs that turn less than
-    `slow` times in original_len positions squeezed by factor, those above `fast` times kept, a ramp in between)."""
+    `slow` times in original_len positions squeezed by factor, those above `fast` times kept, a ramp in between).  device: None
+    for the CPU."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling is {scaling!r}, expected one of {sorted(_SCALINGS)}")
-    freq, amplitude = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float32), ctypes.c_float(1.0)
+    freq, amplitude = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float32, device="cpu"), ctypes.c_float(1.0)
     _check(library().kda_rope_frequencies(rot_dim, base, _SCALINGS[scaling], factor, original_len, slow, fast, _ptr(freq),
                                           ctypes.addressof(amplitude)))
     return freq.to(device) if device is not None else freq, amplitude.value

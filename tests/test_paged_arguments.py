@@ -12,3 +12,11 @@ def test_windows_that_are_no_c_integer(window):
     table, lens = torch.zeros(2, 5, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="window"):
         kda.paged_attention(q, pages, pages, table, lens, window=window)
+
+
+def test_frequencies_under_another_default_device():
+    """They are written by host code: in host memory, whatever torch.empty would take."""
+    want, _ = kda.rope_frequencies(48)
+    with torch.device("meta"):
+        freq, amplitude = kda.rope_frequencies(48)
+    assert freq.device.type == "cpu" and torch.equal(freq, want) and amplitude == 1.0
