@@ -1,11 +1,12 @@
 """Calls of the paged cache that its users make beside the plain ones: tables that share a row, windows over prompts, offsets
-known on the host, keys beside values in a page.  Against the same calls on copies and the fp64 reference
-(paged_reference.py), with the tolerances of test_gpu_paged.py."""
+known on the host, keys beside values in a page, queries in place, positions of the caller. Against the same calls on copies
+and the fp64 reference (paged_reference.py), with the tolerances of test_gpu_paged.py."""
 import pytest
 import torch
 
 import gated_delta_rule_45_amd as kda
-from test_gpu_paged import BF, DEV, F32, Case, gen, i32, rnd, say
+import paged_reference as ref
+from test_gpu_paged import BF, DEV, F32, Case, batch, check_turned, gen, i32, rnd, say
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +121,31 @@ def test_queries_in_place_by_a_second_view():
     view = wide[..., :256].unflatten(-1, (4, 64))
     assert kda.paged_append(k, v, kp, vp, table, lens, q=q, inv_freq=freq, q_out=view) is view
     assert torch.equal(q, want) and torch.equal(wide[..., 256:], rest)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("new,cells", [([3, 3, 3], [3, 40, 1]), ([17, 0, 1, 60], [17, 5, 130, 64]), ([900, 2100], [900, 3000])])
+def test_append_at_positions_that_are_not_the_cells(io, interleaved, new, cells):
+    """Positions of the caller's (a scrolled cache, a picture's rows): what rope does at them, in the tokens' cells."""
+    g = gen(47 + len(new))
+    packed = len(set(new)) > 1
+    B, T, cu = batch(g, new, packed)
+    k, v, q = (rnd(g, B, T, h, d, dtype=io) for h, d in ((2, 64), (2, 128), (6, 64)))
+    table, pages = ref.table_of(cells, 16, 2, g, DEV)
+    kp, vp = ref.pools(pages, 2, 16, 64, 128, io, g, DEV)
+    lens, freq = i32(*cells), kda.rope_frequencies(48, device=DEV)[0]
+    pos = torch.randint(-(2 ** 20), 2 ** 20, (B, T), generator=g, dtype=torch.int32).to(DEV)
+    say(f"[positions {new} {cells} {io}]")
+    mark, k0, v0 = torch.full_like(q, 7.0), kp.cpu(), vp.cpu()
+    y = kda.paged_append(k, v, kp, vp, table, lens, cu, q=q, inv_freq=freq, positions=pos, interleaved=interleaved, amplitude=1.25,
+                         q_out=mark)
+    tq, tk = kda.rope(q, k, freq, pos, interleaved=interleaved, amplitude=1.25)
+    check_turned("q", tq, q, pos, freq, interleaved, 1.25)
+    wk, wv = ref.append(tk.cpu(), v.cpu(), k0, v0, table.cpu(), lens.cpu(), None if cu is None else cu.cpu())
+    assert torch.equal(kp.cpu(), wk) and torch.equal(vp.cpu(), wv)
+    there = torch.zeros(B * T, dtype=torch.bool)
+    for t0, t, c in ref.sequences(B, T, lens, cu, B * T):
+        there[t0 + max(0, t - c):t0 + t] = True  # (padding has no cell and is left as it is)
+    there = there.view(B, T).to(DEV)
+    assert torch.equal(y[there], tq[there]) and (y[~there] == 7).all()
