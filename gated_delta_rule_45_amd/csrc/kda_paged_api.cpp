@@ -289,7 +289,8 @@ kda_status_t plan_launch(const kda_paged_problem_t *p, const Shape &s, bool pack
     int64_t target = (int64_t)cus * l.t.target_per_cu;
     // No tile is worth splitting: it has few blocks; or they are not many and there are tiles enough; or the blocks of a plain
     // batch's own tokens that its tiles see make parts so long that the kernel would not cut any (without the plan, which costs
-    // each workgroup 2 us, and the join, 4 us a call: 4 x 4,096 x 32 heads 577 -> 565 us, 96 x 4 drafted tokens 79 -> 72).
+    // each workgroup 2 us, and the join, 4 us a call: 4 x 4,096 x 32 heads 577 -> 565 us, 96 x 4 drafted tokens 79 -> 72; for
+    // tables about as wide as the batch, as the host knows no lengths).
     // Each of the three holds for every window where it holds without one, and parts of fewer blocks take no more room: so
     // the query, which has no window, counts enough for all of them.
     const bool counted = !packed || cu_host;
@@ -338,7 +339,8 @@ struct AttnPlan {
 // A packed batch may hold both, and what its offsets do not rule out on the host is launched, but for a batch with no more
 // tokens than sequences: the step of one token each that it looks like needs no second launch, and longer sequences among
 // empty ones come out the same from the first.
-// All rows are few in calls of little work, at most 12 M pairs of (row, key head) and cells that a table has room for: one round of
+// All rows are few in calls of little work, at most 12 M pairs of (row, key head) and cells that a table has room for (the host
+// knows no lengths, so that a table wider than its batch takes this gain away): one round of
 // the kernel for few rows is then over before the other one's workgroups have started (1 x 128 tokens over 628 cells,
 // 32 / 8 heads: 33 -> 22 us; 3 ragged chunks of up to 700 over 300: 47 -> 21; 64 x 9 over 209: 36 -> 26; beyond,
 // 1 x 128 over 4,028: 40 both ways, 8 x 40 over 2,040: 40, 70 as few).

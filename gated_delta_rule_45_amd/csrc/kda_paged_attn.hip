@@ -18,6 +18,8 @@
 // Measured (bf16, 32 query and 8 key heads of 128): 64 ragged contexts of up to 8,192 cells 202 us (5.4 TB/s of the cache), one
 // of 131,072 cells 97 us (5.6 TB/s), 96 sequences of 4 tokens, 16 query heads and a window of 1,024 cells 72 us
 // (5.6 TB/s); fp32, 4 x 1,024 tokens behind 4,096 cells, 16 heads: 1.8 ms (87 TFLOP/s of the 154 of a large product).
+// fp32 of the ragged batch 447 us (4.9 TB/s), of the drafted one 149 (5.5 TB/s); its error is 2.5e-7 to 4.2e-7 of the output's norm,
+// with the score's scale folded into the exponent of the hardware's exponential.
 // Values are loaded past the caches' usual order, as nothing reads them twice: 216 -> 200 us for the ragged batch;
 // keys, whose 128-byte lines are read by halves, gain nothing from it (204).
 #include "kda_paged_work.h"

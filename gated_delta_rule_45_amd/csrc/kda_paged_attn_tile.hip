@@ -14,12 +14,12 @@
 // pieces of keys move by row mod 16 (by half of that where two rows make 256 bytes), 32-byte pieces of values, what 16
 // lanes read of a row, by row mod 4: neither then meets a bank twice in the 256 bytes that LDS gives in a cycle.
 //
-// Weights are rounded to bf16 for their product (error of the output 2.1 to 2.4e-3 of its norm, 1.7e-3 of that its own
+// Weights are rounded to bf16 for their product (error of the output 2.1 to 2.5e-3 of its norm, 1.7e-3 of that its own
 // rounding): a second term, as in the kernel for few rows, would add half as many products again.
 //
 // Measured (32 query and 8 key heads of 128): 4 prompts of 4,096 tokens 565 us, 973 TFLOP/s, and 580 on a second card (a large
 // matrix product: 1,378; matrix units busy 46 % of the time, waves waiting 25 %), 6 chunks of 1,024 tokens behind 16,384 cells 1.60 ms, 1,064 TFLOP/s;
-// d_k = d_v = 64: 780 TFLOP/s (the same softmax for half the products).  A half iteration takes 1,600 to 1,700 cycles of
+// the prompts under a window of 1,024 cells 326 us, 737 TFLOP/s; d_k = d_v = 64: 780 TFLOP/s (the same softmax for half the products).  A half iteration takes 1,600 to 1,700 cycles of
 // the 1,024 that its products need.  What it took, on the prompts: products in one run with their LDS reads ten ahead and the
 // weights kept before them (678 -> 634 us; weights left to sink between the products: 738; six or fourteen reads ahead: 2 and
 // 1 % slower), a bank-free order of the keys (630 -> 615), one base address per load (with one per lane 655, else 600).  Loads

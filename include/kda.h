@@ -616,7 +616,7 @@ kda_status_t kda_paged_append(const kda_paged_problem_t *problem, const void *k,
 
 /*
  * kda_paged_attn -- softmax attention of each sequence's new tokens, one or many, over its cells (the full-attention
- * layers of a hybrid; "3:1 KDA and MLA hybrid" section).  The i-th of `new` tokens sits at t = kv_lens[n] - new + i:
+ * layers, with grouped queries, beside those of kda_gdn_*).  The i-th of `new` tokens sits at t = kv_lens[n] - new + i:
  *
  *     o = sum_j p_j v_j,   p = softmax_j(scale q . k_j)   over the cells max(0, t - window + 1) <= j <= t
  *
@@ -631,10 +631,11 @@ kda_status_t kda_paged_append(const kda_paged_problem_t *problem, const void *k,
  * behind max_pages.  What masked cells and cells behind kv_lens hold does not matter, NaN included; rows of out and
  * lse that no sequence owns are left as they are.
  * Statistics and sums are fp32; bf16 io: weights enter their product with the values as two bf16 terms where a sequence has
- * at most 32 rows (new tokens x Hq / Hkv; 64 in calls of up to 32 sequences x key heads, any number in calls of little
- * work), rounded to one where it has more.
+ * at most 32 rows (new tokens x Hq / Hkv; 64 in calls of up to 32 sequences x key heads), rounded to one where it has more.
+ * Any number of rows has two terms where tokens x Hq x max_pages x page_size is at most 12 * 2^20, whatever kv_lens holds,
+ * and in packed calls without cu_seqlens_host of no more tokens than sequences.
  * The results repeat bit for bit; how rows are split goes by all lengths of the batch, so a sequence's last bits may differ
- * in another batch.  Calls that overlap in time need a workspace each.  Errors as for kda_chunk_bwd.
+ * in another batch or with a wider block_table.  Calls that overlap in time need a workspace each.  Errors as for kda_chunk_bwd.
  */
 kda_status_t kda_paged_attn(const kda_paged_problem_t *problem, const void *q, const void *k_pages, const void *v_pages,
                             const int32_t *block_table, const int32_t *kv_lens, const int32_t *cu_seqlens,
