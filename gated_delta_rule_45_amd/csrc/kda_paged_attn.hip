@@ -424,7 +424,8 @@ hipError_t join(const AttnParams &p, int M, int64_t tiles, hipStream_t s) {
 }  // namespace
 
 // Parts: of at least two blocks of 128 cells in bf16 (a block takes a wave about 1 us, the join 4: with one block a part 512 to
-// 4,096 cells of one sequence take 10.0 to 10.3 us instead of 11.1 to 11.6, 256 cells 9.9 instead of 9.1) and one in fp32, whose
+// 4,096 cells of one sequence take 10.0 to 10.3 us instead of 11.1 to 11.6, 256 cells 9.9 instead of
+// 9.1: for a lone sequence one would be better from 512 on) and one in fp32, whose
 // block takes twice as long (1,002 cells 16.0 -> 13.0 us); for two workgroups per CU: one leaves the ends of ragged batches to few (220
 // us instead of 205), three make more parts than the cache's bandwidth needs (131,072 cells: 94 us instead of 89, the
 // batch 200).  Three workgroups of the bf16 kernel fit a CU.
